@@ -13,6 +13,7 @@ device is not an sm_103 GPU, the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -21,6 +22,11 @@ __all__ = ["fa_forward", "fa_forward_f16", "fa_forward_masked", "forward_masked"
            "fa_decode_gqa_select",
            "fa_status_string", "fa_quantize_fp8", "fa_quantize_fp8_workspace_bytes",
            "fa_fp8_vt_stride", "fa_forward_fp8", "quantize_fp8", "forward_fp8", "Fp8Inputs",
+           "fa_qk_norm_rope", "fa_qk_norm_rope_f16", "fa_qk_norm_rope_fp32",
+           "fa_qk_norm_rope_cache", "fa_qk_norm_rope_backward_workspace_bytes",
+           "fa_qk_norm_rope_backward", "fa_qk_norm_rope_backward_f16",
+           "fa_qk_norm_rope_backward_fp32", "rope_frequencies", "qk_norm_rope",
+           "qk_norm_rope_cache", "qk_norm_rope_backward",
            "fa_device_status", "fa_release", "forward", "paged_decode", "FattnError",
            "library_path", "load"]
 
@@ -47,6 +53,9 @@ def library_path() -> str:
 
 
 _vp, _i, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+_ll = ctypes.c_longlong
+_PREP = [_vp] * 8 + [_i] * 6 + [_ll, _ll, _f, _f, _vp]
+_PREP_BWD = [_vp] * 12 + [_i] * 6 + [_ll, _ll, _f, _f, _vp, ctypes.c_ulonglong, _vp]
 EXPORTS = {
     "fa_forward": ([_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp], _i),
     "fa_forward_fp32": ([_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _f, _i, _vp], _i),
@@ -63,6 +72,14 @@ EXPORTS = {
     "fa_fp8_vt_stride": ([_i], ctypes.c_longlong),
     "fa_quantize_fp8": ([_vp] * 10 + [_i, _i, _i, _i, _vp, ctypes.c_ulonglong, _vp], _i),
     "fa_forward_fp8": ([_vp] * 8 + [_i, _i, _i, _i, _f, _i, _vp], _i),
+    "fa_qk_norm_rope": (_PREP, _i),
+    "fa_qk_norm_rope_f16": (_PREP, _i),
+    "fa_qk_norm_rope_fp32": (_PREP, _i),
+    "fa_qk_norm_rope_cache": ([_vp] * 11 + [_i] * 8 + [_ll] * 3 + [_f, _f, _vp], _i),
+    "fa_qk_norm_rope_backward_workspace_bytes": ([_i, _i], ctypes.c_ulonglong),
+    "fa_qk_norm_rope_backward": (_PREP_BWD, _i),
+    "fa_qk_norm_rope_backward_f16": (_PREP_BWD, _i),
+    "fa_qk_norm_rope_backward_fp32": (_PREP_BWD, _i),
     "fa_status_string": ([_i], ctypes.c_char_p),
     "fa_device_status": ([], _i),
     "fa_release": ([], None),
@@ -178,6 +195,51 @@ def fa_forward_fp8(q8, k8, vt8, q_scale, k_scale, v_scale, o, lse, B, H, N, d, s
                    stream) -> int:
     return _check("fa_forward_fp8", load().fa_forward_fp8(
         q8, k8, vt8, q_scale, k_scale, v_scale, o, lse, B, H, N, d, scale, int(causal), stream))
+
+
+def _prep_call(name):
+    def call(q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, num_tokens, num_heads,
+             num_kv_heads, d, rot_dim, interleaved, q_stride, k_stride, eps, mscale,
+             stream) -> int:
+        return _check(name, getattr(load(), name)(
+            q, k, q_weight, k_weight, positions, inv_freq, q_out, k_out, num_tokens, num_heads,
+            num_kv_heads, d, rot_dim, int(interleaved), q_stride, k_stride, eps, mscale, stream))
+    call.__name__ = call.__qualname__ = name
+    return call
+
+
+def _prep_backward_call(name):
+    def call(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, dq, dk, dq_weight,
+             dk_weight, num_tokens, num_heads, num_kv_heads, d, rot_dim, interleaved, q_stride,
+             k_stride, eps, mscale, workspace, workspace_bytes, stream) -> int:
+        return _check(name, getattr(load(), name)(
+            dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, dq, dk, dq_weight,
+            dk_weight, num_tokens, num_heads, num_kv_heads, d, rot_dim, int(interleaved),
+            q_stride, k_stride, eps, mscale, workspace, workspace_bytes, stream))
+    call.__name__ = call.__qualname__ = name
+    return call
+
+
+fa_qk_norm_rope = _prep_call("fa_qk_norm_rope")
+fa_qk_norm_rope_f16 = _prep_call("fa_qk_norm_rope_f16")
+fa_qk_norm_rope_fp32 = _prep_call("fa_qk_norm_rope_fp32")
+fa_qk_norm_rope_backward = _prep_backward_call("fa_qk_norm_rope_backward")
+fa_qk_norm_rope_backward_f16 = _prep_backward_call("fa_qk_norm_rope_backward_f16")
+fa_qk_norm_rope_backward_fp32 = _prep_backward_call("fa_qk_norm_rope_backward_fp32")
+
+
+def fa_qk_norm_rope_cache(q, k, v, q_weight, k_weight, positions, inv_freq, slots, q_out, k_cache,
+                          v_cache, num_tokens, num_heads, num_kv_heads, head_size, block_size,
+                          num_blocks, rot_dim, interleaved, q_stride, k_stride, v_stride, eps,
+                          mscale, stream) -> int:
+    return _check("fa_qk_norm_rope_cache", load().fa_qk_norm_rope_cache(
+        q, k, v, q_weight, k_weight, positions, inv_freq, slots, q_out, k_cache, v_cache,
+        num_tokens, num_heads, num_kv_heads, head_size, block_size, num_blocks, rot_dim,
+        int(interleaved), q_stride, k_stride, v_stride, eps, mscale, stream))
+
+
+def fa_qk_norm_rope_backward_workspace_bytes(num_tokens, d) -> int:
+    return int(load().fa_qk_norm_rope_backward_workspace_bytes(num_tokens, d))
 
 
 def fa_status_string(status: int) -> str:
@@ -400,3 +462,189 @@ def forward_fp8(x, scale=None, causal=False, out=None, lse=None, want_lse=True):
                    _ptr(x.v_scale), _ptr(out), _ptr(lse), B, H, N, d, float(scale),
                    bool(causal), _stream(x.q8))
     return out, lse
+
+
+# -------------------------------------------- packed tokens: [tokens, heads, d] tensors
+def _on_device(fn):
+    """Runs ``fn`` with its first tensor's device current: the C calls work on
+    the current device, and a caller's may be another one."""
+    @functools.wraps(fn)
+    def run(first, *args, **kwargs):
+        import torch
+        if first.is_cuda and first.get_device() != torch.cuda.current_device():
+            with torch.cuda.device(first.device):
+                return fn(first, *args, **kwargs)
+        return fn(first, *args, **kwargs)
+    return run
+
+
+def _rows(name, t, like, heads=None):
+    """Checks a [tokens, heads, d] tensor with dense heads and returns its
+    token stride in elements; ``like`` sets the device, type and token count."""
+    if t.dim() != 3 or t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2] \
+            or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} has an inconsistent shape")
+    if t.dtype != like.dtype or t.device != like.device or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor of the same type and device as the rest")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    return s0 if n > 1 else max(h * d, 1)
+
+
+def _vector(name, t, dtype, like, numel=None):
+    """Checks a dense vector on ``like``'s device."""
+    if t.dtype != dtype or t.device != like.device or not t.is_contiguous() \
+            or (numel is not None and t.numel() != numel):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor"
+                         + (f" of {numel} values" if numel is not None else "")
+                         + " on the same device as the rest")
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_context=4096,
+                     beta_slow=1.0, beta_fast=32.0, device=None):
+    """Rotary frequencies (fp64 [rot_dim/2], radians per position) and the
+    factor ``mscale`` that goes with them, for ``qk_norm_rope``.
+
+    ``scaling`` stretches them ``factor`` times beyond ``original_context``:
+    None, "linear" (position interpolation: every frequency / factor), "ntk"
+    (the base grows so that the lowest frequency is divided by factor and the
+    highest stays) or "yarn" (by wavelength: frequencies that turn more than
+    ``beta_fast`` times over the original context stay, those that turn less
+    than ``beta_slow`` times are divided by factor, linear in between; mscale
+    = 0.1 ln(factor) + 1).  mscale is 1 for the others."""
+    import math
+
+    import torch
+    if rot_dim < 0 or rot_dim % 2 != 0:
+        raise ValueError("rot_dim must be even")
+    if scaling not in (None, "linear", "ntk", "yarn") or not factor >= 1.0 or not base > 1.0:
+        raise ValueError("scaling is None, 'linear', 'ntk' or 'yarn', factor >= 1 and base > 1")
+    mscale = 1.0
+    if scaling == "ntk" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    i = torch.arange(rot_dim // 2, dtype=torch.float64)
+    freq = base ** (-2.0 * i / max(rot_dim, 1))
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "yarn":
+        turns = original_context * freq / (2 * math.pi)
+        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        freq = freq * keep + freq / factor * (1.0 - keep)
+        mscale = 0.1 * math.log(factor) + 1.0
+    return freq.to(device), mscale
+
+
+def _prep_args(q, k, positions, inv_freq, q_weight, k_weight):
+    import torch
+    if q.dtype not in (torch.bfloat16, torch.float16, torch.float32):
+        raise ValueError("q and k must be bf16, fp16 or fp32")
+    qs, ks = _rows("q", q, q), _rows("k", k, q)
+    T, _, d = q.shape
+    _vector("positions", positions, torch.int32, q, T)
+    _vector("inv_freq", inv_freq, torch.float64, q)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _vector(name, w, q.dtype, q, d)
+    return qs, ks
+
+
+_PREP_SUFFIX = {"torch.bfloat16": "", "torch.float16": "_f16", "torch.float32": "_fp32"}
+
+
+@_on_device
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False, mscale=1.0, q_out=None, k_out=None):
+    """RMS norm of each head (where its weight is given) and rotary position
+    embedding of q [T,H,d] and k [T,Hk,d] (bf16, fp16 or fp32 CUDA tensors;
+    heads dense, any token stride that is a multiple of 16 bytes).
+
+    positions int32 [T]; inv_freq fp64 [rot_dim/2] (``rope_frequencies``): the
+    first rot_dim values of a head are rotated.  Returns (q_out, k_out), dense.
+    Runs on the current torch stream."""
+    import torch
+    qs, ks = _prep_args(q, k, positions, inv_freq, q_weight, k_weight)
+    T, H, d = q.shape
+    if q_out is None:
+        q_out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    _vector("q_out", q_out, q.dtype, q, q.numel())
+    _vector("k_out", k_out, q.dtype, q, k.numel())
+    if T == 0:      # empty tensors have no address to pass
+        return q_out, k_out
+    name = "fa_qk_norm_rope" + _PREP_SUFFIX[str(q.dtype)]
+    _check(name, getattr(load(), name)(
+        _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq),
+        _ptr(q_out), _ptr(k_out), T, H, k.shape[1], d, 2 * inv_freq.numel(), int(interleaved),
+        qs, ks, eps, mscale, _stream(q)))
+    return q_out, k_out
+
+
+@_on_device
+def qk_norm_rope_cache(q, k, v, positions, inv_freq, slots, k_cache, v_cache, q_weight=None,
+                       k_weight=None, eps=1e-6, interleaved=False, mscale=1.0, q_out=None):
+    """``qk_norm_rope`` for serving (bf16, d = 128): the prepared keys, and v
+    [T,Hk,d] as it is, are written into the paged caches of ``paged_decode``
+    and ``paged_prefill`` at slots (int64 [T]: block * block_size + offset; a
+    negative slot stores nothing).  Returns the prepared queries, dense."""
+    import torch
+    qs, ks = _prep_args(q, k, positions, inv_freq, q_weight, k_weight)
+    T, H, d = q.shape
+    Hk = k.shape[1]
+    vs = _rows("v", v, q, Hk)
+    _vector("slots", slots, torch.int64, q, T)
+    if q.dtype != torch.bfloat16:
+        raise ValueError("the cache form is bf16")
+    if k_cache.dim() != 5 or v_cache.dim() != 4:
+        raise ValueError("inconsistent cache shapes")
+    nb, hc, dx, bs, x = k_cache.shape
+    if hc != Hk or dx * x != d or x != 8 or tuple(v_cache.shape) != (nb, Hk, d, bs):
+        raise ValueError("inconsistent cache shapes")
+    _vector("k_cache", k_cache, q.dtype, q)
+    _vector("v_cache", v_cache, q.dtype, q)
+    if q_out is None:
+        q_out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    _vector("q_out", q_out, q.dtype, q, q.numel())
+    if T == 0:
+        return q_out
+    _check("fa_qk_norm_rope_cache", load().fa_qk_norm_rope_cache(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
+        _ptr(inv_freq), _ptr(slots), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), T, H, Hk, d, bs,
+        nb, 2 * inv_freq.numel(), int(interleaved), qs, ks, vs, eps, mscale, _stream(q)))
+    return q_out
+
+
+@_on_device
+def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight=None,
+                          k_weight=None, eps=1e-6, interleaved=False, mscale=1.0,
+                          workspace=None):
+    """Gradients of ``qk_norm_rope``: (dq, dk, dq_weight, dk_weight) from the
+    dense gradients dq_out [T,H,d], dk_out [T,Hk,d] of its outputs and its
+    inputs.  The weights' gradients are fp32 [d], None where there is no
+    weight.  ``workspace`` (optional) is a CUDA tensor of at least
+    ``fa_qk_norm_rope_backward_workspace_bytes`` bytes."""
+    import torch
+    qs, ks = _prep_args(q, k, positions, inv_freq, q_weight, k_weight)
+    T, H, d = q.shape
+    if dq_out.shape != q.shape or dk_out.shape != k.shape:
+        raise ValueError("dq_out and dk_out must have the shapes of q and k")
+    _vector("dq_out", dq_out, q.dtype, q)
+    _vector("dk_out", dk_out, q.dtype, q)
+    dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
+    dqw, dkw = (None if w is None else torch.empty(d, dtype=torch.float32, device=q.device)
+                for w in (q_weight, k_weight))
+    if T == 0:
+        return dq, dk, *(w if w is None else w.zero_() for w in (dqw, dkw))
+    if workspace is None and not (dqw is None and dkw is None):
+        nbytes = load().fa_qk_norm_rope_backward_workspace_bytes(T, d)
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+    name = "fa_qk_norm_rope_backward" + _PREP_SUFFIX[str(q.dtype)]
+    _check(name, getattr(load(), name)(
+        _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
+        _ptr(positions), _ptr(inv_freq), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), T, H,
+        k.shape[1], d, 2 * inv_freq.numel(), int(interleaved), qs, ks, eps, mscale,
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _stream(q)))
+    return dq, dk, dqw, dkw

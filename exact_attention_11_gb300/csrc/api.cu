@@ -587,6 +587,168 @@ int fa_paged_decode_gqa(const void *q, const void *k_cache, const void *v_cache,
                                                     ws, counters, status, s));
 }
 
+namespace {
+using fattn::ElemType;
+
+size_t elem_bytes(ElemType t) { return t == ElemType::kF32 ? 4 : 2; }
+
+bool aligned_to(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// A token stride (elements) of a [tokens, heads, d] tensor with dense heads:
+// it covers the heads and keeps every row 16-byte aligned.
+int check_token_stride(long long stride, int heads, int d, size_t es) {
+  if (stride < (long long)heads * d) return FA_ERR_INVALID_ARG;
+  return (unsigned long long)stride * es % 16 == 0 ? FA_OK : FA_ERR_ALIGNMENT;
+}
+
+// Checks shared by the norm-and-rotation calls.
+int check_qk_prep(const fattn::QkPrep &p, ElemType type) {
+  if (!p.q || !p.k || !p.positions) return FA_ERR_INVALID_ARG;
+  if (p.T < 0 || p.H <= 0 || p.Hk <= 0) return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(p.eps) && p.eps >= 0.f) || !std::isfinite(p.mscale)) return FA_ERR_INVALID_ARG;
+  if (p.d != 64 && p.d != 128 && p.d != 256) return FA_ERR_UNSUPPORTED;
+  if (p.rot < 0 || p.rot > p.d) return FA_ERR_INVALID_ARG;
+  if (p.rot % 16 != 0) return FA_ERR_UNSUPPORTED;
+  if (p.rot > 0 && !p.inv_freq) return FA_ERR_INVALID_ARG;
+  if (p.H > 65535 || p.Hk > 65535) return FA_ERR_UNSUPPORTED;
+  if (!aligned16(p.q) || !aligned16(p.k) || !aligned16(p.q_weight) || !aligned16(p.k_weight) ||
+      !aligned_to(p.positions, 4) || !aligned_to(p.inv_freq, 8))
+    return FA_ERR_ALIGNMENT;
+  int rc;
+  if ((rc = check_token_stride(p.q_stride, p.H, p.d, elem_bytes(type))) != FA_OK) return rc;
+  if ((rc = check_token_stride(p.k_stride, p.Hk, p.d, elem_bytes(type))) != FA_OK) return rc;
+  return FA_OK;
+}
+
+// Makes sure that the current device is one the kernels run on.
+int require_device() {
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev = 0;
+  return current_device(&dev);
+}
+
+int qk_norm_rope(ElemType type, const fattn::QkPrep &p, void *q_out, void *k_out,
+                 fa_stream_t stream) {
+  int rc = check_qk_prep(p, type);
+  if (rc != FA_OK) return rc;
+  if (!q_out || !k_out) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q_out) || !aligned16(k_out)) return FA_ERR_ALIGNMENT;
+  if (p.T == 0) return FA_OK;
+  if ((rc = require_device()) != FA_OK) return rc;
+  return cuda_status(
+      fattn::launch_qk_prep(type, p, q_out, k_out, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int qk_norm_rope_backward(ElemType type, const fattn::QkPrep &p, const void *dq_out,
+                          const void *dk_out, void *dq, void *dk, float *dqw, float *dkw,
+                          void *workspace, unsigned long long workspace_bytes,
+                          fa_stream_t stream) {
+  int rc = check_qk_prep(p, type);
+  if (rc != FA_OK) return rc;
+  if (!dq_out || !dk_out || !dq || !dk) return FA_ERR_INVALID_ARG;
+  if ((dqw != nullptr) != (p.q_weight != nullptr) || (dkw != nullptr) != (p.k_weight != nullptr))
+    return FA_ERR_INVALID_ARG;
+  if (!aligned16(dq_out) || !aligned16(dk_out) || !aligned16(dq) || !aligned16(dk) ||
+      !aligned_to(dqw, 4) || !aligned_to(dkw, 4))
+    return FA_ERR_ALIGNMENT;
+  const bool weights = dqw != nullptr || dkw != nullptr;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (p.T == 0 && !weights) return FA_OK;
+  if (p.T > 0 && weights) {
+    if (!workspace) return FA_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
+    if (workspace_bytes < fattn::qk_prep_grad_workspace_bytes(p.T, p.d)) return FA_ERR_INVALID_ARG;
+  }
+  if ((rc = require_device()) != FA_OK) return rc;
+  if (p.T == 0) {
+    if (dqw && cudaMemsetAsync(dqw, 0, sizeof(float) * p.d, s) != cudaSuccess) return FA_ERR_CUDA;
+    if (dkw && cudaMemsetAsync(dkw, 0, sizeof(float) * p.d, s) != cudaSuccess) return FA_ERR_CUDA;
+    return FA_OK;
+  }
+  return cuda_status(fattn::launch_qk_prep_grad(type, p, dq_out, dk_out, dq, dk, dqw, dkw,
+                                                static_cast<float *>(workspace), s));
+}
+}  // namespace
+
+#define FATTN_QK_PREP                                                                            \
+  fattn::QkPrep {                                                                                \
+    q, k, q_weight, k_weight, positions, inv_freq, num_tokens, num_heads, num_kv_heads, d,       \
+        rot_dim, interleaved ? 1 : 0, static_cast<int64_t>(q_stride),                            \
+        static_cast<int64_t>(k_stride), eps, mscale                                              \
+  }
+
+int fa_qk_norm_rope(const void *q, const void *k, const void *q_weight, const void *k_weight,
+                    const int *positions, const double *inv_freq, void *q_out, void *k_out,
+                    int num_tokens, int num_heads, int num_kv_heads, int d, int rot_dim,
+                    int interleaved, long long q_stride, long long k_stride, float eps,
+                    float mscale, fa_stream_t stream) {
+  return qk_norm_rope(ElemType::kBf16, FATTN_QK_PREP, q_out, k_out, stream);
+}
+
+int fa_qk_norm_rope_f16(const void *q, const void *k, const void *q_weight, const void *k_weight,
+                        const int *positions, const double *inv_freq, void *q_out, void *k_out,
+                        int num_tokens, int num_heads, int num_kv_heads, int d, int rot_dim,
+                        int interleaved, long long q_stride, long long k_stride, float eps,
+                        float mscale, fa_stream_t stream) {
+  return qk_norm_rope(ElemType::kF16, FATTN_QK_PREP, q_out, k_out, stream);
+}
+
+int fa_qk_norm_rope_fp32(const void *q, const void *k, const void *q_weight, const void *k_weight,
+                         const int *positions, const double *inv_freq, void *q_out, void *k_out,
+                         int num_tokens, int num_heads, int num_kv_heads, int d, int rot_dim,
+                         int interleaved, long long q_stride, long long k_stride, float eps,
+                         float mscale, fa_stream_t stream) {
+  return qk_norm_rope(ElemType::kF32, FATTN_QK_PREP, q_out, k_out, stream);
+}
+
+int fa_qk_norm_rope_cache(const void *q, const void *k, const void *v, const void *q_weight,
+                          const void *k_weight, const int *positions, const double *inv_freq,
+                          const long long *slots, void *q_out, void *k_cache, void *v_cache,
+                          int num_tokens, int num_heads, int num_kv_heads, int head_size,
+                          int block_size, int num_blocks, int rot_dim, int interleaved,
+                          long long q_stride, long long k_stride, long long v_stride, float eps,
+                          float mscale, fa_stream_t stream) {
+  const int d = head_size;
+  const fattn::QkPrep p = FATTN_QK_PREP;
+  int rc = check_qk_prep(p, ElemType::kBf16);
+  if (rc != FA_OK) return rc;
+  if (!v || !slots || !q_out || !k_cache || !v_cache || num_blocks < 0) return FA_ERR_INVALID_ARG;
+  if (head_size != fattn::kDecodeHeadSize || block_size != fattn::kDecodeBlockSize)
+    return FA_ERR_UNSUPPORTED;
+  if (!aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+      !aligned_to(slots, 8))
+    return FA_ERR_ALIGNMENT;
+  if ((rc = check_token_stride(v_stride, num_kv_heads, d, 2)) != FA_OK) return rc;
+  // One block per 16 tokens and cached head, beside those of the queries and keys.
+  if (((long long)num_tokens + 15) / 16 * num_kv_heads > 0x3fffffffLL) return FA_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return FA_OK;
+  if ((rc = require_device()) != FA_OK) return rc;
+  return cuda_status(fattn::launch_qk_prep_cache(
+      p, v, static_cast<int64_t>(v_stride), slots, (int64_t)num_blocks * block_size, q_out,
+      k_cache, v_cache, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+unsigned long long fa_qk_norm_rope_backward_workspace_bytes(int num_tokens, int d) {
+  if (num_tokens < 0 || d < 0) return 0;
+  return static_cast<unsigned long long>(fattn::qk_prep_grad_workspace_bytes(num_tokens, d));
+}
+
+#define FATTN_QK_PREP_BACKWARD(NAME, TYPE)                                                       \
+  int NAME(const void *dq_out, const void *dk_out, const void *q, const void *k,                 \
+           const void *q_weight, const void *k_weight, const int *positions,                     \
+           const double *inv_freq, void *dq, void *dk, float *dq_weight, float *dk_weight,       \
+           int num_tokens, int num_heads, int num_kv_heads, int d, int rot_dim, int interleaved, \
+           long long q_stride, long long k_stride, float eps, float mscale, void *workspace,     \
+           unsigned long long workspace_bytes, fa_stream_t stream) {                             \
+    return qk_norm_rope_backward(TYPE, FATTN_QK_PREP, dq_out, dk_out, dq, dk, dq_weight,         \
+                                 dk_weight, workspace, workspace_bytes, stream);                 \
+  }
+FATTN_QK_PREP_BACKWARD(fa_qk_norm_rope_backward, ElemType::kBf16)
+FATTN_QK_PREP_BACKWARD(fa_qk_norm_rope_backward_f16, ElemType::kF16)
+FATTN_QK_PREP_BACKWARD(fa_qk_norm_rope_backward_fp32, ElemType::kF32)
+#undef FATTN_QK_PREP_BACKWARD
+#undef FATTN_QK_PREP
+
 int fa_device_status(void) {
   std::lock_guard<std::mutex> lock(g_mu);
   int dev = 0, rc;

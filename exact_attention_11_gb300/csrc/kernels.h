@@ -138,4 +138,28 @@ cudaError_t launch_paged_decode(const void *q, const void *k_cache, const void *
                                 int num_seqs, int num_heads, int max_blocks, float scale,
                                 float *workspace, int *counters, cudaStream_t stream);
 
+// Norm and rotation of queries and keys (qk_prep.cu).  d is 64, 128 or 256,
+// rot a multiple of 16 up to d; strides in elements between tokens, heads
+// dense; weights may be null (no norm on that side).
+enum class ElemType { kBf16, kF16, kF32 };
+struct QkPrep {
+  const void *q, *k, *q_weight, *k_weight;
+  const int *positions;
+  const double *inv_freq;
+  int T, H, Hk, d, rot, interleaved;
+  int64_t q_stride, k_stride;
+  float eps, mscale;
+};
+cudaError_t launch_qk_prep(ElemType type, const QkPrep &p, void *q_out, void *k_out,
+                           cudaStream_t stream);
+// bf16, d = kDecodeHeadSize: keys and values of token t go to slot slots[t]
+// of the paged caches; slots outside [0, n_slots) are skipped.
+cudaError_t launch_qk_prep_cache(const QkPrep &p, const void *v, int64_t v_stride,
+                                 const long long *slots, int64_t n_slots, void *q_out,
+                                 void *k_cache, void *v_cache, cudaStream_t stream);
+size_t qk_prep_grad_workspace_bytes(int T, int d);
+cudaError_t launch_qk_prep_grad(ElemType type, const QkPrep &p, const void *dq_out,
+                                const void *dk_out, void *dq, void *dk, float *dqw, float *dkw,
+                                float *workspace, cudaStream_t stream);
+
 }  // namespace fattn

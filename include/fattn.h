@@ -360,6 +360,131 @@ int fa_paged_decode_noalloc(const void *q, const void *k_cache, const void *v_ca
                             int max_num_blocks_per_seq, float scale, fa_stream_t stream);
 
 /*
+ * Queries and keys before attention: the RMS norm of each head and the rotary
+ * position embedding in one pass over them, and the backward pass.
+ *
+ * For a row x of d values (token t, one head), with its side's weight w:
+ *     y = x * w / sqrt(mean(x^2) + eps)          (y = x when the weight is null)
+ * and for every pair i < rot_dim / 2 of y at angle a = positions[t] * inv_freq[i]
+ *     (y1, y2) -> mscale * (y1 cos a - y2 sin a, y2 cos a + y1 sin a);
+ * the pair is (y[i], y[i + rot_dim/2]), or (y[2i], y[2i+1]) when interleaved.
+ * Values from rot_dim on are not rotated and not scaled by mscale.
+ *
+ *   q              [num_tokens, num_heads, d], k [num_tokens, num_kv_heads, d],
+ *                  heads dense, consecutive tokens q_stride / k_stride elements
+ *                  apart (a slice of a fused projection has its own stride);
+ *                  bf16, or fp16 / fp32 in the _f16 / _fp32 calls.
+ *   q_weight, k_weight  [d] in q's type, shared by the side's heads; null: no
+ *                  norm on that side.
+ *   positions      int32 [num_tokens], any value (a turn is taken modulo its
+ *                  period exactly, so far positions lose no accuracy).
+ *   inv_freq       fp64 [rot_dim / 2] radians per position; null only when
+ *                  rot_dim is 0.
+ *   d              64, 128 or 256;  rot_dim a multiple of 16 in [0, d] (else
+ *                  FA_ERR_UNSUPPORTED).
+ *   eps            finite and >= 0;  mscale finite (1 unless the frequencies
+ *                  were scaled for a longer context by a method that asks for
+ *                  it).
+ * All arithmetic is fp32; each output is rounded once.  Pointers are 16-byte
+ * aligned (positions and slots: naturally aligned) and strides cover the heads
+ * and are a multiple of 16 bytes (else FA_ERR_ALIGNMENT).  num_tokens == 0 does
+ * nothing.  NaN or Inf in a row stays in that row (backward: and reaches the
+ * weight's gradient).
+ *
+ * fa_qk_norm_rope -- q_out [num_tokens, num_heads, d] and k_out [num_tokens,
+ * num_kv_heads, d], dense.  They may be q and k themselves where those are
+ * dense; any other overlap is not allowed.
+ */
+int fa_qk_norm_rope(const void *q, const void *k, const void *q_weight, const void *k_weight,
+                    const int *positions, const double *inv_freq, void *q_out, void *k_out,
+                    int num_tokens, int num_heads, int num_kv_heads, int d, int rot_dim,
+                    int interleaved, long long q_stride, long long k_stride, float eps,
+                    float mscale, fa_stream_t stream);
+int fa_qk_norm_rope_f16(const void *q, const void *k, const void *q_weight, const void *k_weight,
+                        const int *positions, const double *inv_freq, void *q_out, void *k_out,
+                        int num_tokens, int num_heads, int num_kv_heads, int d, int rot_dim,
+                        int interleaved, long long q_stride, long long k_stride, float eps,
+                        float mscale, fa_stream_t stream);
+int fa_qk_norm_rope_fp32(const void *q, const void *k, const void *q_weight, const void *k_weight,
+                         const int *positions, const double *inv_freq, void *q_out, void *k_out,
+                         int num_tokens, int num_heads, int num_kv_heads, int d, int rot_dim,
+                         int interleaved, long long q_stride, long long k_stride, float eps,
+                         float mscale, fa_stream_t stream);
+
+/*
+ * fa_qk_norm_rope_cache -- the bf16 form for serving: the prepared keys, and
+ * the values as they are, go into the paged caches that fa_paged_decode,
+ * fa_paged_decode_gqa and fa_paged_prefill read (their layouts), the prepared
+ * queries to q_out.
+ *
+ *   v              bf16 [num_tokens, num_kv_heads, head_size], tokens v_stride
+ *                  elements apart.
+ *   slots          int64 [num_tokens]: token t is stored in cache block
+ *                  slots[t] / block_size at offset slots[t] % block_size.  A
+ *                  slot outside [0, num_blocks * block_size) -- -1 for a
+ *                  padding token -- stores nothing (its q_out row is written
+ *                  all the same).  Slots in range must differ: where two tokens
+ *                  name one slot, which of them each stored value comes from is
+ *                  not specified.
+ *   k_cache        bf16 [num_blocks, num_kv_heads, head_size/8, block_size, 8].
+ *   v_cache        bf16 [num_blocks, num_kv_heads, head_size, block_size].
+ *   head_size      128;  block_size 16 (else FA_ERR_UNSUPPORTED).
+ * Cache slots that no token names are left as they were.
+ */
+int fa_qk_norm_rope_cache(const void *q, const void *k, const void *v, const void *q_weight,
+                          const void *k_weight, const int *positions, const double *inv_freq,
+                          const long long *slots, void *q_out, void *k_cache, void *v_cache,
+                          int num_tokens, int num_heads, int num_kv_heads, int head_size,
+                          int block_size, int num_blocks, int rot_dim, int interleaved,
+                          long long q_stride, long long k_stride, long long v_stride, float eps,
+                          float mscale, fa_stream_t stream);
+
+/*
+ * fa_qk_norm_rope_backward -- gradients of fa_qk_norm_rope (and _f16, _fp32).
+ * With dq_out, dk_out the dense gradients of its outputs, and g a row of them
+ * rotated back by the same angles (times mscale where rotated):
+ *     dw = sum over the side's rows of g * x / sqrt(mean(x^2) + eps)
+ *     dx = (w g - x mean(w g x) / (mean(x^2) + eps)) / sqrt(mean(x^2) + eps)
+ * (dx = g without a weight).  q, k and the other inputs are the forward's.
+ *   dq, dk                  dense, in q's type, written (they may be dq_out and
+ *                           dk_out themselves).
+ *   dq_weight, dk_weight    fp32 [d], written; null exactly where the side's
+ *                           weight is null.
+ *   workspace               device memory of at least
+ *                           fa_qk_norm_rope_backward_workspace_bytes(num_tokens,
+ *                           d) bytes, 16-byte aligned, scratch during the call;
+ *                           may be null without weights.  Calls that may run at
+ *                           the same time need separate workspaces.
+ * The weights' gradients are summed in fp32 in an order fixed by the sizes and
+ * the GPU: repeated calls agree bit for bit.  num_tokens == 0 writes zeros to
+ * them.
+ */
+unsigned long long fa_qk_norm_rope_backward_workspace_bytes(int num_tokens, int d);
+int fa_qk_norm_rope_backward(const void *dq_out, const void *dk_out, const void *q, const void *k,
+                             const void *q_weight, const void *k_weight, const int *positions,
+                             const double *inv_freq, void *dq, void *dk, float *dq_weight,
+                             float *dk_weight, int num_tokens, int num_heads, int num_kv_heads,
+                             int d, int rot_dim, int interleaved, long long q_stride,
+                             long long k_stride, float eps, float mscale, void *workspace,
+                             unsigned long long workspace_bytes, fa_stream_t stream);
+int fa_qk_norm_rope_backward_f16(const void *dq_out, const void *dk_out, const void *q,
+                                 const void *k, const void *q_weight, const void *k_weight,
+                                 const int *positions, const double *inv_freq, void *dq, void *dk,
+                                 float *dq_weight, float *dk_weight, int num_tokens,
+                                 int num_heads, int num_kv_heads, int d, int rot_dim,
+                                 int interleaved, long long q_stride, long long k_stride,
+                                 float eps, float mscale, void *workspace,
+                                 unsigned long long workspace_bytes, fa_stream_t stream);
+int fa_qk_norm_rope_backward_fp32(const void *dq_out, const void *dk_out, const void *q,
+                                  const void *k, const void *q_weight, const void *k_weight,
+                                  const int *positions, const double *inv_freq, void *dq,
+                                  void *dk, float *dq_weight, float *dk_weight, int num_tokens,
+                                  int num_heads, int num_kv_heads, int d, int rot_dim,
+                                  int interleaved, long long q_stride, long long k_stride,
+                                  float eps, float mscale, void *workspace,
+                                  unsigned long long workspace_bytes, fa_stream_t stream);
+
+/*
  * fa_debug_inject_fault -- test hook for the device-side failure path.
  *
  * mode 1 arms the current device: the next tensor-core forward launched on
