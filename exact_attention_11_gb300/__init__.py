@@ -26,7 +26,9 @@ __all__ = ["fa_forward", "fa_forward_f16", "fa_forward_masked", "forward_masked"
            "fa_qk_norm_rope_cache", "fa_qk_norm_rope_backward_workspace_bytes",
            "fa_qk_norm_rope_backward", "fa_qk_norm_rope_backward_f16",
            "fa_qk_norm_rope_backward_fp32", "rope_frequencies", "qk_norm_rope",
-           "qk_norm_rope_cache", "qk_norm_rope_backward",
+           "qk_norm_rope_cache", "qk_norm_rope_backward", "fa_forward_packed",
+           "fa_forward_packed_f16", "forward_packed", "fa_paged_prefill",
+           "fa_paged_prefill_workspace_bytes", "paged_prefill",
            "fa_device_status", "fa_release", "forward", "paged_decode", "FattnError",
            "library_path", "load"]
 
@@ -80,6 +82,10 @@ EXPORTS = {
     "fa_qk_norm_rope_backward": (_PREP_BWD, _i),
     "fa_qk_norm_rope_backward_f16": (_PREP_BWD, _i),
     "fa_qk_norm_rope_backward_fp32": (_PREP_BWD, _i),
+    "fa_forward_packed": ([_vp] * 6 + [_i] * 5 + [_ll] * 3 + [_f, _i, _vp], _i),
+    "fa_forward_packed_f16": ([_vp] * 6 + [_i] * 5 + [_ll] * 3 + [_f, _i, _vp], _i),
+    "fa_paged_prefill_workspace_bytes": ([_i] * 5, ctypes.c_ulonglong),
+    "fa_paged_prefill": ([_vp] * 7 + [_i] * 8 + [_ll, _f, _vp, ctypes.c_ulonglong, _vp], _i),
     "fa_status_string": ([_i], ctypes.c_char_p),
     "fa_device_status": ([], _i),
     "fa_release": ([], None),
@@ -240,6 +246,38 @@ def fa_qk_norm_rope_cache(q, k, v, q_weight, k_weight, positions, inv_freq, slot
 
 def fa_qk_norm_rope_backward_workspace_bytes(num_tokens, d) -> int:
     return int(load().fa_qk_norm_rope_backward_workspace_bytes(num_tokens, d))
+
+
+def fa_forward_packed(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads,
+                      num_kv_heads, d, q_stride, k_stride, v_stride, scale, causal,
+                      stream) -> int:
+    return _check("fa_forward_packed", load().fa_forward_packed(
+        q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads, num_kv_heads, d, q_stride,
+        k_stride, v_stride, scale, int(causal), stream))
+
+
+def fa_forward_packed_f16(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads,
+                          num_kv_heads, d, q_stride, k_stride, v_stride, scale, causal,
+                          stream) -> int:
+    return _check("fa_forward_packed_f16", load().fa_forward_packed_f16(
+        q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads, num_kv_heads, d, q_stride,
+        k_stride, v_stride, scale, int(causal), stream))
+
+
+def fa_paged_prefill_workspace_bytes(num_seqs, total_tokens, num_heads, num_kv_heads,
+                                     max_num_blocks_per_seq) -> int:
+    return int(load().fa_paged_prefill_workspace_bytes(
+        num_seqs, total_tokens, num_heads, num_kv_heads, max_num_blocks_per_seq))
+
+
+def fa_paged_prefill(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out, num_seqs,
+                     total_tokens, num_heads, num_kv_heads, head_size, block_size, num_blocks,
+                     max_num_blocks_per_seq, q_stride, scale, workspace, workspace_bytes,
+                     stream) -> int:
+    return _check("fa_paged_prefill", load().fa_paged_prefill(
+        q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out, num_seqs, total_tokens,
+        num_heads, num_kv_heads, head_size, block_size, num_blocks, max_num_blocks_per_seq,
+        q_stride, scale, workspace, workspace_bytes, stream))
 
 
 def fa_status_string(status: int) -> str:
@@ -648,3 +686,92 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight=No
         _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
         _stream(q)))
     return dq, dk, dqw, dkw
+
+
+def _packed_args(q, k, v, cu_seqlens):
+    import torch
+    qs, ks = _rows("q", q, q), _rows("k", k, q)
+    vs = _rows("v", v, q, k.shape[1])
+    _vector("cu_seqlens", cu_seqlens, torch.int32, q)
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens holds num_seqs + 1 offsets")
+    return qs, ks, vs
+
+
+@_on_device
+def forward_packed(q, k, v, cu_seqlens, scale=None, causal=True, out=None, lse=None,
+                   want_lse=True):
+    """Exact attention over packed prompts: q [T,H,d], k and v [T,Hk,d] (bf16 or
+    fp16 CUDA tensors, heads dense, any token stride that is a multiple of 8
+    elements), sequence s in rows cu_seqlens[s] .. cu_seqlens[s+1] - 1
+    (int32 [S+1] on the device).  d is 64 or 128; H a multiple of Hk.
+
+    Returns (O [T,H,d], LSE fp32 [H,T] or None).  Rows of no sequence are not
+    written (they are uninitialised in tensors made here).  Runs on the current
+    torch stream."""
+    import torch
+    qs, ks, vs = _packed_args(q, k, v, cu_seqlens)
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("q, k, v must be bf16 or fp16")
+    T, H, d = q.shape
+    if scale is None:
+        scale = d ** -0.5
+    if out is None:
+        out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    _vector("out", out, q.dtype, q, q.numel())
+    if lse is None and want_lse:
+        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _vector("lse", lse, torch.float32, q, H * T)
+    if T == 0:
+        return out, lse
+    name = "fa_forward_packed" + ("_f16" if q.dtype == torch.float16 else "")
+    _check(name, getattr(load(), name)(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens),
+        cu_seqlens.numel() - 1, T, H, k.shape[1], d, qs, ks, vs, scale, int(causal), _stream(q)))
+    return out, lse
+
+
+@_on_device
+def paged_prefill(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, scale=None,
+                  out=None, workspace=None):
+    """Attention of new tokens over a paged cache (layouts of ``paged_decode``):
+    q bf16 [T,H,128] holds each sequence's chunk in rows cu_seqlens[s] ..
+    cu_seqlens[s+1] - 1; the chunk's own keys and values are in the cache
+    already and context_lens counts them.  ``workspace`` (optional) is a CUDA
+    tensor of at least ``fa_paged_prefill_workspace_bytes`` bytes.  Returns out
+    [T,H,128]; rows of no sequence are not written.  Runs on the current torch
+    stream."""
+    import torch
+    qs = _rows("q", q, q)
+    T, H, D = q.shape
+    if q.dtype != torch.bfloat16:
+        raise ValueError("q must be bf16")
+    if k_cache.dim() != 5 or block_tables.dim() != 2:
+        raise ValueError("inconsistent cache shapes")
+    nb, Hk, Dx, bs, x = k_cache.shape
+    S, mb = block_tables.shape
+    if Hk <= 0 or H % Hk != 0 or Dx * x != D or x != 8 or tuple(v_cache.shape) != (nb, Hk, D, bs):
+        raise ValueError("inconsistent cache shapes")
+    _vector("k_cache", k_cache, q.dtype, q)
+    _vector("v_cache", v_cache, q.dtype, q)
+    _vector("block_tables", block_tables, torch.int32, q)
+    _vector("context_lens", context_lens, torch.int32, q, S)
+    _vector("cu_seqlens", cu_seqlens, torch.int32, q, S + 1)
+    if scale is None:
+        scale = D ** -0.5
+    if out is None:
+        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+    _vector("out", out, q.dtype, q, q.numel())
+    if T == 0 or S == 0:
+        return out
+    lib = load()
+    if workspace is None:
+        nbytes = lib.fa_paged_prefill_workspace_bytes(S, T, H, Hk, mb)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    _check("fa_paged_prefill", lib.fa_paged_prefill(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
+        _ptr(cu_seqlens), _ptr(out), S, T, H, Hk, D, bs, nb, mb, qs, scale, _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(q)))
+    return out

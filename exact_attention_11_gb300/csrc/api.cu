@@ -129,9 +129,11 @@ int encode_e4m3_map(CUtensorMap *m, const void *base, int BH, int rows, int inne
 // 16 x 128 (a block's V^T, 4 KB) written with the 32-byte swizzle.  The block
 // extent is the largest int block id: which blocks are read comes from the
 // block tables, as in the plain decode.
+// (fa_paged_prefill knows the cache's block count and passes it: ids outside
+// the cache then read as zeros.)
 int encode_paged_kv_maps(CUtensorMap *tk, CUtensorMap *tv, const void *k_cache,
-                         const void *v_cache, int num_kv_heads) {
-  const cuuint64_t nb = 0x7fffffffull, hk = (cuuint64_t)num_kv_heads;
+                         const void *v_cache, int num_kv_heads, int num_blocks = 0x7fffffff) {
+  const cuuint64_t nb = (cuuint64_t)num_blocks, hk = (cuuint64_t)num_kv_heads;
   const cuuint64_t kd[5] = {64, 2, 16, hk, nb};
   const cuuint64_t ks[4] = {128, 256, 4096, 4096 * hk};
   const cuuint32_t kb[5] = {64, 1, 16, 1, 1};
@@ -150,6 +152,27 @@ int encode_paged_kv_maps(CUtensorMap *tk, CUtensorMap *tv, const void *k_cache,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return FA_ERR_CUDA;
   return FA_OK;
+}
+
+// 3-D 16-bit view of a [T, heads, d] tensor with dense heads whose tokens are
+// `stride` elements apart: {d, heads, T} (queries; boxes of 64 x box1 heads x
+// box2 tokens) or, with tokens_first, {d, T, heads} (keys and values; boxes of
+// 64 x box1 tokens x box2 heads).  128-byte swizzle; tokens past T read as
+// zero.
+int encode_rows_map(CUtensorMap *m, const void *base, int T, int heads, int d, long long stride,
+                    bool tokens_first, int box1, int box2, CUtensorMapDataType dtype) {
+  const cuuint64_t n_tok = (cuuint64_t)T, n_head = (cuuint64_t)heads;
+  const cuuint64_t s_tok = (cuuint64_t)stride * 2, s_head = (cuuint64_t)d * 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, tokens_first ? n_tok : n_head,
+                              tokens_first ? n_head : n_tok};
+  const cuuint64_t strides[2] = {tokens_first ? s_tok : s_head, tokens_first ? s_head : s_tok};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box1, (cuuint32_t)box2};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(m, dtype, 3, const_cast<void *>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
 }
 
 // Keys per row of the transposed FP8 V: N rounded up to 16.
@@ -748,6 +771,147 @@ FATTN_QK_PREP_BACKWARD(fa_qk_norm_rope_backward_f16, ElemType::kF16)
 FATTN_QK_PREP_BACKWARD(fa_qk_norm_rope_backward_fp32, ElemType::kF32)
 #undef FATTN_QK_PREP_BACKWARD
 #undef FATTN_QK_PREP
+
+namespace {
+// Sizes that the packed calls share: T tokens of S sequences, H query heads on
+// Hk key/value heads.
+int check_packed_sizes(int S, int T, int H, int Hk) {
+  if (S < 0 || T < 0 || H <= 0 || Hk <= 0 || H % Hk != 0) return FA_ERR_INVALID_ARG;
+  // A query tile holds 128 / group tokens; indices of rows and items are 32-bit.
+  const int group = H / Hk;
+  if (group > 128 || H > 65535 || S > (1 << 26) || T > (1 << 29)) return FA_ERR_UNSUPPORTED;
+  if ((long long)T * H > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  if ((long long)fattn::packed_blocks(T, S, group) * Hk > 0x3fffffffLL) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+// Checks shared by the packed forward and backward.
+int check_packed(const void *q, const void *k, const void *v, const void *o, const void *lse,
+                 const int *cu_seqlens, int S, int T, int H, int Hk, int d, long long q_stride,
+                 long long k_stride, long long v_stride, float scale) {
+  if (!q || !k || !v || !o || !cu_seqlens) return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
+  int rc = check_packed_sizes(S, T, H, Hk);
+  if (rc != FA_OK) return rc;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned_to(lse, 4) ||
+      !aligned_to(cu_seqlens, 4))
+    return FA_ERR_ALIGNMENT;
+  if ((rc = check_token_stride(q_stride, H, d, 2)) != FA_OK) return rc;
+  if ((rc = check_token_stride(k_stride, Hk, d, 2)) != FA_OK) return rc;
+  return check_token_stride(v_stride, Hk, d, 2);
+}
+
+// The current device's work counters for one launch, and its status word.
+int acquire_sched(cudaStream_t s, int **sched, int **status) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  int dev = 0, rc;
+  if ((rc = current_device(&dev)) != FA_OK) return rc;
+  if ((rc = get_encoder()) != FA_OK) return rc;
+  *sched = sched_slot(g_dev[dev], s);
+  *status = g_dev[dev].status;
+  return FA_OK;
+}
+
+int forward_packed(const void *q, const void *k, const void *v, void *o, float *lse,
+                   const int *cu_seqlens, int S, int T, int H, int Hk, int d, long long q_stride,
+                   long long k_stride, long long v_stride, float scale, int causal,
+                   fa_stream_t stream, bool f16) {
+  int rc = check_packed(q, k, v, o, lse, cu_seqlens, S, T, H, Hk, d, q_stride, k_stride, v_stride,
+                        scale);
+  if (rc != FA_OK) return rc;
+  if (S == 0 || T == 0) return FA_OK;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int *sched = nullptr, *status = nullptr;
+  if ((rc = acquire_sched(s, &sched, &status)) != FA_OK) return rc;
+  const CUtensorMapDataType dt =
+      f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int group = H / Hk;
+  CUtensorMap tq, tk, tv;
+  if ((rc = encode_rows_map(&tq, q, T, H, d, q_stride, false, group,
+                            fattn::packed_tile_tokens(group), dt)) != FA_OK)
+    return rc;
+  if ((rc = encode_rows_map(&tk, k, T, Hk, d, k_stride, true, 128, 1, dt)) != FA_OK) return rc;
+  if ((rc = encode_rows_map(&tv, v, T, Hk, d, v_stride, true, 128, 1, dt)) != FA_OK) return rc;
+  fattn::PackedProblem p{};
+  p.o = o, p.lse = lse, p.cu_seqlens = cu_seqlens;
+  p.S = S, p.T = T, p.H = H, p.Hk = Hk, p.causal = causal ? 1 : 0, p.scale = scale;
+  return cuda_status(fattn::launch_fwd_packed(tq, tk, tv, p, d, f16, sched, status, s));
+}
+}  // namespace
+
+int fa_forward_packed(const void *q, const void *k, const void *v, void *o, float *lse,
+                      const int *cu_seqlens, int num_seqs, int total_tokens, int num_heads,
+                      int num_kv_heads, int d, long long q_stride, long long k_stride,
+                      long long v_stride, float scale, int causal, fa_stream_t stream) {
+  return forward_packed(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads,
+                        num_kv_heads, d, q_stride, k_stride, v_stride, scale, causal, stream,
+                        false);
+}
+
+int fa_forward_packed_f16(const void *q, const void *k, const void *v, void *o, float *lse,
+                          const int *cu_seqlens, int num_seqs, int total_tokens, int num_heads,
+                          int num_kv_heads, int d, long long q_stride, long long k_stride,
+                          long long v_stride, float scale, int causal, fa_stream_t stream) {
+  return forward_packed(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads,
+                        num_kv_heads, d, q_stride, k_stride, v_stride, scale, causal, stream,
+                        true);
+}
+
+unsigned long long fa_paged_prefill_workspace_bytes(int num_seqs, int total_tokens, int num_heads,
+                                                    int num_kv_heads,
+                                                    int max_num_blocks_per_seq) {
+  if (num_seqs <= 0 || total_tokens <= 0 || max_num_blocks_per_seq <= 0) return 0;
+  if (check_packed_sizes(num_seqs, total_tokens, num_heads, num_kv_heads) != FA_OK) return 0;
+  return static_cast<unsigned long long>(fattn::paged_prefill_workspace_bytes(
+      total_tokens, num_seqs, num_heads, num_kv_heads, max_num_blocks_per_seq));
+}
+
+int fa_paged_prefill(const void *q, const void *k_cache, const void *v_cache,
+                     const int *block_tables, const int *context_lens, const int *cu_seqlens,
+                     void *out, int num_seqs, int total_tokens, int num_heads, int num_kv_heads,
+                     int head_size, int block_size, int num_blocks, int max_num_blocks_per_seq,
+                     long long q_stride, float scale, void *workspace,
+                     unsigned long long workspace_bytes, fa_stream_t stream) {
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_seqlens || !out)
+    return FA_ERR_INVALID_ARG;
+  if (num_blocks <= 0 || max_num_blocks_per_seq <= 0) return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
+  int rc = check_packed_sizes(num_seqs, total_tokens, num_heads, num_kv_heads);
+  if (rc != FA_OK) return rc;
+  if (head_size != fattn::kDecodeHeadSize || block_size != fattn::kDecodeBlockSize)
+    return FA_ERR_UNSUPPORTED;
+  if (max_num_blocks_per_seq > (1 << 25)) return FA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      !aligned_to(block_tables, 4) || !aligned_to(context_lens, 4) || !aligned_to(cu_seqlens, 4))
+    return FA_ERR_ALIGNMENT;
+  if ((rc = check_token_stride(q_stride, num_heads, head_size, 2)) != FA_OK) return rc;
+  if (num_seqs == 0 || total_tokens == 0) return FA_OK;
+  const size_t need = fattn::paged_prefill_workspace_bytes(total_tokens, num_seqs, num_heads,
+                                                           num_kv_heads, max_num_blocks_per_seq);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return FA_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
+  }
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int *sched = nullptr, *status = nullptr;
+  if ((rc = acquire_sched(s, &sched, &status)) != FA_OK) return rc;
+  const int group = num_heads / num_kv_heads;
+  CUtensorMap tq, tk, tv;
+  if ((rc = encode_rows_map(&tq, q, total_tokens, num_heads, head_size, q_stride, false, group,
+                            fattn::packed_tile_tokens(group),
+                            CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) != FA_OK)
+    return rc;
+  if ((rc = encode_paged_kv_maps(&tk, &tv, k_cache, v_cache, num_kv_heads, num_blocks)) != FA_OK)
+    return rc;
+  fattn::PackedProblem p{};
+  p.o = out, p.cu_seqlens = cu_seqlens, p.context_lens = context_lens;
+  p.block_tables = block_tables;
+  p.S = num_seqs, p.T = total_tokens, p.H = num_heads, p.Hk = num_kv_heads;
+  p.max_blocks = max_num_blocks_per_seq, p.num_blocks = num_blocks, p.causal = 1, p.scale = scale;
+  return cuda_status(fattn::launch_paged_prefill(tq, tk, tv, p, static_cast<float *>(workspace),
+                                                 sched, status, s));
+}
 
 int fa_device_status(void) {
   std::lock_guard<std::mutex> lock(g_mu);

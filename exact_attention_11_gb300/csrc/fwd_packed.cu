@@ -1,0 +1,1027 @@
+// fwd_packed.cu -- exact attention of several queries per sequence for
+// sequences of different lengths in one call, with grouped key/value heads,
+// on the sm_103a tensor cores:
+//   packed   prompts packed one after another, q [T, H, d], k and v [T, Hk, d],
+//            sequence s in rows cu_seqlens[s] .. cu_seqlens[s+1] - 1, every
+//            query against its own sequence's keys (causal or not);
+//   paged    a chunk of new queries per sequence, q [T, H, d], against the
+//            paged cache that holds the sequence's whole context (the chunk's
+//            own keys included): query i of n sees keys 0 .. ctx - n + i.
+//
+// What is computed per row: O = softmax(scale q K^T) V over the visible keys,
+// key tile by key tile with the running maximum and sum of eqs. (2)-(4) of
+// "Flash Attention" (suniverse77.github.io, section "Online Softmax"), as in
+// fwd_bf16.cu, whose warp roles, TMEM plan and MMA order this kernel shares:
+// two 128-row query tiles A and B take turns on the tensor core, O and S stay
+// in TMEM, P is written over S, one softmax warpgroup per tile.
+//
+// What differs, and why:
+//  * A query tile's 128 rows are (token, head of the group) pairs, tokens
+//    outermost: 128 / G tokens of the G query heads that share a key/value
+//    head.  K and V are read once for the whole group, short chunks still fill
+//    MMA rows, and the causal diagonal touches 128 / G keys of a row instead
+//    of 128.  A tile is one TMA box (64 of d) x G heads x (128 / G) tokens; when
+//    G does not divide 128 the last rows of the tile hold no query.
+//  * Sequence bounds are device data.  An item is (block of two tiles, key/value
+//    head [, context partition]); blocks are numbered so that sequence s starts
+//    at block cu_seqlens[s] / (2 * 128/G) + s, which needs no prefix sum over
+//    lengths and leaves at most one unused number per sequence.  The producer
+//    warp finds an item's sequence by a 32-way search and hands the decoded
+//    item to the other roles.  Items are numbered from the last block down, so
+//    that every sequence's heaviest causal blocks come first and the call ends
+//    with its lightest.
+//  * The key tile that a sequence ends in also holds the next sequence's rows
+//    (packed) or whatever the cache slots past the context hold (paged).  Their
+//    scores are set to -inf, and since a zero weight does not cancel a NaN, a
+//    warp of the producer warpgroup clears their V rows in shared memory
+//    before P V may use that tile.
+//  * Paged K and V are read through the TMA views of the grouped decode
+//    (decode_gqa_tc.cu): K in no-swizzle core matrices, V^T in 32-byte-swizzle
+//    blocks of 16 tokens, both K-major B operands here.  Block ids outside the
+//    cache read as zeros.
+//  * Few rows over long contexts do not fill the GPU: the context is then cut
+//    into partitions of `part_tiles` key tiles; each writes its unnormalised
+//    fp32 rows and (max, sum), and paged_merge_kernel joins them (eq. (4)).
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace fattn {
+namespace {
+
+constexpr int BM = 128;             // rows of a query tile (MMA M)
+constexpr int BN = 128;             // keys per tile
+constexpr int kThreads = 384;
+// The register split of fwd_bf16.cu: 168 at launch, 88 / 208 / 208 after.
+constexpr uint32_t kRegsProducer = 88, kRegsSoftmax = 208;
+static_assert(kRegsProducer + 2 * kRegsSoftmax == 3 * 168, "launch register budget");
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleThreshold = 8.0f;   // log2 units (see fwd_bf16.cu)
+constexpr int kBlk = kDecodeBlockSize;      // 16 tokens per cache block
+constexpr int kTileBlocks = BN / kBlk;      // 8 cache blocks per key tile
+
+template <int D>
+struct Cfg {
+  static constexpr int kStages = D == 64 ? 4 : 2;   // K and V ring depth
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTileBytes = BM * D * 2;
+  static constexpr int kBoxBytes = BM * 128;
+  static constexpr int kQ = 0;
+  static constexpr int kK0 = kQ + 2 * kTileBytes;
+  static constexpr int kV0 = kK0 + kStages * kTileBytes;
+  static constexpr int kStage = kV0 + kStages * kTileBytes;   // 8 x 4 KB of output staging
+  static constexpr int kBar = kStage + 8 * 4096;
+  static constexpr int kBytes = kBar + 1024;
+  static constexpr int kAlloc = kBytes + 1024;
+  static_assert(kAlloc <= 227 * 1024, "shared memory budget");
+  static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
+};
+
+enum : int {
+  kBarQFull = 0,       // + tile
+  kBarQEmpty = 2,      // + tile
+  kBarSFull = 4,       // + tile
+  kBarPReady = 6,      // + 2 * tile + half, 4 warps
+  kBarODone = 10,      // + tile
+  kBarDrain = 12,
+  kBarItemFull = 13,   // + ring slot (2)
+  kBarItemEmpty = 15,  // + ring slot (2)
+  kBarKFull = 17,      // + stage (up to 4)
+  kBarKEmpty = 21,
+  kBarVFull = 25,
+  kBarVEmpty = 29,
+  kBarVFix = 33,       // the stage's ragged V tile has been cleared past the sequence; one
+                       // barrier per stage, as a single one could be two phases ahead of
+                       // the MMA warp's wait
+  kNumBars = 37
+};
+// Arrivals that free an item slot: the MMA thread, the V-clearing warp and the
+// eight softmax warps.
+constexpr int kItemConsumers = 1 + 1 + 8;
+
+// A decoded work item.
+struct Item {
+  int live;          // 0: no more items
+  int row0;          // packed row (token) of tile A's first token
+  int n_tok[2];      // tokens of tiles A and B
+  int kvh;           // key/value head
+  int pos0;          // key index that tile A's first token sees last (its position)
+  int kv_len;        // keys of the sequence
+  int kv0;           // packed: first row of the sequence's keys; paged: sequence
+  int kt0;           // first key tile of this partition
+  int n[2];          // key tiles of tiles A and B in this partition
+  int part;          // partition
+  int split[2];      // tile's rows go to the partition workspace
+};
+
+struct Misc {
+  uint32_t tmem_base;
+  int abort;
+  Item item[2];
+};
+static_assert(8 * kNumBars + sizeof(Misc) <= 1024, "barrier area");
+
+struct Args {
+  uint16_t *o;
+  float *lse;                   // [H][T] or null
+  const int *cu_seqlens, *context_lens, *block_tables;
+  float *ws_o;                  // [part][T * H][D]
+  float2 *ws_ml;                // [part][T * H] (max in log2 units, sum)
+  int *sched, *dev_status;
+  int S, T, H, Hk, G, tpb;      // tpb: tokens per query tile, 128 / G
+  int max_blocks, num_blocks;
+  int n_vblocks, n_split, part_tiles, causal;
+  float scale_log2;
+};
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
+
+// Key tiles that `n` tokens, the last of which sees key `last` last, visit.
+__device__ __forceinline__ int tiles_for(int n, int last, int kv_len) {
+  return n > 0 ? (max(0, min(kv_len, last + 1)) + BN - 1) / BN : 0;
+}
+
+// A query that sees every key of its sequence.
+constexpr int kSeesAll = 0x3fffffff;
+
+// Sequence s: its packed rows [begin, begin + n), keys and first position.
+struct Seq {
+  int begin, n, kv_len, pos;
+};
+template <bool PAGED>
+__device__ __forceinline__ Seq sequence(const Args &a, int s) {
+  Seq q;
+  q.begin = clampi(a.cu_seqlens[s], 0, a.T);
+  q.n = clampi(a.cu_seqlens[s + 1], q.begin, a.T) - q.begin;
+  if (PAGED) {
+    q.kv_len = clampi(a.context_lens[s], 0, a.max_blocks * kBlk);
+    q.pos = q.kv_len - q.n;
+  } else {
+    q.kv_len = q.n;
+    q.pos = a.causal ? 0 : kSeesAll;
+  }
+  return q;
+}
+
+// The last s in [0, S) with first(s) <= v for a non-decreasing first(), or -1;
+// by the whole warp, 32 candidates a round.
+template <typename F>
+__device__ __forceinline__ int warp_search(int S, int v, F first) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = S;
+  while (true) {
+    const int step = (n + 31) / 32;
+    const int i = lo + lane * step;
+    const uint32_t m = __ballot_sync(~0u, lane * step < n && first(i) <= v);
+    if (m == 0) return -1;
+    const int hit = 31 - __clz(m);
+    if (step == 1) return lo + hit;
+    lo += hit * step;
+    n = min(step, n - hit * step);
+  }
+}
+
+// Item w (whole warp); false if it has no work.
+template <bool PAGED>
+__device__ __forceinline__ bool decode_item(const Args &a, int w, Item &it) {
+  const int tb = 2 * a.tpb;
+  it.kvh = w % a.Hk;
+  const int r = w / a.Hk;
+  it.part = r % a.n_split;
+  const int vb = a.n_vblocks - 1 - r / a.n_split;
+  const int s = warp_search(
+      a.S, vb, [&](int i) { return clampi(a.cu_seqlens[i], 0, a.T) / tb + i; });
+  if (s < 0) return false;
+  const Seq q = sequence<PAGED>(a, s);
+  const int tok0 = (vb - q.begin / tb - s) * tb;
+  if (tok0 < 0 || tok0 >= q.n) return false;
+  it.live = 1;
+  it.row0 = q.begin + tok0;
+  it.pos0 = q.pos + tok0;
+  it.kv_len = q.kv_len;
+  it.kv0 = PAGED ? s : q.begin;
+  it.kt0 = it.part * a.part_tiles;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    it.n_tok[t] = clampi(q.n - tok0 - t * a.tpb, 0, a.tpb);
+    const int total = tiles_for(it.n_tok[t], it.pos0 + t * a.tpb + it.n_tok[t] - 1, q.kv_len);
+    it.n[t] = clampi(total - it.kt0, 0, a.part_tiles);
+    it.split[t] = total > a.part_tiles;
+  }
+  return it.part == 0 || it.n[0] > 0 || it.n[1] > 0;
+}
+
+// 16-bit element types: as in fwd_bf16.cu.
+template <bool F16>
+__device__ __forceinline__ constexpr uint32_t idesc16(uint32_t bf16_desc) {
+  return F16 ? (bf16_desc & ~((1u << 7) | (1u << 10))) : bf16_desc;
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if (F16) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+  return pack_bf16x2(lo, hi);
+}
+
+// High descriptor words: 128-byte swizzle with 1024-byte row groups
+// (kSdescHi1024); no swizzle, 8-token groups 2 KB apart (paged K); 32-byte
+// swizzle, 8-row groups 256 bytes apart (paged V^T).
+constexpr uint32_t kHiPagedK = (2048u >> 4) | (1u << 14);
+constexpr uint32_t kHiPagedV = (256u >> 4) | (1u << 14) | (6u << 29);
+
+__device__ __forceinline__ void mma_ss_hi(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                          uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .b64 da, db;\n .reg .pred p;\n mov.b64 da, {%1, %5};\n mov.b64 db, {%2, %6};\n"
+      " setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kSdescHi1024), "r"(b_hi)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_hi(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                          uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .b64 db;\n .reg .pred p;\n mov.b64 db, {%2, %5};\n"
+      " setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(b_hi)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *m, int c0, int c1,
+                                            int c2, int c3, int c4, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *m, int c0, int c1,
+                                            int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+
+// A wait that all lanes of the warp leave with one answer.
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t ph, volatile int *abort_flag) {
+  return __all_sync(~0u, mbar_wait(bar, ph, abort_flag));
+}
+
+__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t ph) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, ph) && globaltimer_ns() - t0 < kWaitLimitNs) {
+  }
+}
+
+// The key tile whose V holds rows past the sequence's keys, or -1.
+__device__ __forceinline__ int ragged_tile(int kv_len) {
+  return kv_len % BN != 0 ? kv_len / BN : -1;
+}
+
+template <int D, bool F16, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+    fwd_packed_kernel(const __grid_constant__ CUtensorMap tm_q,
+                      const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const Args a) {
+  using C = Cfg<D>;
+  static_assert(!PAGED || (D == 128 && !F16), "the paged cache is bf16, d = 128");
+  constexpr int S = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t s_base = smem_u32(smem);
+  const uint32_t bars = s_base + C::kBar;
+  auto bar = [&](int i) { return bars + 8u * i; };
+  Misc *misc = reinterpret_cast<Misc *>(smem + C::kBar + 8 * kNumBars);
+  volatile int *abort_flag = &misc->abort;
+  const int n_items = a.n_vblocks * a.n_split * a.Hk;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // Consumer side of the item ring.  take_item waits for entry k (whole warp, or
+  // the lone MMA thread); after reading what it needs of misc->item[k & 1], the
+  // consumer frees the slot (one arrival per warp).
+  auto take_item = [&](int k, bool whole_warp) -> bool {
+    const bool full = mbar_wait(bar(kBarItemFull + (k & 1)), (k >> 1) & 1, abort_flag);
+    return whole_warp ? __all_sync(~0u, full) : full;
+  };
+  auto free_item = [&](int k, bool whole_warp) {
+    if (whole_warp) __syncwarp();
+    if (!whole_warp || lane == 0) mbar_arrive(bar(kBarItemEmpty + (k & 1)));
+  };
+  auto item_of = [&](int k) -> const volatile Item & {
+    return *reinterpret_cast<const volatile Item *>(&misc->item[k & 1]);
+  };
+
+  if (threadIdx.x == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(kBarQFull + t), 1);
+      mbar_init(bar(kBarQEmpty + t), 1);
+      mbar_init(bar(kBarSFull + t), 1);
+      mbar_init(bar(kBarPReady + 2 * t), 4);
+      mbar_init(bar(kBarPReady + 2 * t + 1), 4);
+      mbar_init(bar(kBarODone + t), 1);
+      mbar_init(bar(kBarItemFull + t), 1);
+      mbar_init(bar(kBarItemEmpty + t), kItemConsumers);
+    }
+    mbar_init(bar(kBarDrain), 1);
+    for (int s = 0; s < S; ++s) {
+      mbar_init(bar(kBarKFull + s), 1);
+      mbar_init(bar(kBarKEmpty + s), 1);
+      mbar_init(bar(kBarVFull + s), 1);
+      mbar_init(bar(kBarVEmpty + s), 2);   // P V done, and seen by the clearing warp
+      mbar_init(bar(kBarVFix + s), 1);
+    }
+    misc->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&misc->tmem_base), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = misc->tmem_base;
+  // A programmatic dependent of the kernel before it on the stream: nothing in
+  // global memory is touched before that one has finished.  The merge kernel
+  // may be scheduled from here on; it waits for this grid in turn.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (PAGED && threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
+    if (warp == 0) {
+      // ---------------------------------------------------------- producer
+      // The whole warp decodes items and holds block ids; lane 0 waits, and
+      // issues the packed copies; lanes 0 .. 7 issue a paged tile's copies.
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+      }
+      int kv = 0, nk = 0, nv = 0, nq[2] = {0, 0};
+      bool ok = true;
+      int w = blockIdx.x;       // the first item is the CTA's own; the rest are claimed
+      int w_claim = 0;          // lane 0: the claim in flight
+      auto claim = [&]() {
+        if (lane == 0) w_claim = static_cast<int>(gridDim.x) + atomicAdd(a.sched, 1);
+      };
+      auto claimed = [&]() { return __shfl_sync(~0u, w_claim, 0); };
+      // The next item with work at or after w, claiming on; live = 0 at the end.
+      Item nxt;
+      int nxt_id = 0;           // paged: block id of the item's block `lane`
+      auto ids_of = [&](const Item &it, int tile) -> int {
+        // Lane i: block i of the four key tiles from `tile` on; past the
+        // context, a block that the cache does not have (reads as zeros).
+        const int b = tile * kTileBlocks + lane;
+        if (b >= (it.kv_len + kBlk - 1) / kBlk) return a.num_blocks;
+        return a.block_tables[static_cast<int64_t>(it.kv0) * a.max_blocks + b];
+      };
+      auto find = [&]() {
+        for (;;) {
+          if (w >= n_items) {
+            nxt.live = 0;
+            return;
+          }
+          if (decode_item<PAGED>(a, w, nxt)) break;
+          claim();
+          w = claimed();
+        }
+        if (PAGED) nxt_id = ids_of(nxt, nxt.kt0);
+      };
+      find();
+      for (int k = 0; ok; ++k) {
+        const Item it = nxt;
+        int ids = nxt_id, ids_next = 0;
+        const int slot = k & 1;
+        if (lane == 0) {
+          ok = mbar_wait(bar(kBarItemEmpty + slot), ((k >> 1) & 1) ^ 1, abort_flag);
+          if (ok) {
+            misc->item[slot] = it;
+            mbar_arrive(bar(kBarItemFull + slot));
+          }
+        }
+        if (!(ok = __shfl_sync(~0u, ok, 0)) || !it.live) break;
+        claim();
+        bool looked = false;
+        // Query tile t, once the last Q K^T of the tile before has read it.
+        auto load_q = [&](int t) -> bool {
+          if (it.n[t] == 0) return true;
+          bool good = true;
+          if (lane == 0) {
+            good = mbar_wait(bar(kBarQEmpty + t), (nq[t] & 1) ^ 1, abort_flag);
+            if (good) {
+              mbar_arrive_expect_tx(bar(kBarQFull + t), a.G * a.tpb * D * 2);
+              for (int b = 0; b < C::kBoxes; ++b)
+                tma_load_3d(s_base + C::kQ + t * C::kTileBytes + b * C::kBoxBytes, &tm_q, b * 64,
+                            it.kvh * a.G, it.row0 + t * a.tpb, bar(kBarQFull + t));
+            }
+          }
+          good = __shfl_sync(~0u, good, 0);
+          if (good) ++nq[t];
+          return good;
+        };
+        if (!(ok = load_q(0))) break;
+        const int n_max = max(it.n[0], it.n[1]);
+        if (n_max == 0 && !(ok = load_q(1))) break;
+        for (int j = 0; j < n_max; ++j, ++kv) {
+          const int st = kv % S;
+          const uint32_t ph = (kv / S) & 1;
+          const int tile = it.kt0 + j;
+          const uint32_t k_dst = s_base + C::kK0 + st * C::kTileBytes;
+          const uint32_t v_dst = s_base + C::kV0 + st * C::kTileBytes;
+          int pb = 0;
+          if (PAGED) {
+            if ((j & 3) == 0) {
+              if (j > 0) ids = ids_next;
+              if (j + 4 < n_max) ids_next = ids_of(it, tile + 4);
+            }
+            pb = __shfl_sync(~0u, ids, (j & 3) * kTileBlocks + (lane & 7));
+          }
+          if (lane == 0) {
+            ok = mbar_wait(bar(kBarKEmpty + st), ph ^ 1, abort_flag);
+            if (ok) mbar_arrive_expect_tx(bar(kBarKFull + st), C::kTileBytes);
+          }
+          if (!(ok = __shfl_sync(~0u, ok, 0))) break;
+          if (PAGED) {
+            if (lane < kTileBlocks) {
+              tma_load_5d(k_dst + lane * 4096, &tm_k, 0, 0, 0, it.kvh, pb, bar(kBarKFull + st));
+              tma_load_5d(k_dst + lane * 4096 + 2048, &tm_k, 0, 1, 0, it.kvh, pb,
+                          bar(kBarKFull + st));
+            }
+          } else if (lane == 0) {
+            for (int b = 0; b < C::kBoxes; ++b)
+              tma_load_3d(k_dst + b * C::kBoxBytes, &tm_k, b * 64, it.kv0 + tile * BN, it.kvh,
+                          bar(kBarKFull + st));
+          }
+          nk = kv + 1;
+          if (j == 0 && !(ok = load_q(1))) break;
+          if (lane == 0) {
+            ok = mbar_wait(bar(kBarVEmpty + st), ph ^ 1, abort_flag);
+            if (ok) mbar_arrive_expect_tx(bar(kBarVFull + st), C::kTileBytes);
+          }
+          if (!(ok = __shfl_sync(~0u, ok, 0))) break;
+          if (PAGED) {
+            if (lane < kTileBlocks)
+              tma_load_4d(v_dst + lane * 4096, &tm_v, 0, 0, it.kvh, pb, bar(kBarVFull + st));
+          } else if (lane == 0) {
+            for (int b = 0; b < C::kBoxes; ++b)
+              tma_load_3d(v_dst + b * C::kBoxBytes, &tm_v, b * 64, it.kv0 + tile * BN, it.kvh,
+                          bar(kBarVFull + st));
+          }
+          nv = kv + 1;
+          if (j == 0) {
+            // With the first tile's copies under way: the next item.
+            w = claimed();
+            find();
+            looked = true;
+          }
+        }
+        if (!ok) break;
+        if (!looked) {
+          w = claimed();
+          find();
+        }
+      }
+      // (A claim in flight after an abort: its value is read before the exit
+      // is counted.)
+      if (!ok && claimed() < 0) *abort_flag = 1;
+      if (!ok && lane == 0) {
+        // Let the copies in flight land before the CTA exits.
+        for (int t = 0; t < 2; ++t)
+          if (nq[t] > 0) drain_wait(bar(kBarQFull + t), (nq[t] - 1) & 1);
+        for (int i = (nk > S ? nk - S : 0); i < nk; ++i)
+          drain_wait(bar(kBarKFull + i % S), (i / S) & 1);
+        for (int i = (nv > S ? nv - S : 0); i < nv; ++i)
+          drain_wait(bar(kBarVFull + i % S), (i / S) & 1);
+      }
+    } else if (warp == 1 && elect_one()) {
+      // ---------------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc_qk = idesc16<F16>(idesc_bf16_f32(BM, BN, false));
+      constexpr uint32_t idesc_pv = idesc16<F16>(idesc_bf16_f32(BM, D, !PAGED));
+      constexpr uint32_t k_hi = PAGED ? kHiPagedK : kSdescHi1024;
+      constexpr uint32_t v_hi = PAGED ? kHiPagedV : kSdescHi1024;
+      const uint32_t dq = sdesc_lo(s_base + C::kQ, 16);
+      const uint32_t dk = sdesc_lo(s_base + C::kK0, PAGED ? 128 : 16);
+      const uint32_t dv = sdesc_lo(s_base + C::kV0, PAGED ? 16 : C::kBoxBytes);
+      auto qk = [&](int t, int kvi) {
+        const uint32_t qa = dq + ((t * C::kTileBytes) >> 4);
+        const uint32_t kb = dk + (((kvi % S) * C::kTileBytes) >> 4);
+        const uint32_t s_col = tmem + (t ? C::kColS1 : C::kColS0);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4;
+          mma_ss_hi(s_col, qa + off, kb + (PAGED ? (kk * 256) >> 4 : off), k_hi, idesc_qk,
+                    kk > 0 ? 1u : 0u);
+        }
+        mma_commit(bar(kBarSFull + t));
+      };
+      // Half h of O_T += P_T V: keys 64h .. 64h + 63 of the tile.
+      auto pv = [&](int t, int kvi, bool first, int h) {
+        const uint32_t vb = dv + (((kvi % S) * C::kTileBytes) >> 4);
+        const uint32_t s_col = tmem + (t ? C::kColS1 : C::kColS0);
+        const uint32_t o_col = tmem + (t ? C::kColO1 : C::kColO0);
+#pragma unroll
+        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+          mma_ts_hi(o_col, s_col + kk * 8, vb + ((kk * (PAGED ? 4096 : 2048)) >> 4), v_hi,
+                    idesc_pv, (!first || kk > 0) ? 1u : 0u);
+      };
+      auto wait_k = [&](int kvi) {
+        return mbar_wait(bar(kBarKFull + kvi % S), (kvi / S) & 1, abort_flag);
+      };
+      int nq[2] = {0, 0}, np[2] = {0, 0}, kv = 0;
+      uint32_t fix_parity = 0;   // bit: stage
+      // First Q K^T of an item for tile t; key tile kvi has to be kept for it.
+      auto first_qk = [&](int t, int n, int kvi) -> bool {
+        if (!mbar_wait(bar(kBarQFull + t), nq[t] & 1, abort_flag) || !wait_k(kvi)) return false;
+        ++nq[t];
+        tc_fence_after();
+        qk(t, kvi);
+        if (n == 1) mma_commit(bar(kBarQEmpty + t));
+        return true;
+      };
+      // P V of step j and, if there is one, Q K^T of the next.
+      auto pv_step = [&](int t, int n, int j, int kvj) -> bool {
+        for (int h = 0; h < 2; ++h) {
+          if (!mbar_wait(bar(kBarPReady + 2 * t + h), np[t] & 1, abort_flag)) return false;
+          tc_fence_after();
+          pv(t, kvj, j == 0, h);
+        }
+        ++np[t];
+        if (j == n - 1) mma_commit(bar(kBarODone + t));
+        return true;
+      };
+      auto next_qk = [&](int t, int n, int j, int kvj) -> bool {
+        if (j + 1 >= n) return true;
+        if (!wait_k(kvj + 1)) return false;
+        tc_fence_after();
+        qk(t, kvj + 1);
+        if (j + 2 == n) mma_commit(bar(kBarQEmpty + t));
+        return true;
+      };
+      // An item as the issuer sees it: key tiles of A and B, and which of them
+      // (counted from the item's first) is the sequence's ragged one.
+      struct Work {
+        int live, n_a, n_b, ragged;
+      };
+      auto fetch = [&](int k, Work &x) -> bool {
+        if (!take_item(k, false)) return false;
+        const volatile Item &i = item_of(k);
+        x.live = i.live, x.n_a = i.n[0], x.n_b = i.n[1];
+        x.ragged = ragged_tile(i.kv_len) - i.kt0;
+        free_item(k, false);
+        return true;
+      };
+      Work it, nx;
+      bool a0_issued = false;   // the item's first Q K^T of tile A went out a step early
+      bool ok = fetch(0, it);
+      for (int k = 0; ok && it.live; ++k) {
+        const int n_max = max(it.n_a, it.n_b);
+        if (it.n_a > 0 && !a0_issued && !(ok = first_qk(0, it.n_a, kv))) break;
+        a0_issued = false;
+        if (it.n_b > 0 && !(ok = first_qk(1, it.n_b, kv))) break;
+        if (n_max > 0) mma_commit(bar(kBarKEmpty + kv % S));
+        bool fetched = false;
+        for (int j = 0; j < n_max; ++j) {
+          const int kvj = kv + j, st = kvj % S;
+          if (j == it.ragged) {
+            if (!(ok = mbar_wait(bar(kBarVFix + st), (fix_parity >> st) & 1, abort_flag))) break;
+            fix_parity ^= 1u << st;
+          } else if (!(ok = mbar_wait(bar(kBarVFull + st), (kvj / S) & 1, abort_flag))) {
+            break;
+          }
+          if (j < it.n_a && !(ok = pv_step(0, it.n_a, j, kvj) && next_qk(0, it.n_a, j, kvj)))
+            break;
+          if (j == n_max - 1) {
+            // S_A is free: the next item's tile A starts now.
+            if (!(ok = fetch(k + 1, nx))) break;
+            fetched = true;
+            if (nx.live && nx.n_a > 0) {
+              if (!(ok = first_qk(0, nx.n_a, kv + n_max))) break;
+              a0_issued = true;
+            }
+          }
+          if (j < it.n_b && !(ok = pv_step(1, it.n_b, j, kvj))) break;
+          mma_commit(bar(kBarVEmpty + st));
+          if (j < it.n_b && !(ok = next_qk(1, it.n_b, j, kvj))) break;
+          if (j + 1 < n_max) mma_commit(bar(kBarKEmpty + (kvj + 1) % S));
+        }
+        if (!ok) break;
+        kv += n_max;
+        if (!fetched && !(ok = fetch(k + 1, nx))) break;
+        it = nx;
+      }
+      // Drain: every MMA issued above has completed once this phase does.
+      mma_commit(bar(kBarDrain));
+      drain_wait(bar(kBarDrain), 0);
+    } else if (warp == 2) {
+      // ------------------------------------- V rows past the sequence's keys
+      int kv = 0;
+      for (int k = 0; take_item(k, true); ++k) {
+        const volatile Item &it = item_of(k);
+        const int live = it.live, n_max = max(it.n[0], it.n[1]), kv_len = it.kv_len;
+        const int ragged = ragged_tile(kv_len) - it.kt0;
+        free_item(k, true);
+        if (!live) break;
+        // The warp follows every V tile and takes part in freeing it, so that
+        // the ring cannot run past the phase that it waits for.
+        bool ok = true;
+        for (int j = 0; j < n_max; ++j, ++kv) {
+          const int st = kv % S;
+          if (!(ok = wait_warp(bar(kBarVFull + st), (kv / S) & 1, abort_flag))) break;
+          if (j == ragged) {
+            uint8_t *v = smem + C::kV0 + st * C::kTileBytes;
+            const int keep = kv_len % BN;
+            if (PAGED) {
+              // Only the block that the context ends in: the later ones of the
+              // tile were read as zeros.  V^T rows are 16 tokens (32 bytes), the
+              // two 16-byte halves of row r exchanged where r & 4.
+              const int blk = keep / kBlk, rest = keep % kBlk;
+              if (rest != 0)
+                for (int r = lane; r < D; r += 32) {
+                  uint16_t *row = reinterpret_cast<uint16_t *>(v + blk * 4096 + r * 32);
+                  for (int t = rest; t < kBlk; ++t)
+                    row[((((t >> 3) ^ (r >> 2)) & 1) << 3) + (t & 7)] = 0;
+                }
+            } else {
+              for (int i = lane; i < (BN - keep) * 8; i += 32)
+#pragma unroll
+                for (int b = 0; b < C::kBoxes; ++b)
+                  *reinterpret_cast<uint4 *>(v + b * C::kBoxBytes + (keep + (i >> 3)) * 128 +
+                                             (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarVFix + st));
+          }
+          if (lane == 0) mbar_arrive(bar(kBarVEmpty + st));
+        }
+        if (!ok) break;
+      }
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
+    // ------------------------------------------------------------ softmax
+    const int t = (warp - 4) >> 2;                 // query tile: 0 = A, 1 = B
+    const int quarter = warp & 3;                  // TMEM lanes 32*quarter .. +31
+    const int r_local = quarter * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t s_tmem = tmem + lane_off + (t ? C::kColS1 : C::kColS0);
+    const uint32_t o_tmem = tmem + lane_off + (t ? C::kColO1 : C::kColO0);
+    const uint64_t c2 = f2(a.scale_log2, a.scale_log2);
+    const int my_tok = r_local / a.G, my_head = r_local - my_tok * a.G;
+    uint8_t *stg = smem + C::kStage + (t * 4 + quarter) * 4096;
+    int sc = 0, n_done = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!(ok = take_item(k, true))) break;
+      const volatile Item &it = item_of(k);
+      const int live = it.live, n_mine = it.n[t], part = it.part;
+      const bool split = it.split[t] != 0;
+      // Keys below lim are visible to this row; a tile needs the test only
+      // where it passes the limit of the query tile's first token.
+      const int tile_pos = it.pos0 + t * a.tpb, key0 = it.kt0 * BN;
+      const int lim = min(it.kv_len, tile_pos + my_tok + 1) - key0;
+      const int lim_first = min(it.kv_len, tile_pos + 1) - key0;
+      // This row's place in the output, [token][head]; -1: it holds no query.
+      const int row = it.row0 + t * a.tpb + my_tok, head = it.kvh * a.G + my_head;
+      const int my_out = my_tok < min(it.n_tok[t], a.tpb) ? row * a.H + head : -1;
+      free_item(k, true);
+      if (!live) break;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n_mine; ++j, ++sc) {
+        if (!(ok = wait_warp(bar(kBarSFull + t), sc & 1, abort_flag))) break;
+        tc_fence_after();
+        uint32_t sv[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_tmem + c * 32, sv[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_wait_ld(sv[c]);
+#define S_(c) sv[(c) >> 5][(c) & 31]
+        if ((j + 1) * BN > lim_first) {
+          const int lim_j = lim - j * BN;
+#pragma unroll
+          for (int c = 0; c < BN; ++c)
+            if (c >= lim_j) S_(c) = __float_as_uint(-INFINITY);
+        }
+        float mx[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mx[i] = fmaxf(__uint_as_float(S_(2 * i)), __uint_as_float(S_(2 * i + 1)));
+#pragma unroll
+        for (int c = 8; c < BN; c += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mx[i] = fmax3(mx[i], __uint_as_float(S_(c + 2 * i)), __uint_as_float(S_(c + 2 * i + 1)));
+        const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        float alpha = 1.f;
+        if (tmax > m + kRescaleThreshold) {  // also true while m = -inf
+          alpha = ex2_approx(m - tmax);
+          m = tmax;
+        }
+        // P V of tile j - 1 was issued before Q K^T of tile j: O_T is complete.
+        if (j > 0 && __any_sync(~0u, alpha != 1.f)) {
+          const uint64_t a2 = f2(alpha, alpha);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tmem_ld32(o_tmem + c * 32, ov);
+            tmem_wait_ld(ov);
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x =
+                  f2_split(fmul2(f2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])), a2));
+              ov[e] = __float_as_uint(x.x);
+              ov[e + 1] = __float_as_uint(x.y);
+            }
+            tmem_st32(o_tmem + c * 32, ov);
+          }
+        }
+        // A row that has seen no key yet has m = -inf: 0 in its place gives
+        // its (all masked) scores p = 0 rather than NaN.
+        const float nmv = m == -INFINITY ? 0.f : -m;
+        const uint64_t nm2 = f2(nmv, nmv);
+        uint64_t sum2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 x = f2_split(
+                ffma2(f2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1])), c2, nm2));
+            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            sum2[(e >> 1) & 1] = fadd2(sum2[(e >> 1) & 1], f2(p.x, p.y));
+            // Rounded to the element type: the MMA takes no wider A operand.
+            pk[e >> 1] = pack2<F16>(p.x, p.y);
+          }
+          tmem_st16(s_tmem + c * 16, pk);
+          if (c & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarPReady + 2 * t + (c >> 1)));
+          }
+        }
+#undef S_
+        const float2 sa = f2_split(fadd2(sum2[0], sum2[1]));
+        l = l * alpha + (sa.x + sa.y);
+      }
+      if (!ok) break;
+      // Epilogue, once the last P V is done.  A tile without key tiles writes
+      // zeros if it has none at all, and nothing if other partitions have them.
+      const bool some = n_mine > 0;
+      if (!some && part > 0) continue;
+      if (some) {
+        if (!(ok = wait_warp(bar(kBarODone + t), n_done & 1, abort_flag))) break;
+        ++n_done;
+        tc_fence_after();
+      }
+      if (split) {
+        // Unnormalised fp32 rows, through this warp's staging 32 columns (128
+        // bytes a row) at a time, so that eight lanes store one row's line.
+        const int64_t base = static_cast<int64_t>(part) * a.T * a.H;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tmem_ld32(o_tmem + c * 32, ov);
+          tmem_wait_ld(ov);
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            *reinterpret_cast<uint4 *>(stg + lane * 128 + ((q ^ (lane & 7)) * 16)) =
+                make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const int rr = (lane >> 3) + 4 * q, ch = lane & 7;
+            const uint4 v =
+                *reinterpret_cast<const uint4 *>(stg + rr * 128 + ((ch ^ (rr & 7)) * 16));
+            const int out_row = __shfl_sync(~0u, my_out, rr);
+            if (out_row >= 0)
+              *reinterpret_cast<uint4 *>(a.ws_o + (base + out_row) * D + c * 32 + ch * 4) = v;
+          }
+          __syncwarp();
+        }
+        if (my_out >= 0) a.ws_ml[base + my_out] = make_float2(m, l);
+        continue;
+      }
+      const float inv_l = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
+        uint32_t ov[2][32];
+        // (Loaded for a tile without keys too, whose rows are set to zero below:
+        // a branch around the loads makes the compiler keep copies of them.)
+        tmem_ld32(o_tmem + 64 * h, ov[0]);
+        tmem_ld32(o_tmem + 64 * h + 32, ov[1]);
+        tmem_wait_ld(ov[0]);
+        tmem_wait_ld(ov[1]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t *c8 = &ov[q >> 2][(q & 3) * 8];
+          uint4 v;
+          v.x = pack2<F16>(__uint_as_float(c8[0]) * inv_l, __uint_as_float(c8[1]) * inv_l);
+          v.y = pack2<F16>(__uint_as_float(c8[2]) * inv_l, __uint_as_float(c8[3]) * inv_l);
+          v.z = pack2<F16>(__uint_as_float(c8[4]) * inv_l, __uint_as_float(c8[5]) * inv_l);
+          v.w = pack2<F16>(__uint_as_float(c8[6]) * inv_l, __uint_as_float(c8[7]) * inv_l);
+          // A row that saw no key is zero whatever its accumulator holds.
+          if (l == 0.f) v = make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4 *>(stg + lane * 128 + ((q ^ (lane & 7)) * 16)) = v;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int rr = (lane >> 3) + 4 * q, ch = lane & 7;
+          const uint4 v = *reinterpret_cast<const uint4 *>(stg + rr * 128 + ((ch ^ (rr & 7)) * 16));
+          const int out_row = __shfl_sync(~0u, my_out, rr);
+          if (out_row >= 0)
+            *reinterpret_cast<uint4 *>(a.o + static_cast<int64_t>(out_row) * D + 64 * h + ch * 8) =
+                v;
+        }
+        __syncwarp();
+      }
+      if (!PAGED && a.lse != nullptr && my_out >= 0)
+        a.lse[static_cast<int64_t>(my_out % a.H) * a.T + my_out / a.H] =
+            l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (threadIdx.x == 0) {
+    if (misc->abort) atomicExch(a.dev_status, kDevTimeout);
+    // The last CTA to finish returns the counters to zero for the next launch.
+    __threadfence();
+    if (atomicAdd(a.sched + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+      a.sched[0] = 0;
+      a.sched[1] = 0;
+      __threadfence();
+    }
+  }
+}
+
+// Joins the partitions of the rows whose tile was split: one warp per (token,
+// head), four dimensions a lane.
+__global__ void __launch_bounds__(256) paged_merge_kernel(const Args a) {
+  constexpr int D = kDecodeHeadSize;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= static_cast<int64_t>(a.T) * a.H) return;   // whole warps
+  const int tok = static_cast<int>(row / a.H);
+  // The sequence that owns the token: the last one that begins at or before it.
+  const int s = warp_search(a.S, tok, [&](int i) { return clampi(a.cu_seqlens[i], 0, a.T); });
+  if (s < 0) return;
+  const Seq q = sequence<true>(a, s);
+  const int i = tok - q.begin;
+  if (i >= q.n) return;                                  // rows behind the last sequence
+  const int u0 = i / a.tpb * a.tpb;                      // first token of its query tile
+  const int last = min(u0 + a.tpb, q.n) - 1;
+  if (tiles_for(1, q.pos + last, q.kv_len) <= a.part_tiles) return;   // written directly
+  const int mine = tiles_for(1, q.pos + i, q.kv_len);    // key tiles this row sees
+  const int parts = (mine + a.part_tiles - 1) / a.part_tiles;
+  const int64_t stride = static_cast<int64_t>(a.T) * a.H;
+  float m = -INFINITY;
+  for (int p = 0; p < parts; ++p) m = fmaxf(m, a.ws_ml[p * stride + row].x);
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (m != -INFINITY)
+    for (int p = 0; p < parts; ++p) {
+      const float2 ml = a.ws_ml[p * stride + row];
+      const float f = ex2_approx(ml.x - m);
+      const float4 v =
+          *reinterpret_cast<const float4 *>(a.ws_o + (p * stride + row) * D + lane * 4);
+      l = fmaf(f, ml.y, l);
+      o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
+      o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+    }
+  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+  uint2 w;
+  w.x = pack_bf16x2(o.x * inv, o.y * inv);
+  w.y = pack_bf16x2(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2 *>(a.o + row * D + lane * 4) = w;
+}
+
+cudaError_t sm_count(int *n) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, dev);
+  return e;
+}
+
+template <int D, bool F16, bool PAGED>
+cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, Args a,
+                   cudaStream_t stream) {
+  using C = Cfg<D>;
+  int sms = 0;
+  cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(fwd_packed_kernel<D, F16, PAGED>,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
+  if (e != cudaSuccess) return e;
+  const int64_t n_items = static_cast<int64_t>(a.n_vblocks) * a.n_split * a.Hk;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(n_items < sms ? n_items : sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kAlloc;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, fwd_packed_kernel<D, F16, PAGED>, tq, tk, tv, a);
+  if (e != cudaSuccess || !PAGED || a.n_split == 1) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.T) * a.H + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel, a);
+}
+
+Args args_of(const PackedProblem &p, int *sched, int *dev_status) {
+  Args a{};
+  a.o = static_cast<uint16_t *>(p.o);
+  a.lse = p.lse;
+  a.cu_seqlens = p.cu_seqlens;
+  a.context_lens = p.context_lens;
+  a.block_tables = p.block_tables;
+  a.sched = sched;
+  a.dev_status = dev_status;
+  a.S = p.S, a.T = p.T, a.H = p.H, a.Hk = p.Hk, a.G = p.H / p.Hk;
+  a.tpb = packed_tile_tokens(a.G);
+  a.max_blocks = p.max_blocks, a.num_blocks = p.num_blocks;
+  a.n_vblocks = packed_blocks(p.T, p.S, a.G);
+  a.n_split = 1, a.part_tiles = 0x7fffffff / BN;
+  a.causal = p.causal;
+  a.scale_log2 = p.scale * 1.4426950408889634f;
+  return a;
+}
+
+}  // namespace
+
+int packed_tile_tokens(int group) { return BM / group; }
+
+int packed_blocks(int T, int S, int group) { return T / (2 * packed_tile_tokens(group)) + S; }
+
+cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                              const PackedProblem &p, int d, bool f16, int *sched,
+                              int *dev_status, cudaStream_t stream) {
+  const Args a = args_of(p, sched, dev_status);
+  if (d == 64)
+    return f16 ? launch<64, true, false>(tq, tk, tv, a, stream)
+               : launch<64, false, false>(tq, tk, tv, a, stream);
+  return f16 ? launch<128, true, false>(tq, tk, tv, a, stream)
+             : launch<128, false, false>(tq, tk, tv, a, stream);
+}
+
+// Partitions of the context: enough items for about two rounds of the SMs, but
+// at least four key tiles (512 keys) each, below which a partition's fixed cost
+// (claim, Q, fp32 rows out and the merge) outweighs its keys.
+PagedSplit paged_split(int T, int S, int Hk, int group, int max_blocks) {
+  constexpr int kTargetItems = 2 * 152, kMinTiles = 4;
+  const int tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;
+  const int64_t items = static_cast<int64_t>(packed_blocks(T, S, group)) * Hk;
+  int n = static_cast<int>(items >= kTargetItems ? 1 : (kTargetItems + items - 1) / items);
+  const int most = tiles / kMinTiles > 1 ? tiles / kMinTiles : 1;
+  if (n > most) n = most;
+  PagedSplit s;
+  s.part_tiles = (tiles + n - 1) / n;
+  s.n_split = (tiles + s.part_tiles - 1) / s.part_tiles;
+  return s;
+}
+
+size_t paged_prefill_workspace_bytes(int T, int S, int H, int Hk, int max_blocks) {
+  const PagedSplit s = paged_split(T, S, Hk, H / Hk, max_blocks);
+  if (s.n_split == 1) return 0;
+  return static_cast<size_t>(s.n_split) * T * H * (kDecodeHeadSize + 2) * sizeof(float);
+}
+
+cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
+                                 const CUtensorMap &tv, const PackedProblem &p, float *workspace,
+                                 int *sched, int *dev_status, cudaStream_t stream) {
+  Args a = args_of(p, sched, dev_status);
+  const PagedSplit s = paged_split(p.T, p.S, p.Hk, a.G, p.max_blocks);
+  if (s.n_split > 1) {
+    a.n_split = s.n_split;
+    a.part_tiles = s.part_tiles;
+    a.ws_o = workspace;
+    a.ws_ml = reinterpret_cast<float2 *>(workspace + static_cast<size_t>(s.n_split) * p.T * p.H *
+                                                         kDecodeHeadSize);
+  }
+  return launch<128, false, true>(tq, tk, tv, a, stream);
+}
+
+}  // namespace fattn

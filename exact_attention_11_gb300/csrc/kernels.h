@@ -162,4 +162,32 @@ cudaError_t launch_qk_prep_grad(ElemType type, const QkPrep &p, const void *dq_o
                                 const void *dk_out, void *dq, void *dk, float *dqw, float *dkw,
                                 float *workspace, cudaStream_t stream);
 
+// Several queries per sequence, sequences of different lengths, grouped heads
+// (fwd_packed.cu).  tq: 3-D map {d, H, T} of the queries, boxes of 64 x G x
+// packed_tile_tokens(G); packed: tk, tv 3-D maps {d, T, Hk}, boxes of 64 x 128
+// x 1; paged: the views of encode_paged_kv_maps with the cache's block count.
+// 128-byte swizzle where not paged.  sched as for launch_fwd_bf16.
+struct PackedProblem {
+  void *o;
+  float *lse;                                   // [H][T], packed only, or null
+  const int *cu_seqlens, *context_lens, *block_tables;
+  int S, T, H, Hk, max_blocks, num_blocks, causal;
+  float scale;
+};
+int packed_tile_tokens(int group);              // tokens of a 128-row query tile
+int packed_blocks(int T, int S, int group);     // bound on the two-tile blocks of a call
+cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                              const PackedProblem &p, int d, bool f16, int *sched,
+                              int *dev_status, cudaStream_t stream);
+// Paged: how the context is cut into partitions, and the fp32 workspace that
+// they need (0 bytes when there is one).
+struct PagedSplit {
+  int n_split, part_tiles;                      // partitions, key tiles of each
+};
+PagedSplit paged_split(int T, int S, int Hk, int group, int max_blocks);
+size_t paged_prefill_workspace_bytes(int T, int S, int H, int Hk, int max_blocks);
+cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
+                                 const CUtensorMap &tv, const PackedProblem &p, float *workspace,
+                                 int *sched, int *dev_status, cudaStream_t stream);
+
 }  // namespace fattn

@@ -32,8 +32,8 @@
  * cudaFreeAsync), so a larger problem never synchronises the device; a call
  * being captured into a CUDA graph cannot grow them and returns
  * FA_ERR_UNSUPPORTED instead, so run one call of the largest size before
- * capturing.  The forward kernels, the backward's main kernel and the
- * tensor-core grouped decode take a pair of work counters per launch: eager launches rotate through 64 pairs,
+ * capturing.  The forward kernels (fa_paged_prefill among them), the
+ * backward's main kernel and the tensor-core grouped decode take a pair of work counters per launch: eager launches rotate through 64 pairs,
  * launches captured into a graph through 64 others that a graph keeps for
  * every replay; so at most 64 eager calls may be in flight on a device at
  * once, and a graph must not run concurrently with itself.
@@ -483,6 +483,83 @@ int fa_qk_norm_rope_backward_fp32(const void *dq_out, const void *dk_out, const 
                                   int interleaved, long long q_stride, long long k_stride,
                                   float eps, float mscale, void *workspace,
                                   unsigned long long workspace_bytes, fa_stream_t stream);
+
+/*
+ * fa_forward_packed -- fa_forward for prompts of different lengths packed one
+ * after another, with grouped key/value heads.
+ *
+ * Sequence s owns rows (tokens) cu_seqlens[s] .. cu_seqlens[s+1] - 1 of q, k, v
+ * and o; every query attends to the keys of its own sequence: all of them, or
+ * those up to its own position when causal != 0.  Query head h uses key/value
+ * head h / (num_heads / num_kv_heads).
+ *
+ *   q             bf16 [total_tokens, num_heads, d], k and v bf16
+ *                 [total_tokens, num_kv_heads, d]; heads dense, consecutive
+ *                 tokens q_stride, k_stride, v_stride elements apart (multiples
+ *                 of 8; a slice of a fused projection has its own stride).
+ *   o             bf16 [total_tokens, num_heads, d], dense, written.
+ *   lse           fp32 [num_heads, total_tokens], written; may be NULL.
+ *   cu_seqlens    int32 [num_seqs + 1] on the device, non-decreasing, from >= 0
+ *                 to <= total_tokens.  Sequences may be empty.  Rows that belong
+ *                 to no sequence -- before cu_seqlens[0], behind
+ *                 cu_seqlens[num_seqs] -- may hold any bits; o and lse are left
+ *                 as they were there.  (Values are clamped into the tensor; if
+ *                 they decrease, what is computed is not specified, but nothing
+ *                 outside the tensors is read or written.)
+ *   num_heads     a multiple of num_kv_heads, at most 128 times it.
+ *   d             64 or 128 (else FA_ERR_UNSUPPORTED).
+ * One sequence's NaN or Inf does not reach another's rows.  Rounding, scale,
+ * alignment and errors as for fa_forward; num_seqs or total_tokens equal to 0
+ * does nothing.
+ * fa_forward_packed_f16: the same with fp16 q, k, v and o (as fa_forward_f16).
+ */
+int fa_forward_packed(const void *q, const void *k, const void *v, void *o, float *lse,
+                      const int *cu_seqlens, int num_seqs, int total_tokens, int num_heads,
+                      int num_kv_heads, int d, long long q_stride, long long k_stride,
+                      long long v_stride, float scale, int causal, fa_stream_t stream);
+int fa_forward_packed_f16(const void *q, const void *k, const void *v, void *o, float *lse,
+                          const int *cu_seqlens, int num_seqs, int total_tokens, int num_heads,
+                          int num_kv_heads, int d, long long q_stride, long long k_stride,
+                          long long v_stride, float scale, int causal, fa_stream_t stream);
+
+/*
+ * fa_paged_prefill -- attention of a chunk of new tokens per sequence over a
+ * paged KV cache that holds the sequence's whole context, the chunk's own keys
+ * and values included (fa_qk_norm_rope_cache writes them).  Chunks may have any
+ * length: whole prompts, pieces of long ones, a few drafted tokens, one token.
+ *
+ * Sequence s has n = cu_seqlens[s+1] - cu_seqlens[s] new queries (rows
+ * cu_seqlens[s] .. of q and out) and ctx = context_lens[s] cached tokens;
+ * its query i sees cached tokens 0 .. ctx - n + i.  A query that sees none
+ * (ctx < n) gets a zero row.
+ *
+ *   q             bf16 [total_tokens, num_heads, head_size], heads dense, tokens
+ *                 q_stride elements apart (a multiple of 8).
+ *   k_cache, v_cache, block_tables, context_lens, head_size, block_size, scale
+ *                 as for fa_paged_decode_gqa; num_blocks is the caches' first
+ *                 extent.  Table entries outside [0, num_blocks) read as zero
+ *                 keys and values; context lengths are clamped to
+ *                 [0, max_num_blocks_per_seq * block_size].
+ *   cu_seqlens    as for fa_forward_packed; sequences may have no new tokens.
+ *   out           bf16 [total_tokens, num_heads, head_size], dense, written for
+ *                 the sequences' rows.
+ *   workspace     device memory of at least fa_paged_prefill_workspace_bytes
+ *                 bytes (0: may be NULL), 16-byte aligned, scratch during the
+ *                 call; calls that may run at the same time need separate ones.
+ *                 It holds the partial rows of long contexts that are cut into
+ *                 partitions when the chunks alone do not fill the GPU.
+ *   num_heads     a multiple of num_kv_heads, at most 128 times it.
+ * Cache slots past a context may hold any bits.  Results are the same from call
+ * to call, bit for bit.  num_seqs or total_tokens equal to 0 does nothing.
+ */
+unsigned long long fa_paged_prefill_workspace_bytes(int num_seqs, int total_tokens, int num_heads,
+                                                    int num_kv_heads, int max_num_blocks_per_seq);
+int fa_paged_prefill(const void *q, const void *k_cache, const void *v_cache,
+                     const int *block_tables, const int *context_lens, const int *cu_seqlens,
+                     void *out, int num_seqs, int total_tokens, int num_heads, int num_kv_heads,
+                     int head_size, int block_size, int num_blocks, int max_num_blocks_per_seq,
+                     long long q_stride, float scale, void *workspace,
+                     unsigned long long workspace_bytes, fa_stream_t stream);
 
 /*
  * fa_debug_inject_fault -- test hook for the device-side failure path.

@@ -1,0 +1,222 @@
+"""Packed prompts of different lengths with grouped heads against float64.
+Tolerances: packed_ref.check_forward."""
+import pytest
+import torch
+
+import exact_attention_11_gb300 as fa
+import packed_ref as ref
+import qk_prep_ref
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+BF16, F16 = torch.bfloat16, torch.float16
+
+
+def draw(lens, H, Hk, d, dtype, seed, before=0, behind=0, fill=float("nan")):
+    """Views of one fused projection and cu_seqlens; `before` and `behind`
+    rows of no sequence hold `fill`."""
+    T = before + sum(lens) + behind
+    g = torch.Generator().manual_seed(seed)
+    qkv = torch.randn(T, H + 2 * Hk, d, generator=g)
+    qkv[:before] = fill
+    qkv[T - behind:] = fill
+    qkv = qkv.to(dtype).to(DEV)
+    cu = torch.tensor([before] + lens).cumsum(0).int().to(DEV)
+    return qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:], cu
+
+
+def check(q, k, v, cu, o, lse, causal, scale=None):
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0
+    scale = scale or q.shape[-1] ** -0.5
+    cu = cu.tolist()
+    for a, b in zip(cu, cu[1:]):
+        if a == b:
+            continue
+        n = b - a
+        last = torch.arange(n, device=DEV) if causal else torch.full((n,), n, device=DEV)
+        r = ref.sequence(q[a:b], k[a:b], v[a:b], scale, last)
+        ref.check_forward(o[a:b], None if lse is None else lse[:, a:b], r, scale, q.dtype)
+
+
+def run(lens, H, Hk, d, dtype, causal, seed, **kw):
+    q, k, v, cu = draw(lens, H, Hk, d, dtype, seed, **kw)
+    o, lse = fa.forward_packed(q, k, v, cu, causal=causal)
+    check(q, k, v, cu, o, lse, causal)
+
+
+HEADS = [(1, 1), (8, 2), (6, 2), (7, 1), (10, 2), (16, 1), (40, 1), (128, 1)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hk", HEADS)
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+def test_heads(H, Hk, d, causal):
+    """Group sizes that divide 128 and that do not; lengths at the tiles'
+    edges, one token, an empty sequence."""
+    run([1, 130, 0, 64, 33], H, Hk, d, BF16, causal, seed=H + d)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+@pytest.mark.parametrize("lens", [[1], [128], [129], [255, 256, 257], [2, 1, 1, 3], [0, 5, 0, 0],
+                                  [700, 31, 1100]], ids=str)
+def test_lengths(lens, d, dtype, causal):
+    run(lens, 4, 2, d, dtype, causal, seed=sum(lens))
+
+
+def test_every_length_up_to_three_tiles():
+    """One sequence of each length 1 .. 270 (one head), causal and not."""
+    for causal in (True, False):
+        run(list(range(1, 271)), 1, 1, 64, BF16, causal, seed=5)
+
+
+@pytest.mark.parametrize("S", [31, 32, 33, 1023, 1025, 2100])
+def test_many_sequences(S):
+    """The 32-way search at one, two and three rounds."""
+    g = torch.Generator().manual_seed(S)
+    lens = torch.randint(0, 9, (S,), generator=g).tolist()
+    run(lens, 2, 1, 64, BF16, True, seed=S)
+
+
+@pytest.mark.parametrize("H,Hk,d", [(8, 2, 128), (12, 4, 64)])
+def test_many_items_per_sm(H, Hk, d):
+    """Several work items per persistent CTA, light and heavy ones mixed."""
+    run([3000, 1, 257, 2049, 640, 5, 1500], H, Hk, d, BF16, True, seed=9)
+    run([1200, 77, 900], H, Hk, d, F16, False, seed=10)
+
+
+def test_rows_of_no_sequence_stay_and_do_not_leak():
+    """NaN before the first and behind the last sequence: neither read into a
+    sequence nor written."""
+    for d in (64, 128):
+        q, k, v, cu = draw([100, 45], 4, 2, d, BF16, seed=3, before=37, behind=200)
+        o = torch.full(q.shape, 7.0, dtype=BF16, device=DEV)
+        lse = torch.full((4, q.shape[0]), 7.0, device=DEV)
+        fa.forward_packed(q, k, v, cu, out=o, lse=lse)
+        check(q, k, v, cu, o, lse, True)
+        for rows in (slice(0, 37), slice(182, None)):
+            assert (o[rows] == 7).all() and (lse[:, rows] == 7).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_sequences_do_not_mix(bad):
+    """A sequence of NaN or Inf leaves its neighbours' bits alone."""
+    q, k, v, cu = draw([70, 33, 150], 4, 4, 64, BF16, seed=4)
+    o, lse = fa.forward_packed(q, k, v, cu, causal=False)
+    for x in (q, k, v):
+        x[70:103] = bad
+    o2, lse2 = fa.forward_packed(q, k, v, cu, causal=False)
+    for rows in (slice(0, 70), slice(103, 253)):
+        assert torch.equal(o[rows], o2[rows]) and torch.equal(lse[:, rows], lse2[:, rows])
+
+
+def test_scores_of_large_size():
+    """Scores of magnitude 10^3: a running maximum that keeps growing."""
+    q, k, v, cu = draw([300, 20], 2, 1, 128, BF16, seed=6)
+    q, k = q * 8, k * 8
+    k[:300] *= torch.linspace(0.1, 1.0, 300, device=DEV)[:, None, None].to(BF16)
+    o, lse = fa.forward_packed(q, k, v, cu, scale=0.5)
+    check(q, k, v, cu, o, lse, True, scale=0.5)
+
+
+def test_matches_the_dense_forward():
+    """Sequences of one length: fa_forward's own result (same tiles, other
+    rows to a tile), to two roundings."""
+    B, H, N, d = 3, 4, 384, 128
+    g = torch.Generator().manual_seed(8)
+    q, k, v = (torch.randn(B, H, N, d, generator=g).to(BF16).to(DEV) for _ in range(3))
+    o, lse = fa.forward(q, k, v, causal=True)
+    pack = lambda x: x.transpose(1, 2).reshape(B * N, H, d).contiguous()  # noqa: E731
+    cu = torch.arange(B + 1, device=DEV).int() * N
+    o2, lse2 = fa.forward_packed(pack(q), pack(k), pack(v), cu.int())
+    assert (pack(o).float() - o2.float()).abs().max() <= 2e-2
+    assert (lse.transpose(0, 1).reshape(H, B * N) - lse2).abs().max() <= 1e-5
+
+
+def test_without_lse_and_empty():
+    q, k, v, cu = draw([40], 2, 1, 64, BF16, seed=1)
+    o, lse = fa.forward_packed(q, k, v, cu, want_lse=False)
+    check(q, k, v, cu, o, None, True)
+    assert lse is None
+    empty = torch.zeros(0, 2, 64, dtype=BF16, device=DEV)
+    o, lse = fa.forward_packed(empty, empty, empty, torch.zeros(4, dtype=torch.int32, device=DEV))
+    assert o.shape == (0, 2, 64) and lse.shape == (2, 0)
+    # no sequence owns any row: nothing is written
+    o = torch.full((40, 2, 64), 3.0, dtype=BF16, device=DEV)
+    fa.forward_packed(q, k, v, torch.zeros(1, dtype=torch.int32, device=DEV), out=o)
+    fa.forward_packed(q, k, v, torch.full((5,), 40, dtype=torch.int32, device=DEV), out=o)
+    assert (o == 3).all()
+
+
+def test_offsets_outside_the_tensor_are_clamped():
+    """Offsets past the tensor are taken as its end, negative ones as its start."""
+    q, k, v, cu = draw([40, 24], 2, 1, 64, BF16, seed=2)
+    want, _ = fa.forward_packed(q, k, v, cu)
+    got, _ = fa.forward_packed(q, k, v, torch.tensor([-5, 40, 1 << 30], device=DEV).int())
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0 and torch.equal(want, got)
+
+
+def test_captured_and_concurrent_calls():
+    """A graph replayed on new inputs, and two calls on two streams."""
+    q, k, v, cu = draw([300, 41, 7], 8, 2, 128, BF16, seed=11)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        o, lse = fa.forward_packed(q, k, v, cu)
+    for seed in (12, 13):
+        q2, k2, v2, _ = draw([300, 41, 7], 8, 2, 128, BF16, seed)
+        for x, y in ((q, q2), (k, k2), (v, v2)):
+            x.copy_(y)
+        cu.copy_(torch.tensor([0, 100 + seed, 200, 348]))
+        graph.replay()
+        torch.cuda.synchronize()
+        want, want_lse = fa.forward_packed(q, k, v, cu)
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    for i in range(20):
+        with torch.cuda.stream(streams[i & 1]):
+            outs.append(fa.forward_packed(q, k, v, cu)[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in outs)
+
+
+def test_helper_refuses():
+    q, k, v, cu = draw([40], 4, 2, 64, BF16, seed=1)
+    bad = [
+        lambda: fa.forward_packed(q.float(), k.float(), v.float(), cu),
+        lambda: fa.forward_packed(q, k[:20], v, cu),
+        lambda: fa.forward_packed(q, k, v[:, :1], cu),
+        lambda: fa.forward_packed(q, k, v.half(), cu),
+        lambda: fa.forward_packed(q, k, v, cu.long()),
+        lambda: fa.forward_packed(q, k, v, cu.cpu()),
+        lambda: fa.forward_packed(q, k, v, cu[:0]),
+        lambda: fa.forward_packed(q[:, ::2], k, v, cu),
+        lambda: fa.forward_packed(q, k, v, cu, out=torch.empty_like(q)[:20]),
+    ]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    for H, Hk, d in ((3, 2, 64), (2, 2, 256), (129, 1, 64)):
+        q, k, v, cu = draw([4], H, Hk, d, BF16, seed=1)
+        with pytest.raises(fa.FattnError):
+            fa.forward_packed(q, k, v, cu)
+
+
+def test_after_norm_and_rotation():
+    """A layer's front half: norm, rotation, packed attention; against the
+    same in float64 from the rounded queries and keys of the first step."""
+    lens, H, Hk, d = [50, 3, 200], 8, 2, 128
+    q, k, v, cu = draw(lens, H, Hk, d, BF16, seed=14)
+    pos = torch.cat([torch.arange(n) for n in lens]).int().to(DEV)
+    g = torch.Generator().manual_seed(15)
+    qw, kw = ((1 + 0.1 * torch.randn(d, generator=g)).to(BF16).to(DEV) for _ in range(2))
+    freq, _ = fa.rope_frequencies(d, device=DEV)
+    qr, kr = fa.qk_norm_rope(q, k, pos, freq, qw, kw)
+    want, size = qk_prep_ref.forward(q.cpu(), qw.cpu(), pos.cpu(), freq.cpu(), 1e-6, False, 1.0)
+    assert ((qr.cpu().double() - want).abs() <= qk_prep_ref.bound(want, size, BF16)).all()
+    o, lse = fa.forward_packed(qr, kr, v, cu)
+    check(qr, kr, v, cu, o, lse, True)
