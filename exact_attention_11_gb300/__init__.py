@@ -27,7 +27,8 @@ __all__ = ["fa_forward", "fa_forward_f16", "fa_forward_masked", "forward_masked"
            "fa_qk_norm_rope_backward", "fa_qk_norm_rope_backward_f16",
            "fa_qk_norm_rope_backward_fp32", "rope_frequencies", "qk_norm_rope",
            "qk_norm_rope_cache", "qk_norm_rope_backward", "fa_forward_packed",
-           "fa_forward_packed_f16", "forward_packed", "fa_paged_prefill",
+           "fa_forward_packed_f16", "forward_packed", "fa_backward_packed",
+           "fa_backward_packed_workspace_bytes", "backward_packed", "fa_paged_prefill",
            "fa_paged_prefill_workspace_bytes", "paged_prefill",
            "fa_device_status", "fa_release", "forward", "paged_decode", "FattnError",
            "library_path", "load"]
@@ -84,6 +85,9 @@ EXPORTS = {
     "fa_qk_norm_rope_backward_fp32": (_PREP_BWD, _i),
     "fa_forward_packed": ([_vp] * 6 + [_i] * 5 + [_ll] * 3 + [_f, _i, _vp], _i),
     "fa_forward_packed_f16": ([_vp] * 6 + [_i] * 5 + [_ll] * 3 + [_f, _i, _vp], _i),
+    "fa_backward_packed_workspace_bytes": ([_i] * 5, ctypes.c_ulonglong),
+    "fa_backward_packed": ([_vp] * 10 + [_i] * 5 + [_ll] * 3 + [_f, _i, _vp, ctypes.c_ulonglong,
+                                                               _vp], _i),
     "fa_paged_prefill_workspace_bytes": ([_i] * 5, ctypes.c_ulonglong),
     "fa_paged_prefill": ([_vp] * 7 + [_i] * 8 + [_ll, _f, _vp, ctypes.c_ulonglong, _vp], _i),
     "fa_status_string": ([_i], ctypes.c_char_p),
@@ -262,6 +266,20 @@ def fa_forward_packed_f16(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, n
     return _check("fa_forward_packed_f16", load().fa_forward_packed_f16(
         q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads, num_kv_heads, d, q_stride,
         k_stride, v_stride, scale, int(causal), stream))
+
+
+def fa_backward_packed_workspace_bytes(num_seqs, total_tokens, num_heads, num_kv_heads, d) -> int:
+    return int(load().fa_backward_packed_workspace_bytes(num_seqs, total_tokens, num_heads,
+                                                         num_kv_heads, d))
+
+
+def fa_backward_packed(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, num_seqs, total_tokens,
+                       num_heads, num_kv_heads, d, q_stride, k_stride, v_stride, scale, causal,
+                       workspace, workspace_bytes, stream) -> int:
+    return _check("fa_backward_packed", load().fa_backward_packed(
+        q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, num_seqs, total_tokens, num_heads,
+        num_kv_heads, d, q_stride, k_stride, v_stride, scale, int(causal), workspace,
+        workspace_bytes, stream))
 
 
 def fa_paged_prefill_workspace_bytes(num_seqs, total_tokens, num_heads, num_kv_heads,
@@ -730,6 +748,43 @@ def forward_packed(q, k, v, cu_seqlens, scale=None, causal=True, out=None, lse=N
         _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens),
         cu_seqlens.numel() - 1, T, H, k.shape[1], d, qs, ks, vs, scale, int(causal), _stream(q)))
     return out, lse
+
+
+@_on_device
+def backward_packed(q, k, v, o, lse, dout, cu_seqlens, scale=None, causal=True, workspace=None):
+    """Gradients (dQ [T,H,d], dK [T,Hk,d], dV [T,Hk,d]) of the bf16
+    ``forward_packed``; ``o`` and ``lse`` are what it returned for the same q, k,
+    v, cu_seqlens, scale and causal, ``dout`` [T,H,d] is dense.  ``workspace``
+    (optional) is a CUDA tensor of at least
+    ``fa_backward_packed_workspace_bytes`` bytes.  Rows of no sequence are not
+    written.  Runs on the current torch stream."""
+    import torch
+    qs, ks, vs = _packed_args(q, k, v, cu_seqlens)
+    if q.dtype != torch.bfloat16:
+        raise ValueError("q, k, v must be bf16")
+    T, H, d = q.shape
+    Hk = k.shape[1]
+    if o.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("o and dout must have q's shape")
+    _vector("o", o, q.dtype, q)
+    _vector("dout", dout, q.dtype, q)
+    _vector("lse", lse, torch.float32, q, H * T)
+    if scale is None:
+        scale = d ** -0.5
+    dq = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+    dk, dv = (torch.empty((T, Hk, d), dtype=q.dtype, device=q.device) for _ in range(2))
+    S = cu_seqlens.numel() - 1
+    if T == 0 or S == 0:
+        return dq, dk, dv
+    lib = load()
+    if workspace is None:
+        nbytes = lib.fa_backward_packed_workspace_bytes(S, T, H, Hk, d)
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+    _check("fa_backward_packed", lib.fa_backward_packed(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+        _ptr(cu_seqlens), S, T, H, Hk, d, qs, ks, vs, scale, int(causal), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(q)))
+    return dq, dk, dv
 
 
 @_on_device

@@ -858,6 +858,59 @@ int fa_forward_packed_f16(const void *q, const void *k, const void *v, void *o, 
                         true);
 }
 
+unsigned long long fa_backward_packed_workspace_bytes(int num_seqs, int total_tokens,
+                                                      int num_heads, int num_kv_heads, int d) {
+  if (num_seqs <= 0 || total_tokens <= 0 || d <= 0) return 0;
+  if (check_packed_sizes(num_seqs, total_tokens, num_heads, num_kv_heads) != FA_OK) return 0;
+  return static_cast<unsigned long long>(
+      fattn::packed_grad_layout(total_tokens, num_seqs, num_heads, num_kv_heads, d).bytes);
+}
+
+int fa_backward_packed(const void *q, const void *k, const void *v, const void *o,
+                       const void *dout, const float *lse, void *dq, void *dk, void *dv,
+                       const int *cu_seqlens, int num_seqs, int total_tokens, int num_heads,
+                       int num_kv_heads, int d, long long q_stride, long long k_stride,
+                       long long v_stride, float scale, int causal, void *workspace,
+                       unsigned long long workspace_bytes, fa_stream_t stream) {
+  if (!dout || !lse || !dq || !dk || !dv) return FA_ERR_INVALID_ARG;
+  const int S = num_seqs, T = total_tokens, H = num_heads, Hk = num_kv_heads;
+  int rc = check_packed(q, k, v, o, lse, cu_seqlens, S, T, H, Hk, d, q_stride, k_stride, v_stride,
+                        scale);
+  if (rc != FA_OK) return rc;
+  if (!aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return FA_ERR_ALIGNMENT;
+  if (S == 0 || T == 0) return FA_OK;
+  // Padded rows and the items (block, head) are 32-bit.
+  if (((long long)T / 128 + S) * 128 > (1 << 30) ||
+      ((long long)T / 128 + S) * (H + Hk) > 0x3fffffffLL)
+    return FA_ERR_UNSUPPORTED;
+  const fattn::PackedGradLayout l = fattn::packed_grad_layout(T, S, H, Hk, d);
+  if (!workspace || workspace_bytes < l.bytes) return FA_ERR_INVALID_ARG;
+  if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int *sched = nullptr, *status = nullptr;
+  if ((rc = acquire_sched(s, &sched, &status)) != FA_OK) return rc;
+  const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int box = fattn::bwd_qdo_box_rows(d), rows = l.n_blocks * 128;
+  float *ws = static_cast<float *>(workspace);
+  fattn::PackedGradMaps m;
+  if ((rc = encode_rows_map(&m.q, q, T, H, d, q_stride, true, box, 1, dt)) != FA_OK) return rc;
+  if ((rc = encode_rows_map(&m.dout, dout, T, H, d, (long long)H * d, true, box, 1, dt)) != FA_OK)
+    return rc;
+  if ((rc = encode_rows_map(&m.k, k, T, Hk, d, k_stride, true, 128, 1, dt)) != FA_OK) return rc;
+  if ((rc = encode_rows_map(&m.v, v, T, Hk, d, v_stride, true, 128, 1, dt)) != FA_OK) return rc;
+  if ((rc = encode_dq_acc_map(&m.dq_acc, ws, H, rows, d)) != FA_OK) return rc;
+  m.dk_acc = m.dv_acc = m.dq_acc;
+  if (H != Hk) {
+    if ((rc = encode_dq_acc_map(&m.dk_acc, ws + l.dk_acc, Hk, rows, d)) != FA_OK) return rc;
+    if ((rc = encode_dq_acc_map(&m.dv_acc, ws + l.dv_acc, Hk, rows, d)) != FA_OK) return rc;
+  }
+  fattn::PackedGrad p{};
+  p.o = o, p.dout = dout, p.lse = lse, p.dq = dq, p.dk = dk, p.dv = dv, p.cu_seqlens = cu_seqlens;
+  p.S = S, p.T = T, p.H = H, p.Hk = Hk, p.d = d, p.causal = causal ? 1 : 0, p.scale = scale;
+  return cuda_status(fattn::launch_bwd_packed(m, p, ws, sched, status, s));
+}
+
 unsigned long long fa_paged_prefill_workspace_bytes(int num_seqs, int total_tokens, int num_heads,
                                                     int num_kv_heads,
                                                     int max_num_blocks_per_seq) {

@@ -37,6 +37,20 @@
 // does: every barrier keeps counting across items, the next item's Q, dO and
 // K, V loads and first S, dP overlap the current item's dV, dK epilogue, and
 // its first dV, dK products wait only for that epilogue's TMEM read-out.
+//
+// PACKED (fa_backward_packed): sequences of different lengths one after
+// another, grouped key/value heads.  An item is (key block of a sequence, query
+// head), found in the table that the preparation kernel wrote; inside it, key
+// and query indices count from the sequence's start, and only the TMA
+// coordinates and output rows add the sequence's place.  A tile that the
+// sequence ends in also holds the next one's rows: a warp of the producer
+// warpgroup clears them in shared memory (K, V, Q and dO: a zero weight does not
+// cancel a NaN) before the MMA warp may use the tile.  The dQ accumulator is
+// padded to whole blocks per sequence, so that no tile's rows fall on another
+// sequence's.  The query heads of a group are items of their own, as a group
+// would make the causal kernel's heaviest items too long to balance; they add
+// their dK, dV to fp32 accumulators with TMA reduces, or, with one query head
+// per key/value head, store them as the dense kernel does.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -79,6 +93,8 @@ constexpr int kOffBar = kOffVec + kSlots * kVecBytes;
 constexpr int kSmemBytes = kOffBar + 512;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 
+constexpr int kRowBoxes = D / 64;                     // 128-byte boxes per row
+
 enum : int {
   kBarKV = 0,
   kBarQFull = 1,        // + slot
@@ -94,17 +110,21 @@ enum : int {
   kBarEpiDone = 27,     // 8 warps: the item's dV, dK have been read out of TMEM
   kBarItemFull = 28,    // + ring slot (2)
   kBarItemEmpty = 30,   // + ring slot (2)
-  kNumBars = 32
+  kBarFix = 32,         // + slot, PACKED: a ragged half of Q and dO has been cleared
+  kBarKVFix = 36,       // PACKED: a ragged key block has been cleared
+  kNumBars = 38         // even: Misc, which follows, holds 16-byte values
 };
-// Arrivals that free an item-ring slot: the MMA thread and the 8 group warps.
+// Arrivals that free an item-ring slot: the MMA thread and the 8 group warps
+// (PACKED: and the clearing warp).
 constexpr int kItemConsumers = 1 + 8;
 
 struct Misc {
   uint32_t tmem_base;
   int abort;
   int item[2];
+  int4 seq[2];          // PACKED: the item's entry of the block table
 };
-static_assert(kNumBars * 8 + sizeof(Misc) <= 512, "barrier area");
+static_assert(kNumBars * 8 + sizeof(Misc) <= 512 && kNumBars % 2 == 0, "barrier area");
 
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t ph, volatile int *abort_flag) {
   return __all_sync(~0u, mbar_wait(bar, ph, abort_flag));
@@ -121,12 +141,31 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t ph) {
 constexpr int kDevBadSmemBase = -2;
 
 // An item: key block jb of head bh (items heaviest first: under the causal
-// mask key block 0 is visited by every query block).
+// mask key block 0 is visited by every query block).  Indices of keys and
+// queries count from the sequence's first row, which is row0 of the tensors
+// (PACKED; else 0); N is its length.
 struct BwdItem {
-  int jb, bh, k0, i_first, n_steps, n_halves;
-  __device__ void decode(int w, int BH, int n_qb, int causal) {
+  int jb, bh, k0, i_first, n_steps, n_halves, N;
+  int kvh, row0, blk0;   // PACKED: key/value head, first row, first padded block
+  __device__ void decode(int w, int BH, int n_qb, int causal, int N_) {
     jb = w / BH;
-    bh = w - jb * BH;
+    bh = kvh = w - jb * BH;
+    N = N_;
+    row0 = blk0 = 0;
+    steps(n_qb, causal);
+  }
+  // Entry e = (first row, length, first padded block, -) of padded block w / H.
+  __device__ void decode_packed(int w, const int4 &e, int H, int G, int causal) {
+    const int blk = w / H;
+    bh = w - blk * H;
+    kvh = bh / G;
+    row0 = e.x;
+    N = e.y;
+    blk0 = e.z;
+    jb = blk - blk0;
+    steps((N + BQ - 1) / BQ, causal);
+  }
+  __device__ void steps(int n_qb, int causal) {
     k0 = jb * BM;
     i_first = causal ? jb : 0;
     n_steps = n_qb - i_first;
@@ -134,6 +173,7 @@ struct BwdItem {
   }
 };
 
+template <bool PACKED>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_pipe64_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
@@ -142,7 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                       const __grid_constant__ CUtensorMap tm_dq, const float *__restrict__ vecs,
                       __nv_bfloat16 *__restrict__ dk, __nv_bfloat16 *__restrict__ dv, int N,
                       int BH, float scale, int causal, int *__restrict__ sched, int fault_cta,
-                      int *__restrict__ dev_status) {
+                      int *__restrict__ dev_status, const __grid_constant__ CUtensorMap tm_dk,
+                      const __grid_constant__ CUtensorMap tm_dv, const BwdPacked pk) {
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t s_base = smem_u32(smem);
   if ((s_base & 1023u) != 0) {
@@ -153,7 +194,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return bars + 8u * i; };
   Misc *misc = reinterpret_cast<Misc *>(smem + kOffBar + 8 * kNumBars);
   volatile int *abort_flag = &misc->abort;
-  const int n_qb = (N + BQ - 1) / BQ;
+  // PACKED: BH is the number of query heads; vecs and the accumulators count
+  // padded blocks.
+  const int n_qb = PACKED ? pk.n_blocks : (N + BQ - 1) / BQ;
   const int n_items = n_qb * BH;
 
   const int warp = threadIdx.x >> 5;
@@ -161,9 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(kBarKV), 1);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(bar(kBarQFull + s), 1);
-      mbar_init(bar(kBarQEmpty + s), 1);
+      mbar_init(bar(kBarQEmpty + s), PACKED ? 2 : 1);   // PACKED: and the clearing warp
       mbar_init(bar(kBarDOFull + s), 1);
-      mbar_init(bar(kBarDOEmpty + s), 1);
+      mbar_init(bar(kBarDOEmpty + s), PACKED ? 2 : 1);
+      if (PACKED) mbar_init(bar(kBarFix + s), 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(bar(kBarSFull + t), 1);
@@ -171,9 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBarDQFull + t), 1);
       mbar_init(bar(kBarDQFree + t), 8);
       mbar_init(bar(kBarItemFull + t), 1);
-      mbar_init(bar(kBarItemEmpty + t), kItemConsumers);
+      mbar_init(bar(kBarItemEmpty + t), kItemConsumers + (PACKED ? 1 : 0));
     }
-    mbar_init(bar(kBarKVDone), 1);
+    if (PACKED) mbar_init(bar(kBarKVFix), 1);
+    mbar_init(bar(kBarKVDone), PACKED ? 2 : 1);
     mbar_init(bar(kBarDrain), 1);
     mbar_init(bar(kBarEpiDone), 8);
     misc->abort = 0;
@@ -195,10 +240,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Consumer side of the item ring: waits for entry k and frees it (one
   // arrival per warp, or the lone MMA thread).
-  auto fetch_item = [&](int k, int &w, bool whole_warp) -> bool {
+  auto fetch_item = [&](int k, int &w, BwdItem &it, bool whole_warp) -> bool {
     const int slot = k & 1;
     if (!mbar_wait(bar(kBarItemFull + slot), (k >> 1) & 1, abort_flag)) return false;
     w = *reinterpret_cast<volatile int *>(&misc->item[slot]);
+    if (PACKED) {
+      const volatile int *e = reinterpret_cast<const volatile int *>(&misc->seq[slot]);
+      it.decode_packed(w, make_int4(e[0], e[1], e[2], 0), BH, pk.group, causal);
+    } else {
+      it.decode(w, BH, n_qb, causal, N);
+    }
     if (whole_warp) __syncwarp();
     if (!whole_warp || (threadIdx.x & 31) == 0) mbar_arrive(bar(kBarItemEmpty + slot));
     return true;
@@ -217,12 +268,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; ok; ++k) {
         const int islot = k & 1;
         if (!(ok = mbar_wait(bar(kBarItemEmpty + islot), ((k >> 1) & 1) ^ 1, abort_flag))) break;
-        const int w = atomicAdd(sched, 1);
+        int w = atomicAdd(sched, 1);
+        int4 entry = make_int4(0, 0, 0, 0);
+        if (PACKED) {
+          // A padded block that no sequence owns has no keys.
+          while (w < n_items && (entry = pk.table[w / BH]).y == 0) w = atomicAdd(sched, 1);
+          misc->seq[islot] = entry;
+        }
         misc->item[islot] = w;
         mbar_arrive(bar(kBarItemFull + islot));
         if (w >= n_items) break;
         BwdItem it;
-        it.decode(w, BH, n_qb, causal);
+        if (PACKED)
+          it.decode_packed(w, entry, BH, pk.group, causal);
+        else
+          it.decode(w, BH, n_qb, causal, N);
         const int h_base = nq;
         // Q / dO half h of the item (with its [LSE2 | D] vectors on QFull).
         auto load_half = [&](int h) -> bool {
@@ -231,16 +291,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int qrow = qb * BQ + (h & 1) * BH_;
           if (!mbar_wait(bar(kBarQEmpty + slot), (use & 1) ^ 1, abort_flag)) return false;
           mbar_arrive_expect_tx(bar(kBarQFull + slot), kHalf + kVecBytes);
-          tma_load_3d(s_base + kOffQ + slot * kHalf, &tm_q, 0, qrow, it.bh, bar(kBarQFull + slot));
+          tma_load_3d(s_base + kOffQ + slot * kHalf, &tm_q, 0, it.row0 + qrow, it.bh, bar(kBarQFull + slot));
           const float *vsrc =
-              vecs + (static_cast<int64_t>(it.bh) * n_qb + qb) * (2 * BQ) + (h & 1) * BH_;
+              vecs + (static_cast<int64_t>(it.bh) * n_qb + it.blk0 + qb) * (2 * BQ) + (h & 1) * BH_;
           bulk_load(s_base + kOffVec + slot * kVecBytes, vsrc, BH_ * 4, bar(kBarQFull + slot));
           bulk_load(s_base + kOffVec + slot * kVecBytes + BH_ * 4, vsrc + BQ, BH_ * 4,
                     bar(kBarQFull + slot));
           nq = g + 1;
           if (!mbar_wait(bar(kBarDOEmpty + slot), (use & 1) ^ 1, abort_flag)) return false;
           mbar_arrive_expect_tx(bar(kBarDOFull + slot), kHalf);
-          tma_load_3d(s_base + kOffDO + slot * kHalf, &tm_do, 0, qrow, it.bh,
+          tma_load_3d(s_base + kOffDO + slot * kHalf, &tm_do, 0, it.row0 + qrow, it.bh,
                       bar(kBarDOFull + slot));
           ndo = g + 1;
           return true;
@@ -257,8 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (k > 0 && !(ok = mbar_wait(bar(kBarKVDone), (k - 1) & 1, abort_flag))) break;
         mbar_arrive_expect_tx(bar(kBarKV), 2 * kTile);
-        tma_load_3d(s_base + kOffK, &tm_k, 0, it.k0, it.bh, bar(kBarKV));
-        tma_load_3d(s_base + kOffV, &tm_v, 0, it.k0, it.bh, bar(kBarKV));
+        tma_load_3d(s_base + kOffK, &tm_k, 0, it.row0 + it.k0, it.kvh, bar(kBarKV));
+        tma_load_3d(s_base + kOffV, &tm_v, 0, it.row0 + it.k0, it.kvh, bar(kBarKV));
         nkv = k + 1;
         for (int h = 2; h < it.n_halves && ok; ++h) ok = load_half(h);
       }
@@ -296,21 +356,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mma_commit(bar(kBarSFull + (h & 1)));
       };
+      // Half h of an item (ring half g): Q and dO have landed and, where the
+      // sequence ends inside the half or before it, have been cleared.
+      uint32_t fix_parity = 0;   // bit: ring slot
+      int kv_fixes = 0;
+      auto wait_half = [&](const BwdItem &it, int h, int g) -> bool {
+        const int slot = g % kSlots;
+        if (!mbar_wait(bar(kBarQFull + slot), (g / kSlots) & 1, abort_flag)) return false;
+        if (!mbar_wait(bar(kBarDOFull + slot), (g / kSlots) & 1, abort_flag)) return false;
+        if (PACKED && (it.i_first * BQ + (h + 1) * BH_ > it.N)) {
+          if (!mbar_wait(bar(kBarFix + slot), (fix_parity >> slot) & 1, abort_flag)) return false;
+          fix_parity ^= 1u << slot;
+        }
+        return true;
+      };
       bool ok = true;
       int g0 = 0;       // ring halves of the earlier items
       int steps = 0;    // steps of the earlier items
       for (int k = 0; ok; ++k) {
         int w;
-        if (!(ok = fetch_item(k, w, false)) || w >= n_items) break;
         BwdItem it;
-        it.decode(w, BH, n_qb, causal);
+        if (!(ok = fetch_item(k, w, it, false)) || w >= n_items) break;
         if (!(ok = mbar_wait(bar(kBarKV), k & 1, abort_flag))) break;
+        if (PACKED && it.k0 + BM > it.N) {
+          if (!(ok = mbar_wait(bar(kBarKVFix), kv_fixes & 1, abort_flag))) break;
+          ++kv_fixes;
+        }
         // The item's first S_t, dP_t (R_t was released by the previous item's
         // last dV_t, dK_t, which execute before them).
         for (int h = 0; h < 2 && h < it.n_halves && ok; ++h) {
           const int g = g0 + h;
-          if (!(ok = mbar_wait(bar(kBarQFull + g % kSlots), (g / kSlots) & 1, abort_flag))) break;
-          if (!(ok = mbar_wait(bar(kBarDOFull + g % kSlots), (g / kSlots) & 1, abort_flag))) break;
+          if (!(ok = wait_half(it, h, g))) break;
           tc_fence_after();
           issue_sdp(h, g);
         }
@@ -342,8 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int h2 = h + 2;
           if (h2 < it.n_halves) {
             const int g2 = g0 + h2;
-            if (!(ok = mbar_wait(bar(kBarQFull + g2 % kSlots), (g2 / kSlots) & 1, abort_flag))) break;
-            if (!(ok = mbar_wait(bar(kBarDOFull + g2 % kSlots), (g2 / kSlots) & 1, abort_flag))) break;
+            if (!(ok = wait_half(it, h2, g2))) break;
             tc_fence_after();
             issue_sdp(h2, g2);
           }
@@ -371,6 +446,58 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       mma_commit(bar(kBarDrain));
       drain_wait(bar(kBarDrain), 0);
+    } else if (PACKED && warp == 2) {
+      // ------------------------------------------- rows past the sequence's end
+      // Follows every copy and takes part in freeing the ring slots, so that no
+      // barrier can run a phase past its wait.
+      const int lane = threadIdx.x & 31;
+      // Rows from `keep` on of a tile of `rows` 128-byte rows (box by box).
+      auto clear = [&](int off, int rows, int keep) {
+        for (int i = lane; i < (rows - keep) * 8; i += 32)
+#pragma unroll
+          for (int b = 0; b < kRowBoxes; ++b)
+            *reinterpret_cast<uint4 *>(smem + off + b * rows * 128 + (keep + (i >> 3)) * 128 +
+                                       (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      };
+      bool ok = true;
+      int g = 0;
+      for (int k = 0; ok; ++k) {
+        int w;
+        BwdItem it;
+        if (!(ok = fetch_item(k, w, it, true)) || w >= n_items) break;
+        auto half = [&](int h) -> bool {
+          const int slot = g % kSlots;
+          const uint32_t ph = (g / kSlots) & 1;
+          if (!wait_warp(bar(kBarQFull + slot), ph, abort_flag)) return false;
+          if (!wait_warp(bar(kBarDOFull + slot), ph, abort_flag)) return false;
+          const int keep = it.N - it.i_first * BQ - h * BH_;   // rows of the sequence
+          if (keep < BH_) {
+            clear(kOffQ + slot * kHalf, BH_, max(keep, 0));
+            clear(kOffDO + slot * kHalf, BH_, max(keep, 0));
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(kBarFix + slot));
+          }
+          if (lane == 0) {
+            mbar_arrive(bar(kBarQEmpty + slot));
+            mbar_arrive(bar(kBarDOEmpty + slot));
+          }
+          ++g;
+          return true;
+        };
+        // In the order of the copies: two halves, K and V, the other halves.
+        for (int h = 0; h < 2 && ok; ++h) ok = half(h);
+        if (!ok || !(ok = wait_warp(bar(kBarKV), k & 1, abort_flag))) break;
+        if (it.k0 + BM > it.N) {
+          clear(kOffK, BM, it.N - it.k0);
+          clear(kOffV, BM, it.N - it.k0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(kBarKVFix));
+        }
+        if (lane == 0) mbar_arrive(bar(kBarKVDone));   // (with the item's last MMA)
+        for (int h = 2; h < it.n_halves && ok; ++h) ok = half(h);
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsGroup));
@@ -392,9 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int steps = 0, g0 = 0;
     for (int k = 0; ok; ++k) {
       int w;
-      if (!(ok = fetch_item(k, w, true)) || w >= n_items) break;
       BwdItem it;
-      it.decode(w, BH, n_qb, causal);
+      if (!(ok = fetch_item(k, w, it, true)) || w >= n_items) break;
       const int key = it.k0 + r;
       // Step i of the item (global step steps + i): its dQ' rows (lanes =
       // queries), columns 32 t .. 32 t + 31 of d: TMEM -> registers ->
@@ -424,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_reduce_add_3d(&tm_dq, stage_u32, 32 * t, (it.i_first + i) * BQ + quarter * 32,
-                            it.bh);
+          tma_reduce_add_3d(&tm_dq, stage_u32, 32 * t,
+                            (it.blk0 + it.i_first + i) * BQ + quarter * 32, it.bh);
           bulk_commit();
         }
         return true;
@@ -444,11 +570,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Masking is needed only where a key of this warp is past N or, on the
         // diagonal block, later than a query (warp-uniform).
         const bool diag = causal && (q0 < it.k0 + BM) && (q0 + BH_ > it.k0);
-        const bool masked = diag || (it.k0 + quarter * 32 + 31 >= N);
+        const bool masked = diag || (it.k0 + quarter * 32 + 31 >= it.N);
         if (masked)
-          bwd_tile::chunks<true>(R, vec, ds_buf, r, key, q0, N, diag, c2);
+          bwd_tile::chunks<true>(R, vec, ds_buf, r, key, q0, it.N, diag, c2);
         else
-          bwd_tile::chunks<false>(R, vec, ds_buf, r, key, q0, N, diag, c2);
+          bwd_tile::chunks<false>(R, vec, ds_buf, r, key, q0, it.N, diag, c2);
         tmem_wait_st();
         fence_proxy_async_smem();
         tc_fence_before();
@@ -468,7 +594,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // that eight lanes store one row's 128 contiguous bytes.
       if (!(ok = wait_warp(bar(kBarKVDone), k & 1, abort_flag))) break;
       tc_fence_after();
-      __nv_bfloat16 *base = (t ? dk : dv) + static_cast<int64_t>(it.bh) * N * D;
+      // Rows are D values apart; PACKED: [row][key/value head].
+      const int64_t row_step = PACKED ? static_cast<int64_t>(pk.kv_heads) * D : D;
+      __nv_bfloat16 *base =
+          (t ? dk : dv) + (PACKED ? it.row0 * row_step + it.kvh * D : static_cast<int64_t>(it.bh) * N * D);
       const float mul = t ? scale : 1.f;
       const uint32_t col = t ? kColDK : kColDV;
       const int key_w = key - lane;   // this warp's first key row
@@ -480,6 +609,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarEpiDone));
+      if (PACKED && pk.group > 1) {
+        // Another query head of the group adds to the same rows: fp32 boxes of
+        // 32 rows x 32 columns into the accumulator (dK there still unscaled).
+        // Rows past the sequence fall on its padding.
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (c > 0) {
+            if (lane == 0) bulk_wait_read_all();
+            __syncwarp();
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(v[c][4 * j], v[c][4 * j + 1], v[c][4 * j + 2], v[c][4 * j + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_reduce_add_3d(t ? &tm_dk : &tm_dv, stage_u32, 32 * c,
+                              it.blk0 * BQ + it.k0 + quarter * 32, it.kvh);
+            bulk_commit();
+          }
+        }
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+        g0 += it.n_halves;
+        steps += it.n_steps;
+        continue;
+      }
 #pragma unroll
       for (int kq = 0; kq < 8; ++kq) {
         const uint32_t *c8 = &v[kq >> 2][(kq & 3) * 8];
@@ -495,8 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int kq = 0; kq < 8; ++kq) {
         const int rr = (lane >> 3) + 4 * kq, ch = lane & 7;
         const uint4 x = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((ch ^ (rr & 7)) * 16));
-        if (key_w + rr < N)
-          *reinterpret_cast<uint4 *>(base + static_cast<int64_t>(key_w + rr) * D + ch * 8) = x;
+        if (key_w + rr < it.N)
+          *reinterpret_cast<uint4 *>(base + (key_w + rr) * row_step + ch * 8) = x;
       }
       // The next read-out writes dQ' boxes over the staging tile.
       __syncwarp();
@@ -525,21 +682,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-}  // namespace
-
-cudaError_t launch_bwd_main_d64(const CUtensorMap &tq64, const CUtensorMap &tk,
-                                const CUtensorMap &tv, const CUtensorMap &tdo64,
-                                const CUtensorMap &tdq, const float *vecs, void *dk, void *dv,
-                                int BH, int N, float scale, int causal, int *sched,
-                                int fault_cta, int *dev_status, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(bwd_pipe64_kernel,
+template <bool PACKED>
+cudaError_t launch_main(const CUtensorMap &tq64, const CUtensorMap &tk, const CUtensorMap &tv,
+                        const CUtensorMap &tdo64, const CUtensorMap &tdq, const float *vecs,
+                        void *dk, void *dv, int BH, int N, float scale, int causal, int *sched,
+                        int fault_cta, int *dev_status, cudaStream_t stream,
+                        const CUtensorMap &tdk, const CUtensorMap &tdv, const BwdPacked &pk) {
+  cudaError_t e = cudaFuncSetAttribute(bwd_pipe64_kernel<PACKED>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   int dev = 0, n_sm = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return e;
-  const int n_qb = (N + BQ - 1) / BQ;
+  const int n_qb = PACKED ? pk.n_blocks : (N + BQ - 1) / BQ;
   const long long n_items = static_cast<long long>(n_qb) * BH;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(n_items < n_sm ? n_items : n_sm));
@@ -551,10 +707,32 @@ cudaError_t launch_bwd_main_d64(const CUtensorMap &tq64, const CUtensorMap &tk,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, bwd_pipe64_kernel, tq64, tk, tv, tdo64, tdq, vecs,
+  return cudaLaunchKernelEx(&cfg, bwd_pipe64_kernel<PACKED>, tq64, tk, tv, tdo64, tdq, vecs,
                             reinterpret_cast<__nv_bfloat16 *>(dk),
                             reinterpret_cast<__nv_bfloat16 *>(dv), N, BH, scale, causal, sched,
-                            fault_cta, dev_status);
+                            fault_cta, dev_status, tdk, tdv, pk);
+}
+
+}  // namespace
+
+cudaError_t launch_bwd_main_d64(const CUtensorMap &tq64, const CUtensorMap &tk,
+                                 const CUtensorMap &tv, const CUtensorMap &tdo64,
+                                 const CUtensorMap &tdq, const float *vecs, void *dk, void *dv,
+                                 int BH, int N, float scale, int causal, int *sched,
+                                 int fault_cta, int *dev_status, cudaStream_t stream) {
+  return launch_main<false>(tq64, tk, tv, tdo64, tdq, vecs, dk, dv, BH, N, scale, causal, sched,
+                            fault_cta, dev_status, stream, tdq, tdq, BwdPacked{});
+}
+
+cudaError_t launch_bwd_packed_main_d64(const CUtensorMap &tq64, const CUtensorMap &tk,
+                                        const CUtensorMap &tv, const CUtensorMap &tdo64,
+                                        const CUtensorMap &tdq, const CUtensorMap &tdk,
+                                        const CUtensorMap &tdv, const float *vecs, void *dk,
+                                        void *dv, int H, const BwdPacked &pk, float scale,
+                                        int causal, int *sched, int *dev_status,
+                                        cudaStream_t stream) {
+  return launch_main<true>(tq64, tk, tv, tdo64, tdq, vecs, dk, dv, H, 0, scale, causal, sched, -1,
+                           dev_status, stream, tdk, tdv, pk);
 }
 
 }  // namespace fattn

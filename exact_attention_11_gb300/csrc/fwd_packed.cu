@@ -49,6 +49,7 @@
 #include <cstdint>
 
 #include "kernels.h"
+#include "packed.cuh"
 #include "ptx.cuh"
 
 namespace fattn {
@@ -139,8 +140,6 @@ struct Args {
   float scale_log2;
 };
 
-__device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
-
 // Key tiles that `n` tokens, the last of which sees key `last` last, visit.
 __device__ __forceinline__ int tiles_for(int n, int last, int kv_len) {
   return n > 0 ? (max(0, min(kv_len, last + 1)) + BN - 1) / BN : 0;
@@ -166,24 +165,6 @@ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
     q.pos = a.causal ? 0 : kSeesAll;
   }
   return q;
-}
-
-// The last s in [0, S) with first(s) <= v for a non-decreasing first(), or -1;
-// by the whole warp, 32 candidates a round.
-template <typename F>
-__device__ __forceinline__ int warp_search(int S, int v, F first) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, n = S;
-  while (true) {
-    const int step = (n + 31) / 32;
-    const int i = lo + lane * step;
-    const uint32_t m = __ballot_sync(~0u, lane * step < n && first(i) <= v);
-    if (m == 0) return -1;
-    const int hit = 31 - __clz(m);
-    if (step == 1) return lo + hit;
-    lo += hit * step;
-    n = min(step, n - hit * step);
-  }
 }
 
 // Item w (whole warp); false if it has no work.

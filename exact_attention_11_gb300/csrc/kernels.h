@@ -103,6 +103,31 @@ cudaError_t launch_bwd_main_d64(const CUtensorMap &tq64, const CUtensorMap &tk,
                                 int BH, int N, float scale, int causal, int *sched,
                                 int fault_cta, int *dev_status, cudaStream_t stream);
 
+// The main kernels for packed sequences: `table` holds for every padded
+// 128-row block (sequence s starts at block cu_seqlens[s] / 128 + s) its
+// sequence's first row, length (0: the block belongs to none) and first padded
+// block.  The accumulators' maps have n_blocks * 128 rows per head; tdk, tdv
+// are used when group > 1.  tq64, tdo64, tk, tv: maps {d, T, heads} of the
+// packed tensors.
+struct BwdPacked {
+  const int4 *table;
+  int n_blocks, group, kv_heads;
+};
+cudaError_t launch_bwd_packed_main_d128(const CUtensorMap &tq64, const CUtensorMap &tk,
+                                        const CUtensorMap &tv, const CUtensorMap &tdo64,
+                                        const CUtensorMap &tdq, const CUtensorMap &tdk,
+                                        const CUtensorMap &tdv, const float *vecs, void *dk,
+                                        void *dv, int H, const BwdPacked &pk, float scale,
+                                        int causal, int *sched, int *dev_status,
+                                        cudaStream_t stream);
+cudaError_t launch_bwd_packed_main_d64(const CUtensorMap &tq64, const CUtensorMap &tk,
+                                       const CUtensorMap &tv, const CUtensorMap &tdo64,
+                                       const CUtensorMap &tdq, const CUtensorMap &tdk,
+                                       const CUtensorMap &tdv, const float *vecs, void *dk,
+                                       void *dv, int H, const BwdPacked &pk, float scale,
+                                       int causal, int *sched, int *dev_status,
+                                       cudaStream_t stream);
+
 int decode_max_parts(int max_num_blocks_per_seq);
 // Grouped key/value heads (decode_gqa.cu): group = num_heads / num_kv_heads
 // must be 2 or a multiple of 4.  Same workspace and counters as the one-head
@@ -189,5 +214,30 @@ size_t paged_prefill_workspace_bytes(int T, int S, int H, int Hk, int max_blocks
 cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
                                  const CUtensorMap &tv, const PackedProblem &p, float *workspace,
                                  int *sched, int *dev_status, cudaStream_t stream);
+
+// Gradients of the packed forward (bwd_packed.cu).  Workspace, in floats from
+// its start: the dQ accumulator [H][n_blocks * 128][d], those of dK and dV
+// [Hk][..][d] (where heads share them), [-LSE2 | -D] per head and block, the
+// block table.
+struct PackedGradLayout {
+  int n_blocks;
+  size_t dk_acc, dv_acc, vecs, table, bytes;
+};
+PackedGradLayout packed_grad_layout(int T, int S, int H, int Hk, int d);
+// q, dout: maps {d, T, H} with boxes of 64 x bwd_qdo_box_rows(d) x 1; k, v
+// {d, T, Hk}, 64 x 128 x 1; the accumulators' fp32 maps as for launch_bwd_bf16.
+struct PackedGradMaps {
+  CUtensorMap q, k, v, dout, dq_acc, dk_acc, dv_acc;
+};
+struct PackedGrad {
+  const void *o, *dout;
+  const float *lse;
+  void *dq, *dk, *dv;
+  const int *cu_seqlens;
+  int S, T, H, Hk, d, causal;
+  float scale;
+};
+cudaError_t launch_bwd_packed(const PackedGradMaps &m, const PackedGrad &p, float *ws, int *sched,
+                              int *dev_status, cudaStream_t stream);
 
 }  // namespace fattn

@@ -523,6 +523,35 @@ int fa_forward_packed_f16(const void *q, const void *k, const void *v, void *o, 
                           long long v_stride, float scale, int causal, fa_stream_t stream);
 
 /*
+ * fa_backward_packed -- gradients of fa_forward_packed (bf16).
+ *
+ * The formulas of fa_backward, sequence by sequence; dK and dV of a key/value
+ * head are the sums over the query heads that use it.
+ *   q, k, v, cu_seqlens, sizes, strides, scale, causal   the forward's.
+ *   o, lse        what fa_forward_packed returned for them (lse [num_heads,
+ *                 total_tokens]).
+ *   dout          bf16 [total_tokens, num_heads, d], dense: the gradient of o.
+ *   dq            bf16 [total_tokens, num_heads, d], dk and dv bf16
+ *                 [total_tokens, num_kv_heads, d], dense, written; rows of no
+ *                 sequence are left as they were (and nothing of theirs is read).
+ *   workspace     device memory of at least fa_backward_packed_workspace_bytes
+ *                 bytes, 16-byte aligned, scratch during the call; calls whose
+ *                 work overlaps on the GPU need separate ones.
+ * One sequence's NaN or Inf does not reach another's gradients.  Rounding and
+ * errors as for fa_backward: products accumulate in fp32, P and dS are rounded to
+ * bf16 before their products; dQ, and with grouped heads dK and dV, are summed in
+ * fp32 with atomic adds, so their last bits may vary from run to run.
+ */
+unsigned long long fa_backward_packed_workspace_bytes(int num_seqs, int total_tokens,
+                                                      int num_heads, int num_kv_heads, int d);
+int fa_backward_packed(const void *q, const void *k, const void *v, const void *o,
+                       const void *dout, const float *lse, void *dq, void *dk, void *dv,
+                       const int *cu_seqlens, int num_seqs, int total_tokens, int num_heads,
+                       int num_kv_heads, int d, long long q_stride, long long k_stride,
+                       long long v_stride, float scale, int causal, void *workspace,
+                       unsigned long long workspace_bytes, fa_stream_t stream);
+
+/*
  * fa_paged_prefill -- attention of a chunk of new tokens per sequence over a
  * paged KV cache that holds the sequence's whole context, the chunk's own keys
  * and values included (fa_qk_norm_rope_cache writes them).  Chunks may have any

@@ -72,3 +72,30 @@ def test_chunk_workspace(lib):
     assert size(64, 4096, 32, 8, 1024) == 0                 # enough rows without a split
     n = size(1, 1, 32, 8, 1024)
     assert n > 0 and n % (32 * 130 * 4) == 0
+
+
+BWD = dict(q=P, k=P, v=P, o=P, dout=P, lse=P, dq=P, dk=P, dv=P, cu_seqlens=P, num_seqs=0,
+           total_tokens=10, num_heads=4, num_kv_heads=2, d=64, q_stride=256, k_stride=128,
+           v_stride=128, scale=0.125, causal=1, workspace=NULL, workspace_bytes=0)
+
+
+@pytest.mark.parametrize("change,expect", [
+    (dict(), 0), (dict(num_seqs=2, total_tokens=0), 0),
+    (dict(dout=NULL), -1), (dict(lse=NULL), -1), (dict(dv=NULL), -1), (dict(k=NULL), -1),
+    (dict(num_kv_heads=3), -1), (dict(scale=0.0), -1), (dict(d=256), -2),
+    (dict(dk=P + 8), -3), (dict(dout=P + 2), -3), (dict(k_stride=120), -1),
+    (dict(num_seqs=1), -1),                                         # no workspace
+    (dict(num_seqs=1, workspace=P, workspace_bytes=100), -1),
+    (dict(num_seqs=1, workspace=P + 4, workspace_bytes=1 << 30), -3),
+    (dict(num_seqs=1 << 24, num_heads=4), -2),                      # padded rows past 2^30
+])
+def test_backward_checks(lib, change, expect):
+    assert lib.fa_backward_packed(*{**BWD, **change}.values(), None) == expect
+
+
+def test_backward_workspace(lib):
+    size = fa.fa_backward_packed_workspace_bytes
+    assert size(0, 10, 4, 2, 64) == 0 and size(1, 10, 4, 3, 64) == 0
+    # one padded block: dQ of 4 heads, dK and dV of 2, vectors, table entry
+    assert size(1, 10, 4, 2, 64) == 4 * (128 * 64 * (4 + 2 * 2) + 4 * 256 + 4)
+    assert size(1, 10, 4, 4, 64) == 4 * (128 * 64 * 4 + 4 * 256 + 4)
