@@ -521,6 +521,8 @@ def forward_fp8(x, scale=None, causal=False, out=None, lse=None, want_lse=True):
 
 
 # -------------------------------------------- packed tokens: [tokens, heads, d] tensors
+# These calls are short (a decode step's take a few microseconds on the GPU), so
+# their checks touch each tensor's attributes as few times as they can.
 def _on_device(fn):
     """Runs ``fn`` with its first tensor's device current: the C calls work on
     the current device, and a caller's may be another one."""
@@ -534,28 +536,31 @@ def _on_device(fn):
     return run
 
 
-def _rows(name, t, like, heads=None):
-    """Checks a [tokens, heads, d] tensor with dense heads and returns its
-    token stride in elements; ``like`` sets the device, type and token count."""
-    if t.dim() != 3 or t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2] \
-            or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} has an inconsistent shape")
-    if t.dtype != like.dtype or t.device != like.device or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor of the same type and device as the rest")
-    n, h, d = t.shape
+def _raw_stream(index):
+    """Handle of the current torch stream of CUDA device ``index``."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)   # current_stream() builds an object first
+
+
+def _rows(name, t, T, heads, d, dtype, dev):
+    """Checks a [T, heads, d] tensor with dense heads; its token stride in elements."""
+    if t.shape != (T, heads, d) or t.dtype != dtype or t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a [{T},{heads},{d}] {dtype} tensor on the CUDA device "
+                         f"of the rest, not {tuple(t.shape)} {t.dtype} on {t.device}")
     s0, s1, s2 = t.stride()
-    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be dense")
-    return s0 if n > 1 else max(h * d, 1)
+    return s0 if T > 1 else max(heads * d, 1)
 
 
-def _vector(name, t, dtype, like, numel=None):
-    """Checks a dense vector on ``like``'s device."""
-    if t.dtype != dtype or t.device != like.device or not t.is_contiguous() \
+def _dense(name, t, dtype, dev, numel=None):
+    """Checks a contiguous tensor and returns its address."""
+    if t.dtype != dtype or t.get_device() != dev or not t.is_contiguous() \
             or (numel is not None and t.numel() != numel):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor"
                          + (f" of {numel} values" if numel is not None else "")
-                         + " on the same device as the rest")
+                         + " on the CUDA device of the rest")
+    return t.data_ptr()
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_context=4096,
@@ -592,21 +597,43 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_c
     return freq.to(device), mscale
 
 
+def _workspace(t, dev):
+    """Bytes of a caller's workspace tensor."""
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the CUDA device of the rest")
+    return t.numel() * t.element_size()
+
+
 def _prep_args(q, k, positions, inv_freq, q_weight, k_weight):
+    """Checks the inputs that the norm-and-rotation helpers share: T, H, Hk, d,
+    q's type's suffix, device, token strides, the six addresses, rot_dim."""
+    T, H, d = q.shape
+    Hk = k.shape[1] if k.dim() == 3 else -1
+    dtype, dev = q.dtype, q.get_device()
+    suffix = _prep_suffix(dtype)
+    qs, ks = _rows("q", q, T, H, d, dtype, dev), _rows("k", k, T, Hk, d, dtype, dev)
+    i32, f64 = _dtypes()
+    ptrs = (q.data_ptr(), k.data_ptr(),
+            None if q_weight is None else _dense("q_weight", q_weight, dtype, dev, d),
+            None if k_weight is None else _dense("k_weight", k_weight, dtype, dev, d),
+            _dense("positions", positions, i32, dev, T), _dense("inv_freq", inv_freq, f64, dev))
+    return T, H, Hk, d, dtype, suffix, dev, qs, ks, ptrs, 2 * inv_freq.numel()
+
+
+def _dtypes():
     import torch
-    if q.dtype not in (torch.bfloat16, torch.float16, torch.float32):
-        raise ValueError("q and k must be bf16, fp16 or fp32")
-    qs, ks = _rows("q", q, q), _rows("k", k, q)
-    T, _, d = q.shape
-    _vector("positions", positions, torch.int32, q, T)
-    _vector("inv_freq", inv_freq, torch.float64, q)
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _vector(name, w, q.dtype, q, d)
-    return qs, ks
+    return torch.int32, torch.float64
 
 
-_PREP_SUFFIX = {"torch.bfloat16": "", "torch.float16": "_f16", "torch.float32": "_fp32"}
+def _prep_suffix(dtype):
+    import torch
+    if dtype == torch.bfloat16:
+        return ""
+    if dtype == torch.float16:
+        return "_f16"
+    if dtype == torch.float32:
+        return "_fp32"
+    raise ValueError("q and k must be bf16, fp16 or fp32")
 
 
 @_on_device
@@ -620,21 +647,19 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     first rot_dim values of a head are rotated.  Returns (q_out, k_out), dense.
     Runs on the current torch stream."""
     import torch
-    qs, ks = _prep_args(q, k, positions, inv_freq, q_weight, k_weight)
-    T, H, d = q.shape
+    T, H, Hk, d, dtype, suffix, dev, qs, ks, ptrs, rot = _prep_args(
+        q, k, positions, inv_freq, q_weight, k_weight)
     if q_out is None:
-        q_out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
+        q_out = torch.empty((T, H, d), dtype=dtype, device=q.device)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    _vector("q_out", q_out, q.dtype, q, q.numel())
-    _vector("k_out", k_out, q.dtype, q, k.numel())
+        k_out = torch.empty((T, Hk, d), dtype=dtype, device=q.device)
+    outs = (_dense("q_out", q_out, dtype, dev, T * H * d),
+            _dense("k_out", k_out, dtype, dev, T * Hk * d))
     if T == 0:      # empty tensors have no address to pass
         return q_out, k_out
-    name = "fa_qk_norm_rope" + _PREP_SUFFIX[str(q.dtype)]
-    _check(name, getattr(load(), name)(
-        _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq),
-        _ptr(q_out), _ptr(k_out), T, H, k.shape[1], d, 2 * inv_freq.numel(), int(interleaved),
-        qs, ks, eps, mscale, _stream(q)))
+    name = "fa_qk_norm_rope" + suffix
+    _check(name, getattr(_lib or load(), name)(
+        *ptrs, *outs, T, H, Hk, d, rot, int(interleaved), qs, ks, eps, mscale, _raw_stream(dev)))
     return q_out, k_out
 
 
@@ -646,30 +671,33 @@ def qk_norm_rope_cache(q, k, v, positions, inv_freq, slots, k_cache, v_cache, q_
     and ``paged_prefill`` at slots (int64 [T]: block * block_size + offset; a
     negative slot stores nothing).  Returns the prepared queries, dense."""
     import torch
-    qs, ks = _prep_args(q, k, positions, inv_freq, q_weight, k_weight)
-    T, H, d = q.shape
-    Hk = k.shape[1]
-    vs = _rows("v", v, q, Hk)
-    _vector("slots", slots, torch.int64, q, T)
-    if q.dtype != torch.bfloat16:
+    T, H, Hk, d, dtype, suffix, dev, qs, ks, ptrs, rot = _prep_args(
+        q, k, positions, inv_freq, q_weight, k_weight)
+    if suffix != "":
         raise ValueError("the cache form is bf16")
-    if k_cache.dim() != 5 or v_cache.dim() != 4:
-        raise ValueError("inconsistent cache shapes")
-    nb, hc, dx, bs, x = k_cache.shape
-    if hc != Hk or dx * x != d or x != 8 or tuple(v_cache.shape) != (nb, Hk, d, bs):
-        raise ValueError("inconsistent cache shapes")
-    _vector("k_cache", k_cache, q.dtype, q)
-    _vector("v_cache", v_cache, q.dtype, q)
+    vs = _rows("v", v, T, Hk, d, dtype, dev)
+    nb, bs = _cache_shape(k_cache, v_cache, Hk, d)
     if q_out is None:
-        q_out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
-    _vector("q_out", q_out, q.dtype, q, q.numel())
+        q_out = torch.empty((T, H, d), dtype=dtype, device=q.device)
+    rest = (_dense("slots", slots, torch.int64, dev, T),
+            _dense("q_out", q_out, dtype, dev, T * H * d),
+            _dense("k_cache", k_cache, dtype, dev), _dense("v_cache", v_cache, dtype, dev))
     if T == 0:
         return q_out
-    _check("fa_qk_norm_rope_cache", load().fa_qk_norm_rope_cache(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(q_weight), _ptr(k_weight), _ptr(positions),
-        _ptr(inv_freq), _ptr(slots), _ptr(q_out), _ptr(k_cache), _ptr(v_cache), T, H, Hk, d, bs,
-        nb, 2 * inv_freq.numel(), int(interleaved), qs, ks, vs, eps, mscale, _stream(q)))
+    _check("fa_qk_norm_rope_cache", (_lib or load()).fa_qk_norm_rope_cache(
+        ptrs[0], ptrs[1], v.data_ptr(), *ptrs[2:], *rest, T, H, Hk, d, bs, nb, rot,
+        int(interleaved), qs, ks, vs, eps, mscale, _raw_stream(dev)))
     return q_out
+
+
+def _cache_shape(k_cache, v_cache, Hk, d):
+    """Number and size of the blocks of a pair of paged caches of Hk heads."""
+    if k_cache.dim() != 5:
+        raise ValueError("inconsistent cache shapes")
+    nb, hc, dx, bs, x = k_cache.shape
+    if hc != Hk or x != 8 or dx * x != d or v_cache.shape != (nb, Hk, d, bs):
+        raise ValueError("inconsistent cache shapes")
+    return nb, bs
 
 
 @_on_device
@@ -682,38 +710,45 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight=No
     weight.  ``workspace`` (optional) is a CUDA tensor of at least
     ``fa_qk_norm_rope_backward_workspace_bytes`` bytes."""
     import torch
-    qs, ks = _prep_args(q, k, positions, inv_freq, q_weight, k_weight)
-    T, H, d = q.shape
+    T, H, Hk, d, dtype, suffix, dev, qs, ks, ptrs, rot = _prep_args(
+        q, k, positions, inv_freq, q_weight, k_weight)
     if dq_out.shape != q.shape or dk_out.shape != k.shape:
         raise ValueError("dq_out and dk_out must have the shapes of q and k")
-    _vector("dq_out", dq_out, q.dtype, q)
-    _vector("dk_out", dk_out, q.dtype, q)
+    ins = (_dense("dq_out", dq_out, dtype, dev), _dense("dk_out", dk_out, dtype, dev))
     dq, dk = torch.empty_like(dq_out), torch.empty_like(dk_out)
-    dqw, dkw = (None if w is None else torch.empty(d, dtype=torch.float32, device=q.device)
-                for w in (q_weight, k_weight))
+    dqw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
+    dkw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
     if T == 0:
         return dq, dk, *(w if w is None else w.zero_() for w in (dqw, dkw))
-    if workspace is None and not (dqw is None and dkw is None):
-        nbytes = load().fa_qk_norm_rope_backward_workspace_bytes(T, d)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
-    name = "fa_qk_norm_rope_backward" + _PREP_SUFFIX[str(q.dtype)]
-    _check(name, getattr(load(), name)(
-        _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
-        _ptr(positions), _ptr(inv_freq), _ptr(dq), _ptr(dk), _ptr(dqw), _ptr(dkw), T, H,
-        k.shape[1], d, 2 * inv_freq.numel(), int(interleaved), qs, ks, eps, mscale,
-        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _stream(q)))
+    lib = _lib or load()
+    nbytes = 0
+    if workspace is not None:
+        nbytes = _workspace(workspace, dev)
+    elif dqw is not None or dkw is not None:
+        nbytes = lib.fa_qk_norm_rope_backward_workspace_bytes(T, d)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    name = "fa_qk_norm_rope_backward" + suffix
+    _check(name, getattr(lib, name)(
+        *ins, *ptrs, dq.data_ptr(), dk.data_ptr(), _ptr(dqw), _ptr(dkw), T, H, Hk, d, rot,
+        int(interleaved), qs, ks, eps, mscale, _ptr(workspace), nbytes, _raw_stream(dev)))
     return dq, dk, dqw, dkw
 
 
-def _packed_args(q, k, v, cu_seqlens):
+def _packed_args(q, k, v, cu_seqlens, dtypes):
+    """Checks q, k, v and cu_seqlens of the packed calls."""
     import torch
-    qs, ks = _rows("q", q, q), _rows("k", k, q)
-    vs = _rows("v", v, q, k.shape[1])
-    _vector("cu_seqlens", cu_seqlens, torch.int32, q)
-    if cu_seqlens.numel() < 1:
+    T, H, d = q.shape
+    Hk = k.shape[1] if k.dim() == 3 else -1
+    dtype, dev = q.dtype, q.get_device()
+    if dtype not in dtypes:
+        raise ValueError("q, k, v must be " + " or ".join(str(x) for x in dtypes))
+    qs = _rows("q", q, T, H, d, dtype, dev)
+    ks, vs = _rows("k", k, T, Hk, d, dtype, dev), _rows("v", v, T, Hk, d, dtype, dev)
+    cu = _dense("cu_seqlens", cu_seqlens, torch.int32, dev)
+    S = cu_seqlens.numel() - 1
+    if S < 0:
         raise ValueError("cu_seqlens holds num_seqs + 1 offsets")
-    return qs, ks, vs
+    return T, H, Hk, d, S, dtype, dev, qs, ks, vs, cu
 
 
 @_on_device
@@ -728,25 +763,25 @@ def forward_packed(q, k, v, cu_seqlens, scale=None, causal=True, out=None, lse=N
     written (they are uninitialised in tensors made here).  Runs on the current
     torch stream."""
     import torch
-    qs, ks, vs = _packed_args(q, k, v, cu_seqlens)
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError("q, k, v must be bf16 or fp16")
-    T, H, d = q.shape
+    T, H, Hk, d, S, dtype, dev, qs, ks, vs, cu = _packed_args(
+        q, k, v, cu_seqlens, (torch.bfloat16, torch.float16))
     if scale is None:
         scale = d ** -0.5
     if out is None:
-        out = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
-    _vector("out", out, q.dtype, q, q.numel())
+        out = torch.empty((T, H, d), dtype=dtype, device=q.device)
     if lse is None and want_lse:
         lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-    if lse is not None:
-        _vector("lse", lse, torch.float32, q, H * T)
-    if T == 0:
+    o_ptr = _dense("out", out, dtype, dev, T * H * d)
+    lse_ptr = None if lse is None else _dense("lse", lse, torch.float32, dev, H * T)
+    if T == 0 or S == 0:
         return out, lse
-    name = "fa_forward_packed" + ("_f16" if q.dtype == torch.float16 else "")
-    _check(name, getattr(load(), name)(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(cu_seqlens),
-        cu_seqlens.numel() - 1, T, H, k.shape[1], d, qs, ks, vs, scale, int(causal), _stream(q)))
+    lib = _lib or load()
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o_ptr, lse_ptr, cu, S, T, H, Hk, d, qs, ks,
+            vs, scale, int(causal), _raw_stream(dev))
+    if dtype == torch.float16:
+        _check("fa_forward_packed_f16", lib.fa_forward_packed_f16(*args))
+    else:
+        _check("fa_forward_packed", lib.fa_forward_packed(*args))
     return out, lse
 
 
@@ -759,31 +794,30 @@ def backward_packed(q, k, v, o, lse, dout, cu_seqlens, scale=None, causal=True, 
     ``fa_backward_packed_workspace_bytes`` bytes.  Rows of no sequence are not
     written.  Runs on the current torch stream."""
     import torch
-    qs, ks, vs = _packed_args(q, k, v, cu_seqlens)
-    if q.dtype != torch.bfloat16:
-        raise ValueError("q, k, v must be bf16")
-    T, H, d = q.shape
-    Hk = k.shape[1]
+    T, H, Hk, d, S, dtype, dev, qs, ks, vs, cu = _packed_args(q, k, v, cu_seqlens,
+                                                              (torch.bfloat16,))
     if o.shape != q.shape or dout.shape != q.shape:
         raise ValueError("o and dout must have q's shape")
-    _vector("o", o, q.dtype, q)
-    _vector("dout", dout, q.dtype, q)
-    _vector("lse", lse, torch.float32, q, H * T)
+    ins = (_dense("o", o, dtype, dev), _dense("dout", dout, dtype, dev),
+           _dense("lse", lse, torch.float32, dev, H * T))
     if scale is None:
         scale = d ** -0.5
-    dq = torch.empty((T, H, d), dtype=q.dtype, device=q.device)
-    dk, dv = (torch.empty((T, Hk, d), dtype=q.dtype, device=q.device) for _ in range(2))
-    S = cu_seqlens.numel() - 1
+    device = q.device
+    dq = torch.empty((T, H, d), dtype=dtype, device=device)
+    dk = torch.empty((T, Hk, d), dtype=dtype, device=device)
+    dv = torch.empty((T, Hk, d), dtype=dtype, device=device)
     if T == 0 or S == 0:
         return dq, dk, dv
-    lib = load()
+    lib = _lib or load()
     if workspace is None:
         nbytes = lib.fa_backward_packed_workspace_bytes(S, T, H, Hk, d)
-        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        nbytes = _workspace(workspace, dev)
     _check("fa_backward_packed", lib.fa_backward_packed(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dout), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
-        _ptr(cu_seqlens), S, T, H, Hk, d, qs, ks, vs, scale, int(causal), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(q)))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), *ins, dq.data_ptr(), dk.data_ptr(),
+        dv.data_ptr(), cu, S, T, H, Hk, d, qs, ks, vs, scale, int(causal), workspace.data_ptr(),
+        nbytes, _raw_stream(dev)))
     return dq, dk, dv
 
 
@@ -798,35 +832,36 @@ def paged_prefill(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, s
     [T,H,128]; rows of no sequence are not written.  Runs on the current torch
     stream."""
     import torch
-    qs = _rows("q", q, q)
     T, H, D = q.shape
-    if q.dtype != torch.bfloat16:
+    dtype, dev = q.dtype, q.get_device()
+    if dtype != torch.bfloat16:
         raise ValueError("q must be bf16")
-    if k_cache.dim() != 5 or block_tables.dim() != 2:
+    qs = _rows("q", q, T, H, D, dtype, dev)
+    Hk = k_cache.shape[1] if k_cache.dim() == 5 else -1
+    nb, bs = _cache_shape(k_cache, v_cache, Hk, D)
+    if block_tables.dim() != 2 or Hk <= 0 or H % Hk != 0:
         raise ValueError("inconsistent cache shapes")
-    nb, Hk, Dx, bs, x = k_cache.shape
     S, mb = block_tables.shape
-    if Hk <= 0 or H % Hk != 0 or Dx * x != D or x != 8 or tuple(v_cache.shape) != (nb, Hk, D, bs):
-        raise ValueError("inconsistent cache shapes")
-    _vector("k_cache", k_cache, q.dtype, q)
-    _vector("v_cache", v_cache, q.dtype, q)
-    _vector("block_tables", block_tables, torch.int32, q)
-    _vector("context_lens", context_lens, torch.int32, q, S)
-    _vector("cu_seqlens", cu_seqlens, torch.int32, q, S + 1)
+    i32 = torch.int32
+    ptrs = (q.data_ptr(), _dense("k_cache", k_cache, dtype, dev),
+            _dense("v_cache", v_cache, dtype, dev), _dense("block_tables", block_tables, i32, dev),
+            _dense("context_lens", context_lens, i32, dev, S),
+            _dense("cu_seqlens", cu_seqlens, i32, dev, S + 1))
     if scale is None:
         scale = D ** -0.5
     if out is None:
-        out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
-    _vector("out", out, q.dtype, q, q.numel())
+        out = torch.empty((T, H, D), dtype=dtype, device=q.device)
+    out_ptr = _dense("out", out, dtype, dev, T * H * D)
     if T == 0 or S == 0:
         return out
-    lib = load()
-    if workspace is None:
+    lib = _lib or load()
+    if workspace is not None:
+        nbytes = _workspace(workspace, dev)
+    else:
         nbytes = lib.fa_paged_prefill_workspace_bytes(S, T, H, Hk, mb)
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     _check("fa_paged_prefill", lib.fa_paged_prefill(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), _ptr(context_lens),
-        _ptr(cu_seqlens), _ptr(out), S, T, H, Hk, D, bs, nb, mb, qs, scale, _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(q)))
+        *ptrs, out_ptr, S, T, H, Hk, D, bs, nb, mb, qs, scale, _ptr(workspace), nbytes,
+        _raw_stream(dev)))
     return out

@@ -22,14 +22,14 @@
 //    MMA rows, and the causal diagonal touches 128 / G keys of a row instead
 //    of 128.  A tile is one TMA box (64 of d) x G heads x (128 / G) tokens; when
 //    G does not divide 128 the last rows of the tile hold no query.
-//  * Sequence bounds are device data.  An item is (block of two tiles, key/value
-//    head [, context partition]); blocks are numbered so that sequence s starts
-//    at block cu_seqlens[s] / (2 * 128/G) + s, which needs no prefix sum over
-//    lengths and leaves at most one unused number per sequence.  The producer
-//    warp finds an item's sequence by a 32-way search and hands the decoded
-//    item to the other roles.  Items are numbered from the last block down, so
-//    that every sequence's heaviest causal blocks come first and the call ends
-//    with its lightest.
+//  * Sequence bounds are device data.  An item is (block of two tiles, context
+//    partition, key/value head).  Up to kCachedSeqs sequences, each CTA reads the
+//    bounds once and numbers the items densely with a prefix sum in shared memory;
+//    beyond, sequence s starts at block cu_seqlens[s] / (2 * 128/G) + s, which
+//    needs no prefix sum and leaves some numbers unused.  The producer warp finds
+//    an item's sequence by a 32-way search and hands the decoded item to the other
+//    roles.  Items are numbered from the last block down, so that every sequence's
+//    heaviest causal blocks come first and the call ends with its lightest.
 //  * The key tile that a sequence ends in also holds the next sequence's rows
 //    (packed) or whatever the cache slots past the context hold (paged).  Their
 //    scores are set to -inf, and since a zero weight does not cancel a NaN, a
@@ -39,8 +39,9 @@
 //    (decode_gqa_tc.cu): K in no-swizzle core matrices, V^T in 32-byte-swizzle
 //    blocks of 16 tokens, both K-major B operands here.  Block ids outside the
 //    cache read as zeros.
-//  * Few rows over long contexts do not fill the GPU: the context is then cut
-//    into partitions of `part_tiles` key tiles; each writes its unnormalised
+//  * Few rows over long contexts do not fill the GPU, and a long context beside
+//    short ones would finish alone: a block's context is then cut into equal
+//    partitions of about `part_tiles` key tiles; each writes its unnormalised
 //    fp32 rows and (max, sum), and paged_merge_kernel joins them (eq. (4)).
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -66,40 +67,43 @@ constexpr float kRescaleThreshold = 8.0f;   // log2 units (see fwd_bf16.cu)
 constexpr int kBlk = kDecodeBlockSize;      // 16 tokens per cache block
 constexpr int kTileBlocks = BN / kBlk;      // 8 cache blocks per key tile
 
-template <int D>
+// Shared memory: two Q tile buffers, a ring of `kSlots` key or value tiles (K of
+// tile 0, V of tile 0, K of tile 1, ...), output staging (packed), barriers and
+// the item ring, then the cached sequence bounds.  Both Q buffers and the tile
+// ring are first in, first out across items: a one-tile item's Q may arrive while
+// the one before is still in use.  The paged kernel, which often waits on HBM with
+// one short query tile, has a fifth slot in place of the staging.
+template <int D, bool PAGED>
 struct Cfg {
-  static constexpr int kStages = D == 64 ? 4 : 2;   // K and V ring depth
+  static constexpr int kSlots = D == 64 ? 8 : (PAGED ? 5 : 4);
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = BM * D * 2;
   static constexpr int kBoxBytes = BM * 128;
   static constexpr int kQ = 0;
-  static constexpr int kK0 = kQ + 2 * kTileBytes;
-  static constexpr int kV0 = kK0 + kStages * kTileBytes;
-  static constexpr int kStage = kV0 + kStages * kTileBytes;   // 8 x 4 KB of output staging
-  static constexpr int kBar = kStage + 8 * 4096;
-  static constexpr int kBytes = kBar + 1024;
-  static constexpr int kAlloc = kBytes + 1024;
+  static constexpr int kRing = kQ + 2 * kTileBytes;
+  static constexpr int kStage = kRing + kSlots * kTileBytes;   // 8 x 4 KB
+  static constexpr int kBar = kStage + (PAGED ? 0 : 8 * 4096);
+  static constexpr int kAlloc = kBar + 3072;
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
   static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
 };
 
+constexpr int kMaxSlots = 8;
 enum : int {
-  kBarQFull = 0,       // + tile
-  kBarQEmpty = 2,      // + tile
+  kBarQFull = 0,       // + Q buffer (2)
+  kBarQEmpty = 2,      // + Q buffer (2)
   kBarSFull = 4,       // + tile
   kBarPReady = 6,      // + 2 * tile + half, 4 warps
   kBarODone = 10,      // + tile
   kBarDrain = 12,
   kBarItemFull = 13,   // + ring slot (2)
   kBarItemEmpty = 15,  // + ring slot (2)
-  kBarKFull = 17,      // + stage (up to 4)
-  kBarKEmpty = 21,
-  kBarVFull = 25,
-  kBarVEmpty = 29,
-  kBarVFix = 33,       // the stage's ragged V tile has been cleared past the sequence; one
-                       // barrier per stage, as a single one could be two phases ahead of
-                       // the MMA warp's wait
-  kNumBars = 37
+  kBarFull = 17,       // + slot: the key or value tile has landed
+  kBarEmpty = kBarFull + kMaxSlots,   // + slot: its MMAs are done, the clearing warp has seen it
+  kBarFix = kBarEmpty + kMaxSlots,    // + slot: a ragged value tile has been cleared past the
+                                      // sequence; one barrier per slot, as a single one could be
+                                      // two phases ahead of the MMA warp's wait
+  kNumBars = kBarFix + kMaxSlots
 };
 // Arrivals that free an item slot: the MMA thread, the V-clearing warp and the
 // eight softmax warps.
@@ -117,15 +121,21 @@ struct Item {
   int kt0;           // first key tile of this partition
   int n[2];          // key tiles of tiles A and B in this partition
   int part;          // partition
-  int split[2];      // tile's rows go to the partition workspace
+  int split;         // the rows go to the partition workspace
 };
 
+constexpr int kCachedSeqs = 200;
 struct Misc {
   uint32_t tmem_base;
   int abort;
   Item item[2];
+  int2 seq[kCachedSeqs + 1];    // (first row, context length)
+  int first[kCachedSeqs + 1];   // items of the sequences before; [S]: of all
 };
-static_assert(8 * kNumBars + sizeof(Misc) <= 1024, "barrier area");
+static_assert(8 * kNumBars + sizeof(Misc) <= 3072, "barrier area");
+// Status latched when the dynamic shared memory does not start on a 1024-byte
+// boundary (the kernel then does nothing).
+constexpr int kDevBadSmemBase = -2;
 
 struct Args {
   uint16_t *o;
@@ -152,13 +162,12 @@ constexpr int kSeesAll = 0x3fffffff;
 struct Seq {
   int begin, n, kv_len, pos;
 };
-template <bool PAGED>
-__device__ __forceinline__ Seq sequence(const Args &a, int s) {
+__device__ __forceinline__ Seq make_seq(const Args &a, bool paged, int begin, int end, int ctx) {
   Seq q;
-  q.begin = clampi(a.cu_seqlens[s], 0, a.T);
-  q.n = clampi(a.cu_seqlens[s + 1], q.begin, a.T) - q.begin;
-  if (PAGED) {
-    q.kv_len = clampi(a.context_lens[s], 0, a.max_blocks * kBlk);
+  q.begin = begin;
+  q.n = max(end - begin, 0);
+  if (paged) {
+    q.kv_len = clampi(ctx, 0, a.max_blocks * kBlk);
     q.pos = q.kv_len - q.n;
   } else {
     q.kv_len = q.n;
@@ -166,34 +175,94 @@ __device__ __forceinline__ Seq sequence(const Args &a, int s) {
   }
   return q;
 }
-
-// Item w (whole warp); false if it has no work.
+__device__ __forceinline__ int seq_begin(const Args &a, int s) {
+  return clampi(a.cu_seqlens[s], 0, a.T);
+}
 template <bool PAGED>
-__device__ __forceinline__ bool decode_item(const Args &a, int w, Item &it) {
-  const int tb = 2 * a.tpb;
-  it.kvh = w % a.Hk;
-  const int r = w / a.Hk;
-  it.part = r % a.n_split;
-  const int vb = a.n_vblocks - 1 - r / a.n_split;
-  const int s = warp_search(
-      a.S, vb, [&](int i) { return clampi(a.cu_seqlens[i], 0, a.T) / tb + i; });
-  if (s < 0) return false;
-  const Seq q = sequence<PAGED>(a, s);
-  const int tok0 = (vb - q.begin / tb - s) * tb;
-  if (tok0 < 0 || tok0 >= q.n) return false;
+__device__ __forceinline__ Seq global_seq(const Args &a, int s) {
+  return make_seq(a, PAGED, seq_begin(a, s), seq_begin(a, s + 1), PAGED ? a.context_lens[s] : 0);
+}
+
+// Partitions of a sequence's blocks: as many as part_tiles fits into its context,
+// to the nearest, so that none is cut to leave a small rest.  Each block cuts its
+// own key tiles into that many.
+__device__ __forceinline__ int parts_of(const Args &a, const Seq &q) {
+  const int total = tiles_for(q.n, q.pos + q.n - 1, q.kv_len);
+  return clampi((2 * total + a.part_tiles) / (2 * a.part_tiles), 1, a.n_split);
+}
+__device__ __forceinline__ int part_size(int total, int parts) {
+  return max(1, (total + parts - 1) / parts);
+}
+
+// Numbers the items of all sequences (one warp): Misc::seq -> Misc::first.
+template <bool PAGED>
+__device__ __forceinline__ void number_items(const Args &a, Misc *m) {
+  const int lane = threadIdx.x & 31, tb = 2 * a.tpb;
+  int carry = 0;
+  for (int base = 0; base < a.S; base += 32) {
+    const int i = base + lane;
+    int n = 0;
+    if (i < a.S) {
+      const Seq q = make_seq(a, PAGED, m->seq[i].x, m->seq[i + 1].x, m->seq[i].y);
+      n = (q.n + tb - 1) / tb * parts_of(a, q) * a.Hk;
+    }
+    int sum = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int x = __shfl_up_sync(~0u, sum, off);
+      if (lane >= off) sum += x;
+    }
+    if (i < a.S) m->first[i] = carry + sum - n;
+    carry += __shfl_sync(~0u, sum, 31);
+  }
+  if (lane == 0) m->first[a.S] = carry;
+}
+
+// Item w of n_items (whole warp); false if it has no work.  m: the numbered
+// sequences, or null.
+template <bool PAGED>
+__device__ __forceinline__ bool decode_item(const Args &a, const Misc *m, int n_items, int w,
+                                            Item &it) {
+  const int tb = 2 * a.tpb, u = n_items - 1 - w;
+  int s, blk, parts;
+  Seq q;
+  if (m != nullptr) {
+    s = warp_search(a.S, u, [&](int i) { return m->first[i]; });
+    q = make_seq(a, PAGED, m->seq[s].x, m->seq[s + 1].x, m->seq[s].y);
+    parts = parts_of(a, q);
+    const int r = u - m->first[s];
+    it.kvh = r % a.Hk;
+    it.part = r / a.Hk % parts;
+    blk = r / a.Hk / parts;
+  } else {
+    it.kvh = u % a.Hk;
+    it.part = u / a.Hk % a.n_split;
+    const int vb = u / a.Hk / a.n_split;
+    s = warp_search(a.S, vb, [&](int i) { return seq_begin(a, i) / tb + i; });
+    if (s < 0) return false;
+    q = global_seq<PAGED>(a, s);
+    parts = parts_of(a, q);
+    blk = vb - q.begin / tb - s;
+    if (blk < 0 || it.part >= parts) return false;
+  }
+  const int tok0 = blk * tb;
+  if (tok0 >= q.n) return false;
   it.live = 1;
   it.row0 = q.begin + tok0;
   it.pos0 = q.pos + tok0;
   it.kv_len = q.kv_len;
   it.kv0 = PAGED ? s : q.begin;
-  it.kt0 = it.part * a.part_tiles;
+  int total[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     it.n_tok[t] = clampi(q.n - tok0 - t * a.tpb, 0, a.tpb);
-    const int total = tiles_for(it.n_tok[t], it.pos0 + t * a.tpb + it.n_tok[t] - 1, q.kv_len);
-    it.n[t] = clampi(total - it.kt0, 0, a.part_tiles);
-    it.split[t] = total > a.part_tiles;
+    total[t] = tiles_for(it.n_tok[t], it.pos0 + t * a.tpb + it.n_tok[t] - 1, q.kv_len);
   }
+  const int size = part_size(max(total[0], total[1]), parts);
+  it.split = parts > 1;
+  it.kt0 = it.part * size;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) it.n[t] = clampi(total[t] - it.kt0, 0, size);
   return it.part == 0 || it.n[0] > 0 || it.n[1] > 0;
 }
 
@@ -275,18 +344,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     fwd_packed_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const Args a) {
-  using C = Cfg<D>;
+  using C = Cfg<D, PAGED>;
   static_assert(!PAGED || (D == 128 && !F16), "the paged cache is bf16, d = 128");
-  constexpr int S = C::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  constexpr int R = C::kSlots;
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t s_base = smem_u32(smem);
+  if ((s_base & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicExch(a.dev_status, kDevBadSmemBase);
+    return;
+  }
   const uint32_t bars = s_base + C::kBar;
   auto bar = [&](int i) { return bars + 8u * i; };
   Misc *misc = reinterpret_cast<Misc *>(smem + C::kBar + 8 * kNumBars);
   volatile int *abort_flag = &misc->abort;
-  const int n_items = a.n_vblocks * a.n_split * a.Hk;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // Consumer side of the item ring.  take_item waits for entry k (whole warp, or
@@ -316,12 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(kBarItemEmpty + t), kItemConsumers);
     }
     mbar_init(bar(kBarDrain), 1);
-    for (int s = 0; s < S; ++s) {
-      mbar_init(bar(kBarKFull + s), 1);
-      mbar_init(bar(kBarKEmpty + s), 1);
-      mbar_init(bar(kBarVFull + s), 1);
-      mbar_init(bar(kBarVEmpty + s), 2);   // P V done, and seen by the clearing warp
-      mbar_init(bar(kBarVFix + s), 1);
+    for (int s = 0; s < R; ++s) {
+      mbar_init(bar(kBarFull + s), 1);
+      mbar_init(bar(kBarEmpty + s), 2);
+      mbar_init(bar(kBarFix + s), 1);
     }
     misc->abort = 0;
     fence_barrier_init();
@@ -339,6 +407,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // may be scheduled from here on; it waits for this grid in turn.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (PAGED && threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const bool cached = a.S <= kCachedSeqs;
+  if (cached)
+    for (int i = threadIdx.x; i <= a.S; i += kThreads)
+      misc->seq[i] = make_int2(seq_begin(a, i), PAGED && i < a.S ? a.context_lens[i] : 0);
+  __syncthreads();
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsProducer));
@@ -351,7 +424,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
       }
-      int kv = 0, nk = 0, nv = 0, nq[2] = {0, 0};
+      if (cached) {
+        number_items<PAGED>(a, misc);
+        __syncwarp();
+      }
+      const Misc *numbered = cached ? misc : nullptr;
+      const int n_items = cached ? misc->first[a.S] : a.n_vblocks * a.n_split * a.Hk;
+      int e = 0, nq = 0;        // tiles and Q tiles copied so far
       bool ok = true;
       int w = blockIdx.x;       // the first item is the CTA's own; the rest are claimed
       int w_claim = 0;          // lane 0: the claim in flight
@@ -375,11 +454,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             nxt.live = 0;
             return;
           }
-          if (decode_item<PAGED>(a, w, nxt)) break;
+          if (decode_item<PAGED>(a, numbered, n_items, w, nxt)) break;
           claim();
           w = claimed();
         }
         if (PAGED) nxt_id = ids_of(nxt, nxt.kt0);
+      };
+      // Waits (lane 0) for ring slot e % R to be free and announces its copy.
+      auto open_slot = [&]() -> bool {
+        bool good = true;
+        if (lane == 0) {
+          good = mbar_wait(bar(kBarEmpty + e % R), ((e / R) & 1) ^ 1, abort_flag);
+          if (good) mbar_arrive_expect_tx(bar(kBarFull + e % R), C::kTileBytes);
+        }
+        return __shfl_sync(~0u, good, 0);
       };
       find();
       for (int k = 0; ok; ++k) {
@@ -395,33 +483,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!(ok = __shfl_sync(~0u, ok, 0)) || !it.live) break;
         claim();
-        bool looked = false;
-        // Query tile t, once the last Q K^T of the tile before has read it.
+        // Query tile t into the next Q buffer, once the last Q K^T of the tile
+        // that was there has read it.
         auto load_q = [&](int t) -> bool {
           if (it.n[t] == 0) return true;
           bool good = true;
+          const int buf = nq & 1;
           if (lane == 0) {
-            good = mbar_wait(bar(kBarQEmpty + t), (nq[t] & 1) ^ 1, abort_flag);
+            good = mbar_wait(bar(kBarQEmpty + buf), ((nq >> 1) & 1) ^ 1, abort_flag);
             if (good) {
-              mbar_arrive_expect_tx(bar(kBarQFull + t), a.G * a.tpb * D * 2);
+              mbar_arrive_expect_tx(bar(kBarQFull + buf), a.G * a.tpb * D * 2);
               for (int b = 0; b < C::kBoxes; ++b)
-                tma_load_3d(s_base + C::kQ + t * C::kTileBytes + b * C::kBoxBytes, &tm_q, b * 64,
-                            it.kvh * a.G, it.row0 + t * a.tpb, bar(kBarQFull + t));
+                tma_load_3d(s_base + C::kQ + buf * C::kTileBytes + b * C::kBoxBytes, &tm_q, b * 64,
+                            it.kvh * a.G, it.row0 + t * a.tpb, bar(kBarQFull + buf));
             }
           }
           good = __shfl_sync(~0u, good, 0);
-          if (good) ++nq[t];
+          if (good) ++nq;
           return good;
         };
-        if (!(ok = load_q(0))) break;
         const int n_max = max(it.n[0], it.n[1]);
-        if (n_max == 0 && !(ok = load_q(1))) break;
-        for (int j = 0; j < n_max; ++j, ++kv) {
-          const int st = kv % S;
-          const uint32_t ph = (kv / S) & 1;
+        for (int j = 0; j < n_max; ++j) {
           const int tile = it.kt0 + j;
-          const uint32_t k_dst = s_base + C::kK0 + st * C::kTileBytes;
-          const uint32_t v_dst = s_base + C::kV0 + st * C::kTileBytes;
           int pb = 0;
           if (PAGED) {
             if ((j & 3) == 0) {
@@ -430,47 +513,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             pb = __shfl_sync(~0u, ids, (j & 3) * kTileBlocks + (lane & 7));
           }
-          if (lane == 0) {
-            ok = mbar_wait(bar(kBarKEmpty + st), ph ^ 1, abort_flag);
-            if (ok) mbar_arrive_expect_tx(bar(kBarKFull + st), C::kTileBytes);
-          }
-          if (!(ok = __shfl_sync(~0u, ok, 0))) break;
+          if (!(ok = open_slot())) break;
+          const uint32_t k_dst = s_base + C::kRing + (e % R) * C::kTileBytes;
+          const uint32_t k_bar = bar(kBarFull + e % R);
           if (PAGED) {
             if (lane < kTileBlocks) {
-              tma_load_5d(k_dst + lane * 4096, &tm_k, 0, 0, 0, it.kvh, pb, bar(kBarKFull + st));
-              tma_load_5d(k_dst + lane * 4096 + 2048, &tm_k, 0, 1, 0, it.kvh, pb,
-                          bar(kBarKFull + st));
+              tma_load_5d(k_dst + lane * 4096, &tm_k, 0, 0, 0, it.kvh, pb, k_bar);
+              tma_load_5d(k_dst + lane * 4096 + 2048, &tm_k, 0, 1, 0, it.kvh, pb, k_bar);
             }
           } else if (lane == 0) {
             for (int b = 0; b < C::kBoxes; ++b)
               tma_load_3d(k_dst + b * C::kBoxBytes, &tm_k, b * 64, it.kv0 + tile * BN, it.kvh,
-                          bar(kBarKFull + st));
+                          k_bar);
           }
-          nk = kv + 1;
-          if (j == 0 && !(ok = load_q(1))) break;
-          if (lane == 0) {
-            ok = mbar_wait(bar(kBarVEmpty + st), ph ^ 1, abort_flag);
-            if (ok) mbar_arrive_expect_tx(bar(kBarVFull + st), C::kTileBytes);
-          }
-          if (!(ok = __shfl_sync(~0u, ok, 0))) break;
+          ++e;
+          if (j == 0 && !(ok = load_q(0) && load_q(1))) break;
+          if (!(ok = open_slot())) break;
+          const uint32_t v_dst = s_base + C::kRing + (e % R) * C::kTileBytes;
+          const uint32_t v_bar = bar(kBarFull + e % R);
           if (PAGED) {
             if (lane < kTileBlocks)
-              tma_load_4d(v_dst + lane * 4096, &tm_v, 0, 0, it.kvh, pb, bar(kBarVFull + st));
+              tma_load_4d(v_dst + lane * 4096, &tm_v, 0, 0, it.kvh, pb, v_bar);
           } else if (lane == 0) {
             for (int b = 0; b < C::kBoxes; ++b)
               tma_load_3d(v_dst + b * C::kBoxBytes, &tm_v, b * 64, it.kv0 + tile * BN, it.kvh,
-                          bar(kBarVFull + st));
+                          v_bar);
           }
-          nv = kv + 1;
-          if (j == 0) {
-            // With the first tile's copies under way: the next item.
+          ++e;
+          if (j == min(1, n_max - 1)) {
+            // With the ring filled: the next item.
             w = claimed();
             find();
-            looked = true;
           }
         }
         if (!ok) break;
-        if (!looked) {
+        if (n_max == 0) {
           w = claimed();
           find();
         }
@@ -480,12 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok && claimed() < 0) *abort_flag = 1;
       if (!ok && lane == 0) {
         // Let the copies in flight land before the CTA exits.
-        for (int t = 0; t < 2; ++t)
-          if (nq[t] > 0) drain_wait(bar(kBarQFull + t), (nq[t] - 1) & 1);
-        for (int i = (nk > S ? nk - S : 0); i < nk; ++i)
-          drain_wait(bar(kBarKFull + i % S), (i / S) & 1);
-        for (int i = (nv > S ? nv - S : 0); i < nv; ++i)
-          drain_wait(bar(kBarVFull + i % S), (i / S) & 1);
+        for (int i = (nq > 2 ? nq - 2 : 0); i < nq; ++i)
+          drain_wait(bar(kBarQFull + (i & 1)), (i >> 1) & 1);
+        for (int i = (e > R ? e - R : 0); i < e; ++i)
+          drain_wait(bar(kBarFull + i % R), (i / R) & 1);
       }
     } else if (warp == 1 && elect_one()) {
       // ---------------------------------------------------------- MMA issuer
@@ -494,11 +569,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t k_hi = PAGED ? kHiPagedK : kSdescHi1024;
       constexpr uint32_t v_hi = PAGED ? kHiPagedV : kSdescHi1024;
       const uint32_t dq = sdesc_lo(s_base + C::kQ, 16);
-      const uint32_t dk = sdesc_lo(s_base + C::kK0, PAGED ? 128 : 16);
-      const uint32_t dv = sdesc_lo(s_base + C::kV0, PAGED ? 16 : C::kBoxBytes);
-      auto qk = [&](int t, int kvi) {
-        const uint32_t qa = dq + ((t * C::kTileBytes) >> 4);
-        const uint32_t kb = dk + (((kvi % S) * C::kTileBytes) >> 4);
+      const uint32_t dk = sdesc_lo(s_base + C::kRing, PAGED ? 128 : 16);
+      const uint32_t dv = sdesc_lo(s_base + C::kRing, PAGED ? 16 : C::kBoxBytes);
+      // Tile kvi's keys are entry 2 kvi of the ring, its values 2 kvi + 1.
+      auto wait_full = [&](int e) {
+        return mbar_wait(bar(kBarFull + e % R), (e / R) & 1, abort_flag);
+      };
+      // S_t = Q_t K^T with Q tile qi (buffer qi & 1); `last`: Q is not needed again.
+      auto qk = [&](int t, int qi, int kvi, bool last) -> bool {
+        if (!wait_full(2 * kvi)) return false;
+        tc_fence_after();
+        const uint32_t qa = dq + (((qi & 1) * C::kTileBytes) >> 4);
+        const uint32_t kb = dk + ((((2 * kvi) % R) * C::kTileBytes) >> 4);
         const uint32_t s_col = tmem + (t ? C::kColS1 : C::kColS0);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
@@ -507,10 +589,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     kk > 0 ? 1u : 0u);
         }
         mma_commit(bar(kBarSFull + t));
+        if (last) mma_commit(bar(kBarQEmpty + (qi & 1)));
+        return true;
       };
       // Half h of O_T += P_T V: keys 64h .. 64h + 63 of the tile.
       auto pv = [&](int t, int kvi, bool first, int h) {
-        const uint32_t vb = dv + (((kvi % S) * C::kTileBytes) >> 4);
+        const uint32_t vb = dv + ((((2 * kvi + 1) % R) * C::kTileBytes) >> 4);
         const uint32_t s_col = tmem + (t ? C::kColS1 : C::kColS0);
         const uint32_t o_col = tmem + (t ? C::kColO1 : C::kColO0);
 #pragma unroll
@@ -518,21 +602,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_ts_hi(o_col, s_col + kk * 8, vb + ((kk * (PAGED ? 4096 : 2048)) >> 4), v_hi,
                     idesc_pv, (!first || kk > 0) ? 1u : 0u);
       };
-      auto wait_k = [&](int kvi) {
-        return mbar_wait(bar(kBarKFull + kvi % S), (kvi / S) & 1, abort_flag);
+      int nq = 0, np[2] = {0, 0}, kv = 0;
+      uint32_t fix_parity = 0;   // bit: ring slot
+      // First Q K^T of an item's tile t: takes the next Q tile.
+      auto first_qk = [&](int t, int n, int kvi, int &qi) -> bool {
+        qi = nq++;
+        if (!mbar_wait(bar(kBarQFull + (qi & 1)), (qi >> 1) & 1, abort_flag)) return false;
+        return qk(t, qi, kvi, n == 1);
       };
-      int nq[2] = {0, 0}, np[2] = {0, 0}, kv = 0;
-      uint32_t fix_parity = 0;   // bit: stage
-      // First Q K^T of an item for tile t; key tile kvi has to be kept for it.
-      auto first_qk = [&](int t, int n, int kvi) -> bool {
-        if (!mbar_wait(bar(kBarQFull + t), nq[t] & 1, abort_flag) || !wait_k(kvi)) return false;
-        ++nq[t];
-        tc_fence_after();
-        qk(t, kvi);
-        if (n == 1) mma_commit(bar(kBarQEmpty + t));
-        return true;
-      };
-      // P V of step j and, if there is one, Q K^T of the next.
+      // P V of step j.
       auto pv_step = [&](int t, int n, int j, int kvj) -> bool {
         for (int h = 0; h < 2; ++h) {
           if (!mbar_wait(bar(kBarPReady + 2 * t + h), np[t] & 1, abort_flag)) return false;
@@ -541,14 +619,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ++np[t];
         if (j == n - 1) mma_commit(bar(kBarODone + t));
-        return true;
-      };
-      auto next_qk = [&](int t, int n, int j, int kvj) -> bool {
-        if (j + 1 >= n) return true;
-        if (!wait_k(kvj + 1)) return false;
-        tc_fence_after();
-        qk(t, kvj + 1);
-        if (j + 2 == n) mma_commit(bar(kBarQEmpty + t));
         return true;
       };
       // An item as the issuer sees it: key tiles of A and B, and which of them
@@ -565,38 +635,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       Work it, nx;
+      int qa = 0, qb = 0;       // Q tiles of the item's A and B
+      int qa_next = 0;
       bool a0_issued = false;   // the item's first Q K^T of tile A went out a step early
       bool ok = fetch(0, it);
       for (int k = 0; ok && it.live; ++k) {
         const int n_max = max(it.n_a, it.n_b);
-        if (it.n_a > 0 && !a0_issued && !(ok = first_qk(0, it.n_a, kv))) break;
+        if (a0_issued)
+          qa = qa_next;
+        else if (it.n_a > 0 && !(ok = first_qk(0, it.n_a, kv, qa)))
+          break;
         a0_issued = false;
-        if (it.n_b > 0 && !(ok = first_qk(1, it.n_b, kv))) break;
-        if (n_max > 0) mma_commit(bar(kBarKEmpty + kv % S));
+        if (it.n_b > 0 && !(ok = first_qk(1, it.n_b, kv, qb))) break;
+        if (n_max > 0) mma_commit(bar(kBarEmpty + (2 * kv) % R));
         bool fetched = false;
         for (int j = 0; j < n_max; ++j) {
-          const int kvj = kv + j, st = kvj % S;
+          const int kvj = kv + j, ev = 2 * kvj + 1, sv = ev % R;
           if (j == it.ragged) {
-            if (!(ok = mbar_wait(bar(kBarVFix + st), (fix_parity >> st) & 1, abort_flag))) break;
-            fix_parity ^= 1u << st;
-          } else if (!(ok = mbar_wait(bar(kBarVFull + st), (kvj / S) & 1, abort_flag))) {
+            if (!(ok = mbar_wait(bar(kBarFix + sv), (fix_parity >> sv) & 1, abort_flag))) break;
+            fix_parity ^= 1u << sv;
+          } else if (!(ok = wait_full(ev))) {
             break;
           }
-          if (j < it.n_a && !(ok = pv_step(0, it.n_a, j, kvj) && next_qk(0, it.n_a, j, kvj)))
-            break;
+          if (j < it.n_a) {
+            if (!(ok = pv_step(0, it.n_a, j, kvj))) break;
+            if (j + 1 < it.n_a && !(ok = qk(0, qa, kvj + 1, j + 2 == it.n_a))) break;
+          }
           if (j == n_max - 1) {
             // S_A is free: the next item's tile A starts now.
             if (!(ok = fetch(k + 1, nx))) break;
             fetched = true;
             if (nx.live && nx.n_a > 0) {
-              if (!(ok = first_qk(0, nx.n_a, kv + n_max))) break;
+              if (!(ok = first_qk(0, nx.n_a, kv + n_max, qa_next))) break;
               a0_issued = true;
             }
           }
           if (j < it.n_b && !(ok = pv_step(1, it.n_b, j, kvj))) break;
-          mma_commit(bar(kBarVEmpty + st));
-          if (j < it.n_b && !(ok = next_qk(1, it.n_b, j, kvj))) break;
-          if (j + 1 < n_max) mma_commit(bar(kBarKEmpty + (kvj + 1) % S));
+          mma_commit(bar(kBarEmpty + sv));
+          if (j + 1 < it.n_b && !(ok = qk(1, qb, kvj + 1, j + 2 == it.n_b))) break;
+          if (j + 1 < n_max) mma_commit(bar(kBarEmpty + (2 * kvj + 2) % R));
         }
         if (!ok) break;
         kv += n_max;
@@ -608,21 +685,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain_wait(bar(kBarDrain), 0);
     } else if (warp == 2) {
       // ------------------------------------- V rows past the sequence's keys
-      int kv = 0;
+      int e = 0;
       for (int k = 0; take_item(k, true); ++k) {
         const volatile Item &it = item_of(k);
         const int live = it.live, n_max = max(it.n[0], it.n[1]), kv_len = it.kv_len;
         const int ragged = ragged_tile(kv_len) - it.kt0;
         free_item(k, true);
         if (!live) break;
-        // The warp follows every V tile and takes part in freeing it, so that
-        // the ring cannot run past the phase that it waits for.
+        // The warp follows every tile and takes part in freeing it, so that the
+        // ring cannot run past the phase that it waits for.
         bool ok = true;
-        for (int j = 0; j < n_max; ++j, ++kv) {
-          const int st = kv % S;
-          if (!(ok = wait_warp(bar(kBarVFull + st), (kv / S) & 1, abort_flag))) break;
-          if (j == ragged) {
-            uint8_t *v = smem + C::kV0 + st * C::kTileBytes;
+        for (int j = 0; j < 2 * n_max; ++j, ++e) {
+          const int st = e % R;
+          if (!(ok = wait_warp(bar(kBarFull + st), (e / R) & 1, abort_flag))) break;
+          if (j == 2 * ragged + 1) {
+            uint8_t *v = smem + C::kRing + st * C::kTileBytes;
             const int keep = kv_len % BN;
             if (PAGED) {
               // Only the block that the context ends in: the later ones of the
@@ -644,9 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarVFix + st));
+            if (lane == 0) mbar_arrive(bar(kBarFix + st));
           }
-          if (lane == 0) mbar_arrive(bar(kBarVEmpty + st));
+          if (lane == 0) mbar_arrive(bar(kBarEmpty + st));
         }
         if (!ok) break;
       }
@@ -669,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = take_item(k, true))) break;
       const volatile Item &it = item_of(k);
       const int live = it.live, n_mine = it.n[t], part = it.part;
-      const bool split = it.split[t] != 0;
+      const bool split = it.split != 0;
       // Keys below lim are visible to this row; a tile needs the test only
       // where it passes the limit of the query tile's first token.
       const int tile_pos = it.pos0 + t * a.tpb, key0 = it.kt0 * BN;
@@ -768,30 +845,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n_done;
         tc_fence_after();
       }
-      if (split) {
-        // Unnormalised fp32 rows, through this warp's staging 32 columns (128
-        // bytes a row) at a time, so that eight lanes store one row's line.
+      if (PAGED && split) {
+        // Unnormalised fp32 rows, a thread's own row from its registers (the few
+        // rows of a split block do not repay staging them).
         const int64_t base = static_cast<int64_t>(part) * a.T * a.H;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t ov[32];
           tmem_ld32(o_tmem + c * 32, ov);
           tmem_wait_ld(ov);
+          if (my_out >= 0) {
+            uint4 *dst = reinterpret_cast<uint4 *>(a.ws_o + (base + my_out) * D + c * 32);
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<uint4 *>(stg + lane * 128 + ((q ^ (lane & 7)) * 16)) =
-                make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int rr = (lane >> 3) + 4 * q, ch = lane & 7;
-            const uint4 v =
-                *reinterpret_cast<const uint4 *>(stg + rr * 128 + ((ch ^ (rr & 7)) * 16));
-            const int out_row = __shfl_sync(~0u, my_out, rr);
-            if (out_row >= 0)
-              *reinterpret_cast<uint4 *>(a.ws_o + (base + out_row) * D + c * 32 + ch * 4) = v;
+            for (int q = 0; q < 8; ++q)
+              dst[q] = make_uint4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
           }
-          __syncwarp();
         }
         if (my_out >= 0) a.ws_ml[base + my_out] = make_float2(m, l);
         continue;
@@ -816,8 +884,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           v.w = pack2<F16>(__uint_as_float(c8[6]) * inv_l, __uint_as_float(c8[7]) * inv_l);
           // A row that saw no key is zero whatever its accumulator holds.
           if (l == 0.f) v = make_uint4(0u, 0u, 0u, 0u);
-          *reinterpret_cast<uint4 *>(stg + lane * 128 + ((q ^ (lane & 7)) * 16)) = v;
+          if (!PAGED)
+            *reinterpret_cast<uint4 *>(stg + lane * 128 + ((q ^ (lane & 7)) * 16)) = v;
+          else if (my_out >= 0)
+            *reinterpret_cast<uint4 *>(a.o + static_cast<int64_t>(my_out) * D + 64 * h + q * 8) = v;
         }
+        if (PAGED) continue;
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
@@ -866,14 +938,16 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const Args a) {
   // The sequence that owns the token: the last one that begins at or before it.
   const int s = warp_search(a.S, tok, [&](int i) { return clampi(a.cu_seqlens[i], 0, a.T); });
   if (s < 0) return;
-  const Seq q = sequence<true>(a, s);
+  const Seq q = global_seq<true>(a, s);
   const int i = tok - q.begin;
   if (i >= q.n) return;                                  // rows behind the last sequence
-  const int u0 = i / a.tpb * a.tpb;                      // first token of its query tile
-  const int last = min(u0 + a.tpb, q.n) - 1;
-  if (tiles_for(1, q.pos + last, q.kv_len) <= a.part_tiles) return;   // written directly
+  const int cut = parts_of(a, q);
+  if (cut == 1) return;                                  // written directly
+  // The block's last token sets the partitions' size, the row's own those it is in.
+  const int last = min((i / (2 * a.tpb) + 1) * 2 * a.tpb, q.n) - 1;
+  const int size = part_size(tiles_for(1, q.pos + last, q.kv_len), cut);
   const int mine = tiles_for(1, q.pos + i, q.kv_len);    // key tiles this row sees
-  const int parts = (mine + a.part_tiles - 1) / a.part_tiles;
+  const int parts = (mine + size - 1) / size;
   const int64_t stride = static_cast<int64_t>(a.T) * a.H;
   float m = -INFINITY;
   for (int p = 0; p < parts; ++p) m = fmaxf(m, a.ws_ml[p * stride + row].x);
@@ -906,7 +980,7 @@ cudaError_t sm_count(int *n) {
 template <int D, bool F16, bool PAGED>
 cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, Args a,
                    cudaStream_t stream) {
-  using C = Cfg<D>;
+  using C = Cfg<D, PAGED>;
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
@@ -968,19 +1042,26 @@ cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, cons
              : launch<128, false, false>(tq, tk, tv, a, stream);
 }
 
-// Partitions of the context: enough items for about two rounds of the SMs, but
-// at least four key tiles (512 keys) each, below which a partition's fixed cost
-// (claim, Q, fp32 rows out and the merge) outweighs its keys.
+// Partition length, from what the host knows: the longest context's bound and the
+// average rows of a block.  With W key tiles of work per SM (in units of a block's
+// tile) cut into partitions of p, a partition's fixed cost c (its claim, Q and
+// start, and its rows' trip through the workspace: 1 KB a row, at an SM's share of
+// the HBM rate about 0.02 tiles) adds W c / p, and the SMs end up to p apart, 0.7 p
+// on average: p = sqrt(W c / 0.7) balances the two.  At least four key tiles (512
+// keys).
 PagedSplit paged_split(int T, int S, int Hk, int group, int max_blocks) {
-  constexpr int kTargetItems = 2 * 152, kMinTiles = 4;
-  const int tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;
-  const int64_t items = static_cast<int64_t>(packed_blocks(T, S, group)) * Hk;
-  int n = static_cast<int>(items >= kTargetItems ? 1 : (kTargetItems + items - 1) / items);
-  const int most = tiles / kMinTiles > 1 ? tiles / kMinTiles : 1;
-  if (n > most) n = most;
+  constexpr double kSms = 152;
+  const int64_t tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;
+  const int64_t blocks = packed_blocks(T, S, group);
+  const double work = static_cast<double>(blocks) * Hk * static_cast<double>(tiles) / kSms;
+  const double rows = static_cast<double>(T) * group / static_cast<double>(blocks);
+  int64_t part = static_cast<int64_t>(std::sqrt(work * (1.5 + 0.02 * rows) / 0.7));
+  if (part < 4) part = 4;
+  if (part > tiles) part = tiles;
   PagedSplit s;
-  s.part_tiles = (tiles + n - 1) / n;
-  s.n_split = (tiles + s.part_tiles - 1) / s.part_tiles;
+  s.part_tiles = static_cast<int>(part);
+  const int64_t n = (2 * tiles + part) / (2 * part);
+  s.n_split = static_cast<int>(n < 1 ? 1 : n);
   return s;
 }
 
