@@ -24,12 +24,13 @@
 //    G does not divide 128 the last rows of the tile hold no query.
 //  * Sequence bounds are device data.  An item is (block of two tiles, context
 //    partition, key/value head).  Up to kCachedSeqs sequences, each CTA reads the
-//    bounds once and numbers the items densely with a prefix sum in shared memory;
-//    beyond, sequence s starts at block cu_seqlens[s] / (2 * 128/G) + s, which
-//    needs no prefix sum and leaves some numbers unused.  The producer warp finds
-//    an item's sequence by a 32-way search and hands the decoded item to the other
-//    roles.  Items are numbered from the last block down, so that every sequence's
-//    heaviest causal blocks come first and the call ends with its lightest.
+//    bounds once, sorts the sequences by their heaviest item and numbers all items
+//    with a prefix sum in shared memory, heaviest sequence first and within a
+//    sequence from its last block (the heaviest under the causal mask) down, so
+//    that the call ends with its lightest items; beyond, sequence s starts at block
+//    cu_seqlens[s] / (2 * 128/G) + s, which needs no prefix sum and leaves some
+//    numbers unused.  The producer warp finds an item's sequence by a 32-way
+//    search and hands the decoded item to the other roles.
 //  * The key tile that a sequence ends in also holds the next sequence's rows
 //    (packed) or whatever the cache slots past the context hold (paged).  Their
 //    scores are set to -inf, and since a zero weight does not cancel a NaN, a
@@ -41,8 +42,8 @@
 //    cache read as zeros.
 //  * Few rows over long contexts do not fill the GPU, and a long context beside
 //    short ones would finish alone: a block's context is then cut into equal
-//    partitions of about `part_tiles` key tiles; each writes its unnormalised
-//    fp32 rows and (max, sum), and paged_merge_kernel joins them (eq. (4)).
+//    partitions (parts_of); each writes its unnormalised fp32 rows and (max, sum),
+//    and paged_merge_kernel joins them (eq. (4)).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -124,13 +125,19 @@ struct Item {
   int split;         // the rows go to the partition workspace
 };
 
-constexpr int kCachedSeqs = 200;
+constexpr int kCachedSeqs = 112;
 struct Misc {
   uint32_t tmem_base;
   int abort;
   Item item[2];
   int2 seq[kCachedSeqs + 1];    // (first row, context length)
-  int first[kCachedSeqs + 1];   // items of the sequences before; [S]: of all
+  // By weight of their items, lightest first: the sequences, their partitions, and
+  // the items of those before ([S]: of all).
+  int first[kCachedSeqs + 1];
+  int16_t parts[kCachedSeqs];
+  uint8_t order[kCachedSeqs];
+  int key[kCachedSeqs];         // scratch of the sort
+  int16_t n_parts[kCachedSeqs];
 };
 static_assert(8 * kNumBars + sizeof(Misc) <= 3072, "barrier area");
 // Status latched when the dynamic shared memory does not start on a 1024-byte
@@ -146,7 +153,7 @@ struct Args {
   int *sched, *dev_status;
   int S, T, H, Hk, G, tpb;      // tpb: tokens per query tile, 128 / G
   int max_blocks, num_blocks;
-  int n_vblocks, n_split, part_tiles, causal;
+  int n_vblocks, n_split, causal;   // n_split: most partitions of a context
   float scale_log2;
 };
 
@@ -183,39 +190,93 @@ __device__ __forceinline__ Seq global_seq(const Args &a, int s) {
   return make_seq(a, PAGED, seq_begin(a, s), seq_begin(a, s + 1), PAGED ? a.context_lens[s] : 0);
 }
 
-// Partitions of a sequence's blocks: as many as part_tiles fits into its context,
-// to the nearest, so that none is cut to leave a small rest.  Each block cuts its
-// own key tiles into that many.
-__device__ __forceinline__ int parts_of(const Args &a, const Seq &q) {
-  const int total = tiles_for(q.n, q.pos + q.n - 1, q.kv_len);
-  return clampi((2 * total + a.part_tiles) / (2 * a.part_tiles), 1, a.n_split);
+// Work of a sequence: key tiles of its last block, and blocks.
+struct Work {
+  int tiles, blocks;
+};
+__device__ __forceinline__ Work work_of(const Args &a, const Seq &q) {
+  return {tiles_for(q.n, q.pos + q.n - 1, q.kv_len), (q.n + 2 * a.tpb - 1) / (2 * a.tpb)};
+}
+
+// Partitions.  With W key tiles of work per SM cut into partitions of p, a
+// partition's cost c (in key tiles: its start, and its rows' trip through the
+// workspace, 1 KB each at an SM's share of the HBM rate) adds W c / p, and the SMs
+// end up to p apart, 0.7 p on average: p = sqrt(W c / 0.7) balances the two, at
+// least four key tiles.  `work`: key tiles of the call's blocks, of one key/value
+// head.  Each block of the sequence cuts its own key tiles into that many.
+// (Roundings are spelled out: the merge kernel has to reach the same number.)
+__device__ __forceinline__ int parts_of(const Args &a, const Seq &q, int tiles, int64_t work) {
+  constexpr float kFixed = 3.f, kRow = 0.02f, kLeast = 4.f;
+  if (a.n_split == 1) return 1;
+  const float w = __fmul_rn(__ll2float_rn(work * a.Hk), 1.f / (152.f * 0.7f));
+  const float c = __fmaf_rn(kRow, static_cast<float>(min(q.n, 2 * a.tpb) * a.G), kFixed);
+  const float size = fmaxf(__fsqrt_rn(__fmul_rn(w, c)), kLeast);
+  return clampi(__float2int_rn(__fdiv_rn(static_cast<float>(tiles), size)), 1, a.n_split);
 }
 __device__ __forceinline__ int part_size(int total, int parts) {
   return max(1, (total + parts - 1) / parts);
 }
 
-// Numbers the items of all sequences (one warp): Misc::seq -> Misc::first.
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(~0u, v, off);
+  return v;
+}
+
+// Sorts the sequences and numbers their items (one warp): Misc::seq -> order, parts,
+// first.  Run once by a cold instruction cache: short code, not unrolled.
 template <bool PAGED>
 __device__ __forceinline__ void number_items(const Args &a, Misc *m) {
-  const int lane = threadIdx.x & 31, tb = 2 * a.tpb;
-  int carry = 0;
-  for (int base = 0; base < a.S; base += 32) {
-    const int i = base + lane;
-    int n = 0;
-    if (i < a.S) {
-      const Seq q = make_seq(a, PAGED, m->seq[i].x, m->seq[i + 1].x, m->seq[i].y);
-      n = (q.n + tb - 1) / tb * parts_of(a, q) * a.Hk;
+  const int lane = threadIdx.x & 31;
+  auto seq = [&](int i) {
+    return make_seq(a, PAGED, m->seq[i].x, m->seq[i + 1].x, m->seq[i].y);
+  };
+  int64_t work = 0;
+  if (PAGED && a.n_split > 1) {
+#pragma unroll 1
+    for (int i = lane; i < a.S; i += 32) {
+      const Work w = work_of(a, seq(i));
+      work += static_cast<int64_t>(w.tiles) * w.blocks;
     }
+    work = warp_sum(work);
+  }
+  // Key: key tiles of an item, then the index, so that no two are equal.
+#pragma unroll 1
+  for (int i = lane; i < a.S; i += 32) {
+    const Seq q = seq(i);
+    const int tiles = work_of(a, q).tiles;
+    const int parts = PAGED ? parts_of(a, q, tiles, work) : 1;
+    const int size = PAGED ? part_size(tiles, parts) : tiles;
+    m->key[i] = min(size, (1 << 23) - 1) * 128 + i;
+    m->n_parts[i] = static_cast<int16_t>(parts);
+  }
+  __syncwarp();
+#pragma unroll 1
+  for (int i = lane; i < a.S; i += 32) {
+    const int key = m->key[i];
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < a.S; ++j) rank += m->key[j] < key ? 1 : 0;
+    m->order[rank] = static_cast<uint8_t>(i);
+    m->parts[rank] = m->n_parts[i];
+    m->first[rank] = work_of(a, seq(i)).blocks * m->n_parts[i] * a.Hk;
+  }
+  __syncwarp();
+  int carry = 0;
+#pragma unroll 1
+  for (int base = 0; base < a.S; base += 32) {
+    const int n = base + lane < a.S ? m->first[base + lane] : 0;
     int sum = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int x = __shfl_up_sync(~0u, sum, off);
       if (lane >= off) sum += x;
     }
-    if (i < a.S) m->first[i] = carry + sum - n;
+    if (base + lane < a.S) m->first[base + lane] = carry + sum - n;
     carry += __shfl_sync(~0u, sum, 31);
   }
   if (lane == 0) m->first[a.S] = carry;
+  __syncwarp();
 }
 
 // Item w of n_items (whole warp); false if it has no work.  m: the numbered
@@ -224,26 +285,29 @@ template <bool PAGED>
 __device__ __forceinline__ bool decode_item(const Args &a, const Misc *m, int n_items, int w,
                                             Item &it) {
   const int tb = 2 * a.tpb, u = n_items - 1 - w;
-  int s, blk, parts;
+  int s, blk, parts = 1;
   Seq q;
+  it.part = 0;
   if (m != nullptr) {
-    s = warp_search(a.S, u, [&](int i) { return m->first[i]; });
+    const int at = warp_search(a.S, u, [&](int i) { return m->first[i]; });
+    s = m->order[at];
     q = make_seq(a, PAGED, m->seq[s].x, m->seq[s + 1].x, m->seq[s].y);
-    parts = parts_of(a, q);
-    const int r = u - m->first[s];
-    it.kvh = r % a.Hk;
-    it.part = r / a.Hk % parts;
-    blk = r / a.Hk / parts;
-  } else {
-    it.kvh = u % a.Hk;
-    it.part = u / a.Hk % a.n_split;
-    const int vb = u / a.Hk / a.n_split;
+    const int r = u - m->first[at];
+    blk = r / a.Hk;
+    it.kvh = r - blk * a.Hk;
+    if (PAGED && (parts = m->parts[at]) > 1) {
+      const int x = blk / parts;
+      it.part = blk - x * parts;
+      blk = x;
+    }
+  } else {   // contexts are not cut here: there are items enough
+    const int vb = u / a.Hk;
+    it.kvh = u - vb * a.Hk;
     s = warp_search(a.S, vb, [&](int i) { return seq_begin(a, i) / tb + i; });
     if (s < 0) return false;
     q = global_seq<PAGED>(a, s);
-    parts = parts_of(a, q);
     blk = vb - q.begin / tb - s;
-    if (blk < 0 || it.part >= parts) return false;
+    if (blk < 0) return false;
   }
   const int tok0 = blk * tb;
   if (tok0 >= q.n) return false;
@@ -426,10 +490,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (cached) {
         number_items<PAGED>(a, misc);
-        __syncwarp();
       }
       const Misc *numbered = cached ? misc : nullptr;
-      const int n_items = cached ? misc->first[a.S] : a.n_vblocks * a.n_split * a.Hk;
+      const int n_items = cached ? misc->first[a.S] : a.n_vblocks * a.Hk;
       int e = 0, nq = 0;        // tiles and Q tiles copied so far
       bool ok = true;
       int w = blockIdx.x;       // the first item is the CTA's own; the rest are claimed
@@ -623,10 +686,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // An item as the issuer sees it: key tiles of A and B, and which of them
       // (counted from the item's first) is the sequence's ragged one.
-      struct Work {
+      struct Step {
         int live, n_a, n_b, ragged;
       };
-      auto fetch = [&](int k, Work &x) -> bool {
+      auto fetch = [&](int k, Step &x) -> bool {
         if (!take_item(k, false)) return false;
         const volatile Item &i = item_of(k);
         x.live = i.live, x.n_a = i.n[0], x.n_b = i.n[1];
@@ -634,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         free_item(k, false);
         return true;
       };
-      Work it, nx;
+      Step it, nx;
       int qa = 0, qb = 0;       // Q tiles of the item's A and B
       int qa_next = 0;
       bool a0_issued = false;   // the item's first Q K^T of tile A went out a step early
@@ -926,48 +989,53 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the partitions of the rows whose tile was split: one warp per (token,
-// head), four dimensions a lane.
+// Joins the partitions of the rows whose context was cut: gridDim.y blocks per
+// sequence (which end at once if it was not), one warp per (token, head), four
+// dimensions a lane.
 __global__ void __launch_bounds__(256) paged_merge_kernel(const Args a) {
   constexpr int D = kDecodeHeadSize;
+  // The next kernel of the stream may be scheduled: it waits for this grid.
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  // The call's work, as number_items adds it up (every warp for itself).
   const int lane = threadIdx.x & 31;
-  if (row >= static_cast<int64_t>(a.T) * a.H) return;   // whole warps
-  const int tok = static_cast<int>(row / a.H);
-  // The sequence that owns the token: the last one that begins at or before it.
-  const int s = warp_search(a.S, tok, [&](int i) { return clampi(a.cu_seqlens[i], 0, a.T); });
-  if (s < 0) return;
-  const Seq q = global_seq<true>(a, s);
-  const int i = tok - q.begin;
-  if (i >= q.n) return;                                  // rows behind the last sequence
-  const int cut = parts_of(a, q);
+  int64_t work = 0;
+  for (int i = lane; i < a.S; i += 32) {
+    const Work w = work_of(a, global_seq<true>(a, i));
+    work += static_cast<int64_t>(w.tiles) * w.blocks;
+  }
+  work = warp_sum(work);
+  const Seq q = global_seq<true>(a, blockIdx.x);
+  const int cut = parts_of(a, q, work_of(a, q).tiles, work);
   if (cut == 1) return;                                  // written directly
-  // The block's last token sets the partitions' size, the row's own those it is in.
-  const int last = min((i / (2 * a.tpb) + 1) * 2 * a.tpb, q.n) - 1;
-  const int size = part_size(tiles_for(1, q.pos + last, q.kv_len), cut);
-  const int mine = tiles_for(1, q.pos + i, q.kv_len);    // key tiles this row sees
-  const int parts = (mine + size - 1) / size;
   const int64_t stride = static_cast<int64_t>(a.T) * a.H;
-  float m = -INFINITY;
-  for (int p = 0; p < parts; ++p) m = fmaxf(m, a.ws_ml[p * stride + row].x);
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (m != -INFINITY)
-    for (int p = 0; p < parts; ++p) {
-      const float2 ml = a.ws_ml[p * stride + row];
-      const float f = ex2_approx(ml.x - m);
-      const float4 v =
-          *reinterpret_cast<const float4 *>(a.ws_o + (p * stride + row) * D + lane * 4);
-      l = fmaf(f, ml.y, l);
-      o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
-    }
-  const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-  uint2 w;
-  w.x = pack_bf16x2(o.x * inv, o.y * inv);
-  w.y = pack_bf16x2(o.z * inv, o.w * inv);
-  *reinterpret_cast<uint2 *>(a.o + row * D + lane * 4) = w;
+  for (int x = blockIdx.y * 8 + (threadIdx.x >> 5); x < q.n * a.H; x += gridDim.y * 8) {
+    const int i = x / a.H;                               // token of the sequence
+    const int64_t row = static_cast<int64_t>(q.begin) * a.H + x;
+    // The block's last token sets the partitions' size, the row's own those it is in.
+    const int last = min((i / (2 * a.tpb) + 1) * 2 * a.tpb, q.n) - 1;
+    const int size = part_size(tiles_for(1, q.pos + last, q.kv_len), cut);
+    const int parts = (tiles_for(1, q.pos + i, q.kv_len) + size - 1) / size;
+    float m = -INFINITY;
+    for (int p = 0; p < parts; ++p) m = fmaxf(m, a.ws_ml[p * stride + row].x);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (m != -INFINITY)
+      for (int p = 0; p < parts; ++p) {
+        const float2 ml = a.ws_ml[p * stride + row];
+        const float f = ex2_approx(ml.x - m);
+        const float4 v =
+            *reinterpret_cast<const float4 *>(a.ws_o + (p * stride + row) * D + lane * 4);
+        l = fmaf(f, ml.y, l);
+        o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+      }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint2 w;
+    w.x = pack_bf16x2(o.x * inv, o.y * inv);
+    w.y = pack_bf16x2(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2 *>(a.o + row * D + lane * 4) = w;
+  }
 }
 
 cudaError_t sm_count(int *n) {
@@ -987,7 +1055,7 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   e = cudaFuncSetAttribute(fwd_packed_kernel<D, F16, PAGED>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
   if (e != cudaSuccess) return e;
-  const int64_t n_items = static_cast<int64_t>(a.n_vblocks) * a.n_split * a.Hk;
+  const int64_t n_items = static_cast<int64_t>(a.n_vblocks) * a.n_split * a.Hk;   // a bound
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(n_items < sms ? n_items : sms));
   cfg.blockDim = dim3(kThreads);
@@ -1000,7 +1068,8 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, fwd_packed_kernel<D, F16, PAGED>, tq, tk, tv, a);
   if (e != cudaSuccess || !PAGED || a.n_split == 1) return e;
-  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.T) * a.H + 7) / 8));
+  // Eight blocks an SM in all, spread over the sequences (at most kCachedSeqs).
+  cfg.gridDim = dim3(static_cast<unsigned>(a.S), static_cast<unsigned>(8 * sms / a.S));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel, a);
@@ -1019,7 +1088,7 @@ Args args_of(const PackedProblem &p, int *sched, int *dev_status) {
   a.tpb = packed_tile_tokens(a.G);
   a.max_blocks = p.max_blocks, a.num_blocks = p.num_blocks;
   a.n_vblocks = packed_blocks(p.T, p.S, a.G);
-  a.n_split = 1, a.part_tiles = 0x7fffffff / BN;
+  a.n_split = 1;
   a.causal = p.causal;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   return a;
@@ -1042,45 +1111,34 @@ cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, cons
              : launch<128, false, false>(tq, tk, tv, a, stream);
 }
 
-// Partition length, from what the host knows: the longest context's bound and the
-// average rows of a block.  With W key tiles of work per SM (in units of a block's
-// tile) cut into partitions of p, a partition's fixed cost c (its claim, Q and
-// start, and its rows' trip through the workspace: 1 KB a row, at an SM's share of
-// the HBM rate about 0.02 tiles) adds W c / p, and the SMs end up to p apart, 0.7 p
-// on average: p = sqrt(W c / 0.7) balances the two.  At least four key tiles (512
-// keys).
-PagedSplit paged_split(int T, int S, int Hk, int group, int max_blocks) {
-  constexpr double kSms = 152;
-  const int64_t tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;
-  const int64_t blocks = packed_blocks(T, S, group);
-  const double work = static_cast<double>(blocks) * Hk * static_cast<double>(tiles) / kSms;
-  const double rows = static_cast<double>(T) * group / static_cast<double>(blocks);
-  int64_t part = static_cast<int64_t>(std::sqrt(work * (1.5 + 0.02 * rows) / 0.7));
-  if (part < 4) part = 4;
-  if (part > tiles) part = tiles;
-  PagedSplit s;
-  s.part_tiles = static_cast<int>(part);
-  const int64_t n = (2 * tiles + part) / (2 * part);
-  s.n_split = static_cast<int>(n < 1 ? 1 : n);
-  return s;
+// The most partitions of a context, from what the host knows (the longest one's
+// bound): as parts_of reckons for a sequence of one token that is alone, and no more
+// than a workspace of 256 MB holds -- with that many rows the blocks fill the GPU.
+// Beyond kCachedSeqs sequences nothing is cut.
+int paged_max_parts(int T, int S, int H, int Hk, int max_blocks) {
+  if (S > kCachedSeqs) return 1;
+  const double tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;
+  const double least = std::fmax(4.0, std::sqrt(tiles * Hk / 152 * 3.0 / 0.7));
+  const double room = 256e6 / (sizeof(float) * (kDecodeHeadSize + 2.0) * T * H);
+  const double n = std::fmin(std::fmin(tiles / least + 0.5, room), 32767);
+  return n < 1 ? 1 : static_cast<int>(n);
 }
 
 size_t paged_prefill_workspace_bytes(int T, int S, int H, int Hk, int max_blocks) {
-  const PagedSplit s = paged_split(T, S, Hk, H / Hk, max_blocks);
-  if (s.n_split == 1) return 0;
-  return static_cast<size_t>(s.n_split) * T * H * (kDecodeHeadSize + 2) * sizeof(float);
+  const int n = paged_max_parts(T, S, H, Hk, max_blocks);
+  if (n == 1) return 0;
+  return static_cast<size_t>(n) * T * H * (kDecodeHeadSize + 2) * sizeof(float);
 }
 
 cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
                                  const CUtensorMap &tv, const PackedProblem &p, float *workspace,
                                  int *sched, int *dev_status, cudaStream_t stream) {
   Args a = args_of(p, sched, dev_status);
-  const PagedSplit s = paged_split(p.T, p.S, p.Hk, a.G, p.max_blocks);
-  if (s.n_split > 1) {
-    a.n_split = s.n_split;
-    a.part_tiles = s.part_tiles;
+  const int n = paged_max_parts(p.T, p.S, p.H, p.Hk, p.max_blocks);
+  if (n > 1) {
+    a.n_split = n;
     a.ws_o = workspace;
-    a.ws_ml = reinterpret_cast<float2 *>(workspace + static_cast<size_t>(s.n_split) * p.T * p.H *
+    a.ws_ml = reinterpret_cast<float2 *>(workspace + static_cast<size_t>(n) * p.T * p.H *
                                                          kDecodeHeadSize);
   }
   return launch<128, false, true>(tq, tk, tv, a, stream);

@@ -204,12 +204,9 @@ int packed_blocks(int T, int S, int group);     // bound on the two-tile blocks 
 cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                               const PackedProblem &p, int d, bool f16, int *sched,
                               int *dev_status, cudaStream_t stream);
-// Paged: how the context is cut into partitions, and the fp32 workspace that
-// they need (0 bytes when there is one).
-struct PagedSplit {
-  int n_split, part_tiles;                      // partitions, key tiles of each
-};
-PagedSplit paged_split(int T, int S, int Hk, int group, int max_blocks);
+// Paged: the most partitions that a context is cut into, and the fp32 workspace that
+// they need (0 bytes when it is one).
+int paged_max_parts(int T, int S, int H, int Hk, int max_blocks);
 size_t paged_prefill_workspace_bytes(int T, int S, int H, int Hk, int max_blocks);
 cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
                                  const CUtensorMap &tv, const PackedProblem &p, float *workspace,

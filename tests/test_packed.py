@@ -69,9 +69,10 @@ def test_chunk_workspace(lib):
     assert size(0, 5, 4, 2, 100) == 0 and size(1, 0, 4, 2, 100) == 0
     assert size(1, 1, 4, 3, 100) == 0                       # heads that do not divide
     assert size(1, 1, 32, 8, 8) == 0                        # one partition
-    assert size(64, 4096, 32, 8, 64) == 0                   # enough rows without a split
+    assert size(64, 16384, 32, 8, 1024) == 0                # enough rows without a split
     n = size(1, 1, 32, 8, 1024)
     assert n > 0 and n % (32 * 130 * 4) == 0
+    assert size(113, 113, 32, 8, 1024) == 0                 # that many sequences are not cut
 
 
 BWD = dict(q=P, k=P, v=P, o=P, dout=P, lse=P, dq=P, dk=P, dv=P, cu_seqlens=P, num_seqs=0,
