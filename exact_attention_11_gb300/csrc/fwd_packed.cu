@@ -202,16 +202,20 @@ __device__ __forceinline__ Work work_of(const Args &a, const Seq &q) {
 // partition's cost c (in key tiles: its start, and its rows' trip through the
 // workspace, 1 KB each at an SM's share of the HBM rate) adds W c / p, and the SMs
 // end up to p apart, 0.7 p on average: p = sqrt(W c / 0.7) balances the two, at
-// least four key tiles.  `work`: key tiles of the call's blocks, of one key/value
-// head.  Each block of the sequence cuts its own key tiles into that many.
-// (Roundings are spelled out: the merge kernel has to reach the same number.)
+// least four key tiles; what is shorter than 1.5 p stays whole.  (Constants fitted
+// to a model of the schedule over nine mixes of chunks and contexts; halving or
+// doubling c costs up to 25% on one of them.)  `work`: key tiles of the call's
+// blocks, of one key/value head.  Each block of the sequence cuts its own key tiles
+// into that many.  (Roundings are spelled out: the merge kernel has to reach the
+// same number.)
 __device__ __forceinline__ int parts_of(const Args &a, const Seq &q, int tiles, int64_t work) {
-  constexpr float kFixed = 3.f, kRow = 0.02f, kLeast = 4.f;
+  constexpr float kFixed = 2.f, kRow = 0.02f, kLeast = 4.f;
   if (a.n_split == 1) return 1;
   const float w = __fmul_rn(__ll2float_rn(work * a.Hk), 1.f / (152.f * 0.7f));
   const float c = __fmaf_rn(kRow, static_cast<float>(min(q.n, 2 * a.tpb) * a.G), kFixed);
   const float size = fmaxf(__fsqrt_rn(__fmul_rn(w, c)), kLeast);
-  return clampi(__float2int_rn(__fdiv_rn(static_cast<float>(tiles), size)), 1, a.n_split);
+  const float n = __fdiv_rn(static_cast<float>(tiles), size);
+  return n < 1.5f ? 1 : min(__float2int_ru(n), a.n_split);
 }
 __device__ __forceinline__ int part_size(int total, int parts) {
   return max(1, (total + parts - 1) / parts);
@@ -1016,20 +1020,35 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const Args a) {
     const int last = min((i / (2 * a.tpb) + 1) * 2 * a.tpb, q.n) - 1;
     const int size = part_size(tiles_for(1, q.pos + last, q.kv_len), cut);
     const int parts = (tiles_for(1, q.pos + i, q.kv_len) + size - 1) / size;
-    float m = -INFINITY;
-    for (int p = 0; p < parts; ++p) m = fmaxf(m, a.ws_ml[p * stride + row].x);
-    float l = 0.f;
+    // 32 partitions at a time, lane p holding partition p's (max, sum): their rows'
+    // loads do not wait for one another.
+    float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (m != -INFINITY)
-      for (int p = 0; p < parts; ++p) {
-        const float2 ml = a.ws_ml[p * stride + row];
-        const float f = ex2_approx(ml.x - m);
-        const float4 v =
-            *reinterpret_cast<const float4 *>(a.ws_o + (p * stride + row) * D + lane * 4);
-        l = fmaf(f, ml.y, l);
-        o.x = fmaf(f, v.x, o.x), o.y = fmaf(f, v.y, o.y);
-        o.z = fmaf(f, v.z, o.z), o.w = fmaf(f, v.w, o.w);
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+      const int n = min(32, parts - p0);
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < n) ml = a.ws_ml[(p0 + lane) * stride + row];
+      float mx = ml.x;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, off));
+      mx = fmaxf(mx, m);
+      if (mx == -INFINITY) continue;                     // no key seen so far
+      const float f = ex2_approx(ml.x - mx), old = ex2_approx(m - mx);
+      float sum = f * ml.y;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(~0u, sum, off);
+      l = fmaf(l, old, sum);
+      o.x *= old, o.y *= old, o.z *= old, o.w *= old;
+      m = mx;
+      const float *src = a.ws_o + (p0 * stride + row) * D + lane * 4;
+#pragma unroll 16
+      for (int p = 0; p < n; ++p) {
+        const float4 v = *reinterpret_cast<const float4 *>(src + p * stride * D);
+        const float w = __shfl_sync(~0u, f, p);
+        o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y);
+        o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
       }
+    }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint2 w;
     w.x = pack_bf16x2(o.x * inv, o.y * inv);
@@ -1118,9 +1137,9 @@ cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, cons
 int paged_max_parts(int T, int S, int H, int Hk, int max_blocks) {
   if (S > kCachedSeqs) return 1;
   const double tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;
-  const double least = std::fmax(4.0, std::sqrt(tiles * Hk / 152 * 3.0 / 0.7));
+  const double least = std::fmax(4.0, std::sqrt(tiles * Hk / 152 * 2.0 / 0.7));
   const double room = 256e6 / (sizeof(float) * (kDecodeHeadSize + 2.0) * T * H);
-  const double n = std::fmin(std::fmin(tiles / least + 0.5, room), 32767);
+  const double n = std::fmin(std::fmin(tiles / least + 1, room), 32767);
   return n < 1 ? 1 : static_cast<int>(n);
 }
 
