@@ -70,39 +70,54 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
   const int row_in = threadIdx.x / L, part = threadIdx.x % L;
   const int64_t rows = static_cast<int64_t>(a.n_blocks) * BQ;
   const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int r = row_in; r < BQ; r += kRows) {
-    const int64_t acc_row = static_cast<int64_t>(blk) * BQ + r;
-    if (h >= a.H) {
-      const int64_t at = ((h - a.H) * rows + acc_row) * D + part * 8;
+  constexpr int kRounds = BQ / kRows;
+  if (h >= a.H) {
+#pragma unroll
+    for (int u = 0; u < kRounds; ++u) {
+      const int64_t at =
+          ((h - a.H) * rows + static_cast<int64_t>(blk) * BQ + u * kRows + row_in) * D + part * 8;
       reinterpret_cast<float4 *>(a.dk_acc + at)[0] = z;
       reinterpret_cast<float4 *>(a.dk_acc + at)[1] = z;
       reinterpret_cast<float4 *>(a.dv_acc + at)[0] = z;
       reinterpret_cast<float4 *>(a.dv_acc + at)[1] = z;
-      continue;
     }
-    const int i = local * BQ + r;
-    const bool real = i < n;
+    return;
+  }
+  // Every round's loads go out before the first is used.
+  uint4 x[kRounds], y[kRounds];
+  float lse[kRounds];
+#pragma unroll
+  for (int u = 0; u < kRounds; ++u) {
+    const int i = local * BQ + u * kRows + row_in;
+    if (i >= n) continue;
+    const int64_t at = (static_cast<int64_t>(begin + i) * a.H + h) * D + part * 8;
+    x[u] = *reinterpret_cast<const uint4 *>(a.o + at);
+    y[u] = *reinterpret_cast<const uint4 *>(a.dout + at);
+    lse[u] = a.lse[static_cast<int64_t>(h) * a.T + begin + i];
+  }
+  float *vec = a.vecs + (static_cast<int64_t>(h) * a.n_blocks + blk) * (2 * BQ);
+#pragma unroll
+  for (int u = 0; u < kRounds; ++u) {
+    const int r = u * kRows + row_in;
+    const bool real = local * BQ + r < n;
     float acc = 0.f;
     if (real) {
-      const int64_t at = (static_cast<int64_t>(begin + i) * a.H + h) * D + part * 8;
-      const uint4 x = *reinterpret_cast<const uint4 *>(a.o + at);
-      const uint4 y = *reinterpret_cast<const uint4 *>(a.dout + at);
-      const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+      const uint32_t xw[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+      const uint32_t yw[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         acc = fmaf(__uint_as_float(xw[e] << 16), __uint_as_float(yw[e] << 16), acc);
         acc = fmaf(__uint_as_float(xw[e] & 0xffff0000u), __uint_as_float(yw[e] & 0xffff0000u), acc);
       }
-      float *q = a.dq_acc + (h * rows + acc_row) * D + part * 8;
+      float *q = a.dq_acc + (h * rows + static_cast<int64_t>(blk) * BQ + r) * D + part * 8;
       reinterpret_cast<float4 *>(q)[0] = z;
       reinterpret_cast<float4 *>(q)[1] = z;
     }
 #pragma unroll
     for (int off = L / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(~0u, acc, off);
     if (part == 0) {
-      float *v = a.vecs + (static_cast<int64_t>(h) * a.n_blocks + blk) * (2 * BQ);
-      v[r] = real ? -a.lse[static_cast<int64_t>(h) * a.T + begin + i] * kLog2e : -INFINITY;
-      v[BQ + r] = real ? -acc : 0.f;
+      vec[r] = real ? -lse[u] * kLog2e : -INFINITY;
+      vec[BQ + r] = real ? -acc : 0.f;
     }
   }
 }
