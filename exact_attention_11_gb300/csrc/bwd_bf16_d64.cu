@@ -154,7 +154,7 @@ struct BwdItem {
     row0 = blk0 = 0;
     steps(n_qb, causal);
   }
-  // Entry e = (first row, length, first padded block, -) of padded block w / H.
+  // Entry w / H of the table, e = (first row, length, first padded block, key block).
   __device__ void decode_packed(int w, const int4 &e, int H, int G, int causal) {
     const int blk = w / H;
     bh = w - blk * H;
@@ -162,7 +162,7 @@ struct BwdItem {
     row0 = e.x;
     N = e.y;
     blk0 = e.z;
-    jb = blk - blk0;
+    jb = e.w;
     steps((N + BQ - 1) / BQ, causal);
   }
   __device__ void steps(int n_qb, int causal) {
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     w = *reinterpret_cast<volatile int *>(&misc->item[slot]);
     if (PACKED) {
       const volatile int *e = reinterpret_cast<const volatile int *>(&misc->seq[slot]);
-      it.decode_packed(w, make_int4(e[0], e[1], e[2], 0), BH, pk.group, causal);
+      it.decode_packed(w, make_int4(e[0], e[1], e[2], e[3]), BH, pk.group, causal);
     } else {
       it.decode(w, BH, n_qb, causal, N);
     }
@@ -271,8 +271,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         int w = atomicAdd(sched, 1);
         int4 entry = make_int4(0, 0, 0, 0);
         if (PACKED) {
-          // A padded block that no sequence owns has no keys.
-          while (w < n_items && (entry = pk.table[w / BH]).y == 0) w = atomicAdd(sched, 1);
+          // Entries of length 0 end a sorted table, else are passed over.
+          while (w < n_items && (entry = pk.table[w / BH]).y == 0)
+            w = pk.sorted ? n_items : atomicAdd(sched, 1);
+          // (Offsets that decrease leave entries unwritten: whatever they hold, the
+          // item stays inside the tensors.)
+          entry.x = min(max(entry.x, 0), pk.tokens - 1);
+          entry.y = min(max(entry.y, 1), pk.tokens - entry.x);
+          const int n_kb = (entry.y + BM - 1) / BM;
+          entry.z = min(max(entry.z, 0), max(pk.n_blocks - n_kb, 0));
+          entry.w = min(max(entry.w, 0), n_kb - 1);
           misc->seq[islot] = entry;
         }
         misc->item[islot] = w;

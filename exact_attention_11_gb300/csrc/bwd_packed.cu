@@ -8,7 +8,9 @@
 //                        cu_seqlens[s] / 128 + s: no prefix sum over lengths, at
 //                        most one unused block per sequence): its entry in the
 //                        block table, [-LSE2 x 128 | -D x 128] of every query
-//                        head, and zeros in the fp32 accumulators
+//                        head, and zeros in the fp32 accumulators.  The table goes
+//                        by length, longest sequence first, so that the main
+//                        kernel's items come heaviest first
 //   main kernel          one item per (key block, query head)
 //   packed_out_kernel    dQ = scale * accumulator (and dK, dV where heads share
 //                        them), rounded to bf16 into the packed rows
@@ -27,6 +29,9 @@ namespace fattn {
 namespace {
 
 constexpr int BQ = 128;
+// Up to this many sequences the table is sorted (each block compares its sequence
+// with all others); beyond, it goes by block number, unused blocks in between.
+constexpr int kSortedSeqs = 2048;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct SideArgs {
@@ -64,8 +69,35 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
     local = blk - begin / BQ - s;
   }
   const bool live = s >= 0 && local * BQ < n;
-  if (h == 0 && threadIdx.x == 0)
-    a.table[blk] = live ? make_int4(begin, n, blk - local, 0) : make_int4(0, 0, 0, 0);
+  if (h == 0 && a.S > kSortedSeqs) {
+    if (threadIdx.x == 0)
+      a.table[blk] = live ? make_int4(begin, n, blk - local, local) : make_int4(0, 0, 0, 0);
+  } else if (h == 0) {
+    // The block's place in the table: behind the blocks of longer sequences (of
+    // equal ones, those before it); an unused block, behind all used ones.
+    int before = 0;
+    for (int j = threadIdx.x; j < a.S; j += 256) {
+      const int b = clampi(a.cu_seqlens[j], 0, a.T);
+      const int len = clampi(a.cu_seqlens[j + 1], b, a.T) - b;
+      const int blocks = (len + BQ - 1) / BQ;
+      if (live)
+        before += (len > n || (len == n && j < s)) ? blocks : 0;
+      else   // all used blocks, less those numbered before this one
+        before += blocks - clampi(blk - b / BQ - j, 0, blocks);
+    }
+    __shared__ int sum[8];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) before += __shfl_xor_sync(~0u, before, off);
+    if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = before;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      before = 0;
+      for (int u = 0; u < 8; ++u) before += sum[u];
+      // (Offsets that decrease may lead anywhere: stay inside the table.)
+      const int at = clampi(live ? before + local : before + blk, 0, a.n_blocks - 1);
+      a.table[at] = live ? make_int4(begin, n, blk - local, local) : make_int4(0, 0, 0, 0);
+    }
+  }
   if (!live) return;
   const int row_in = threadIdx.x / L, part = threadIdx.x % L;
   const int64_t rows = static_cast<int64_t>(a.n_blocks) * BQ;
@@ -168,6 +200,8 @@ cudaError_t launch_d(const PackedGradMaps &m, const PackedGrad &p, const SideArg
   if (e != cudaSuccess) return e;
   BwdPacked pk;
   pk.table = a.table;
+  pk.tokens = a.T;
+  pk.sorted = a.S <= kSortedSeqs;
   pk.n_blocks = a.n_blocks;
   pk.group = p.H / p.Hk;
   pk.kv_heads = p.Hk;

@@ -103,15 +103,15 @@ cudaError_t launch_bwd_main_d64(const CUtensorMap &tq64, const CUtensorMap &tk,
                                 int BH, int N, float scale, int causal, int *sched,
                                 int fault_cta, int *dev_status, cudaStream_t stream);
 
-// The main kernels for packed sequences: `table` holds for every padded
-// 128-row block (sequence s starts at block cu_seqlens[s] / 128 + s) its
-// sequence's first row, length (0: the block belongs to none) and first padded
-// block.  The accumulators' maps have n_blocks * 128 rows per head; tdk, tdv
+// The main kernels for packed sequences: `table` holds for every 128-row key block,
+// longest sequence first, its sequence's first row, length and first padded block
+// (sequence s starts at block cu_seqlens[s] / 128 + s) and its number in the
+// sequence; entries of length 0 end it (or, not `sorted`, lie in between).  The accumulators' maps have n_blocks * 128 rows per head; tdk, tdv
 // are used when group > 1.  tq64, tdo64, tk, tv: maps {d, T, heads} of the
 // packed tensors.
 struct BwdPacked {
   const int4 *table;
-  int n_blocks, group, kv_heads;
+  int n_blocks, group, kv_heads, tokens, sorted;
 };
 cudaError_t launch_bwd_packed_main_d128(const CUtensorMap &tq64, const CUtensorMap &tk,
                                         const CUtensorMap &tv, const CUtensorMap &tdo64,

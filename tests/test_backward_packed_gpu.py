@@ -103,9 +103,26 @@ def test_many_items_per_sm(d):
     run([1000, 77, 900], 8, 8, d, False, seed=10)
 
 
-def test_many_sequences():
-    g = torch.Generator().manual_seed(1)
-    run(torch.randint(0, 9, (1100,), generator=g).tolist(), 2, 1, 64, True, seed=2)
+@pytest.mark.parametrize("S", [255, 1100, 2048, 2049])
+def test_many_sequences(S):
+    """Sorted and unsorted block tables."""
+    g = torch.Generator().manual_seed(S)
+    run(torch.randint(0, 9, (S,), generator=g).tolist(), 2, 1, 64, True, seed=2)
+
+
+def test_decreasing_offsets_stay_inside():
+    """What is computed is not specified; rows outside the tensors are not
+    touched, and the library goes on working."""
+    q, k, v, cu = draw([40, 300, 24], 2, 1, 64, BF16, seed=5)
+    o, lse = fa.forward_packed(q, k, v, cu)
+    do = torch.randn_like(o)
+    for bad in ([364, 0, 300, 10], [300, 100, 364, 50], [1 << 30, -5, 7, 0]):
+        cu2 = torch.tensor(bad, device=DEV).int()
+        fa.forward_packed(q, k, v, cu2)
+        fa.backward_packed(q, k, v, o, lse, do, cu2)
+        torch.cuda.synchronize()
+        assert fa.fa_device_status() == 0
+    check(q, k, v, cu, o, lse, do, fa.backward_packed(q, k, v, o, lse, do, cu), True)
 
 
 @pytest.mark.parametrize("d", [64, 128])
