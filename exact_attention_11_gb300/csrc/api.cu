@@ -802,14 +802,18 @@ int check_packed(const void *q, const void *k, const void *v, const void *o, con
   return check_token_stride(v_stride, Hk, d, 2);
 }
 
-// The current device's work counters for one launch, and its status word.
-int acquire_sched(cudaStream_t s, int **sched, int **status) {
+// The current device's work counters for one launch, its status word, and the CTA
+// that is to lose its copies (0 if fa_debug_inject_fault armed `mode`, else -1).
+int acquire_sched(cudaStream_t s, int mode, int **sched, int **status, int *fault_cta) {
   std::lock_guard<std::mutex> lock(g_mu);
   int dev = 0, rc;
   if ((rc = current_device(&dev)) != FA_OK) return rc;
   if ((rc = get_encoder()) != FA_OK) return rc;
-  *sched = sched_slot(g_dev[dev], s);
-  *status = g_dev[dev].status;
+  DeviceState &st = g_dev[dev];
+  *sched = sched_slot(st, s);
+  *status = st.status;
+  *fault_cta = st.inject_fault == mode ? 0 : -1;
+  if (st.inject_fault == mode) st.inject_fault = 0;
   return FA_OK;
 }
 
@@ -822,8 +826,8 @@ int forward_packed(const void *q, const void *k, const void *v, void *o, float *
   if (rc != FA_OK) return rc;
   if (S == 0 || T == 0) return FA_OK;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  int *sched = nullptr, *status = nullptr;
-  if ((rc = acquire_sched(s, &sched, &status)) != FA_OK) return rc;
+  int *sched = nullptr, *status = nullptr, fault_cta = -1;
+  if ((rc = acquire_sched(s, 1, &sched, &status, &fault_cta)) != FA_OK) return rc;
   const CUtensorMapDataType dt =
       f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int group = H / Hk;
@@ -836,7 +840,8 @@ int forward_packed(const void *q, const void *k, const void *v, void *o, float *
   fattn::PackedProblem p{};
   p.o = o, p.lse = lse, p.cu_seqlens = cu_seqlens;
   p.S = S, p.T = T, p.H = H, p.Hk = Hk, p.causal = causal ? 1 : 0, p.scale = scale;
-  return cuda_status(fattn::launch_fwd_packed(tq, tk, tv, p, d, f16, sched, status, s));
+  return cuda_status(
+      fattn::launch_fwd_packed(tq, tk, tv, p, d, f16, sched, status, fault_cta, s));
 }
 }  // namespace
 
@@ -888,8 +893,8 @@ int fa_backward_packed(const void *q, const void *k, const void *v, const void *
   if (!workspace || workspace_bytes < l.bytes) return FA_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  int *sched = nullptr, *status = nullptr;
-  if ((rc = acquire_sched(s, &sched, &status)) != FA_OK) return rc;
+  int *sched = nullptr, *status = nullptr, fault_cta = -1;
+  if ((rc = acquire_sched(s, 2, &sched, &status, &fault_cta)) != FA_OK) return rc;
   const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int box = fattn::bwd_qdo_box_rows(d), rows = l.n_blocks * 128;
   float *ws = static_cast<float *>(workspace);
@@ -908,7 +913,7 @@ int fa_backward_packed(const void *q, const void *k, const void *v, const void *
   fattn::PackedGrad p{};
   p.o = o, p.dout = dout, p.lse = lse, p.dq = dq, p.dk = dk, p.dv = dv, p.cu_seqlens = cu_seqlens;
   p.S = S, p.T = T, p.H = H, p.Hk = Hk, p.d = d, p.causal = causal ? 1 : 0, p.scale = scale;
-  return cuda_status(fattn::launch_bwd_packed(m, p, ws, sched, status, s));
+  return cuda_status(fattn::launch_bwd_packed(m, p, ws, sched, status, fault_cta, s));
 }
 
 unsigned long long fa_paged_prefill_workspace_bytes(int num_seqs, int total_tokens, int num_heads,
@@ -947,8 +952,8 @@ int fa_paged_prefill(const void *q, const void *k_cache, const void *v_cache,
     if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
   }
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  int *sched = nullptr, *status = nullptr;
-  if ((rc = acquire_sched(s, &sched, &status)) != FA_OK) return rc;
+  int *sched = nullptr, *status = nullptr, fault_cta = -1;
+  if ((rc = acquire_sched(s, 1, &sched, &status, &fault_cta)) != FA_OK) return rc;
   const int group = num_heads / num_kv_heads;
   CUtensorMap tq, tk, tv;
   if ((rc = encode_rows_map(&tq, q, total_tokens, num_heads, head_size, q_stride, false, group,
@@ -963,7 +968,7 @@ int fa_paged_prefill(const void *q, const void *k_cache, const void *v_cache,
   p.S = num_seqs, p.T = total_tokens, p.H = num_heads, p.Hk = num_kv_heads;
   p.max_blocks = max_num_blocks_per_seq, p.num_blocks = num_blocks, p.causal = 1, p.scale = scale;
   return cuda_status(fattn::launch_paged_prefill(tq, tk, tv, p, static_cast<float *>(workspace),
-                                                 sched, status, s));
+                                                 sched, status, fault_cta, s));
 }
 
 int fa_device_status(void) {

@@ -734,10 +734,10 @@ cudaError_t launch_bwd_packed_main_d128(const CUtensorMap &tq64, const CUtensorM
                                         const CUtensorMap &tdq, const CUtensorMap &tdk,
                                         const CUtensorMap &tdv, const float *vecs, void *dk,
                                         void *dv, int H, const BwdPacked &pk, float scale,
-                                        int causal, int *sched, int *dev_status,
+                                        int causal, int *sched, int *dev_status, int fault_cta,
                                         cudaStream_t stream) {
-  return launch_main<true>(tq64, tk, tv, tdo64, tdq, vecs, dk, dv, H, 0, scale, causal, sched, -1,
-                           dev_status, stream, tdk, tdv, pk);
+  return launch_main<true>(tq64, tk, tv, tdo64, tdq, vecs, dk, dv, H, 0, scale, causal, sched,
+                           fault_cta, dev_status, stream, tdk, tdv, pk);
 }
 
 }  // namespace fattn

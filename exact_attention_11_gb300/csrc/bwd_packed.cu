@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(256) packed_out_kernel(const SideArgs a) {
 
 template <int D>
 cudaError_t launch_d(const PackedGradMaps &m, const PackedGrad &p, const SideArgs &a, int *sched,
-                     int *dev_status, cudaStream_t stream) {
+                     int *dev_status, int fault_cta, cudaStream_t stream) {
   const int heads = p.H + (a.dk_acc != nullptr ? p.Hk : 0);
   packed_prep_kernel<D><<<static_cast<unsigned>(a.n_blocks * heads), 256, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
@@ -207,7 +207,7 @@ cudaError_t launch_d(const PackedGradMaps &m, const PackedGrad &p, const SideArg
   pk.kv_heads = p.Hk;
   auto main_kernel = D == 128 ? launch_bwd_packed_main_d128 : launch_bwd_packed_main_d64;
   e = main_kernel(m.q, m.k, m.v, m.dout, m.dq_acc, m.dk_acc, m.dv_acc, a.vecs, p.dk, p.dv, p.H, pk,
-                  p.scale, p.causal, sched, dev_status, stream);
+                  p.scale, p.causal, sched, dev_status, fault_cta, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.T));
@@ -237,7 +237,7 @@ PackedGradLayout packed_grad_layout(int T, int S, int H, int Hk, int d) {
 }
 
 cudaError_t launch_bwd_packed(const PackedGradMaps &m, const PackedGrad &p, float *ws, int *sched,
-                              int *dev_status, cudaStream_t stream) {
+                              int *dev_status, int fault_cta, cudaStream_t stream) {
   const PackedGradLayout l = packed_grad_layout(p.T, p.S, p.H, p.Hk, p.d);
   SideArgs a{};
   a.o = static_cast<const __nv_bfloat16 *>(p.o);
@@ -254,8 +254,8 @@ cudaError_t launch_bwd_packed(const PackedGradMaps &m, const PackedGrad &p, floa
   a.dv = static_cast<__nv_bfloat16 *>(p.dv);
   a.S = p.S, a.T = p.T, a.H = p.H, a.Hk = p.Hk, a.n_blocks = l.n_blocks;
   a.scale = p.scale;
-  return p.d == 128 ? launch_d<128>(m, p, a, sched, dev_status, stream)
-                    : launch_d<64>(m, p, a, sched, dev_status, stream);
+  return p.d == 128 ? launch_d<128>(m, p, a, sched, dev_status, fault_cta, stream)
+                    : launch_d<64>(m, p, a, sched, dev_status, fault_cta, stream);
 }
 
 }  // namespace fattn

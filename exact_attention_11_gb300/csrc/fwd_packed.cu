@@ -153,6 +153,7 @@ struct Args {
   int *sched, *dev_status;
   int S, T, H, Hk, G, tpb;      // tpb: tokens per query tile, 128 / G
   int max_blocks, num_blocks;
+  int fault_cta;                // a CTA that loses its copies (failure-path test), or -1
   int n_vblocks, n_split, causal;   // n_split: most partitions of a context
   float scale_log2;
 };
@@ -550,6 +551,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!(ok = __shfl_sync(~0u, ok, 0)) || !it.live) break;
         claim();
+        if (static_cast<int>(blockIdx.x) == a.fault_cta) {
+          // Failure-path test: as if the item's copies were lost; the MMA warp's
+          // bounded wait for them runs out.
+          ok = false;
+          break;
+        }
         // Query tile t into the next Q buffer, once the last Q K^T of the tile
         // that was there has read it.
         auto load_q = [&](int t) -> bool {
@@ -1094,7 +1101,7 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel, a);
 }
 
-Args args_of(const PackedProblem &p, int *sched, int *dev_status) {
+Args args_of(const PackedProblem &p, int *sched, int *dev_status, int fault_cta) {
   Args a{};
   a.o = static_cast<uint16_t *>(p.o);
   a.lse = p.lse;
@@ -1103,6 +1110,7 @@ Args args_of(const PackedProblem &p, int *sched, int *dev_status) {
   a.block_tables = p.block_tables;
   a.sched = sched;
   a.dev_status = dev_status;
+  a.fault_cta = fault_cta;
   a.S = p.S, a.T = p.T, a.H = p.H, a.Hk = p.Hk, a.G = p.H / p.Hk;
   a.tpb = packed_tile_tokens(a.G);
   a.max_blocks = p.max_blocks, a.num_blocks = p.num_blocks;
@@ -1121,8 +1129,8 @@ int packed_blocks(int T, int S, int group) { return T / (2 * packed_tile_tokens(
 
 cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                               const PackedProblem &p, int d, bool f16, int *sched,
-                              int *dev_status, cudaStream_t stream) {
-  const Args a = args_of(p, sched, dev_status);
+                              int *dev_status, int fault_cta, cudaStream_t stream) {
+  const Args a = args_of(p, sched, dev_status, fault_cta);
   if (d == 64)
     return f16 ? launch<64, true, false>(tq, tk, tv, a, stream)
                : launch<64, false, false>(tq, tk, tv, a, stream);
@@ -1151,8 +1159,9 @@ size_t paged_prefill_workspace_bytes(int T, int S, int H, int Hk, int max_blocks
 
 cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
                                  const CUtensorMap &tv, const PackedProblem &p, float *workspace,
-                                 int *sched, int *dev_status, cudaStream_t stream) {
-  Args a = args_of(p, sched, dev_status);
+                                 int *sched, int *dev_status, int fault_cta,
+                                 cudaStream_t stream) {
+  Args a = args_of(p, sched, dev_status, fault_cta);
   const int n = paged_max_parts(p.T, p.S, p.H, p.Hk, p.max_blocks);
   if (n > 1) {
     a.n_split = n;

@@ -118,14 +118,14 @@ cudaError_t launch_bwd_packed_main_d128(const CUtensorMap &tq64, const CUtensorM
                                         const CUtensorMap &tdq, const CUtensorMap &tdk,
                                         const CUtensorMap &tdv, const float *vecs, void *dk,
                                         void *dv, int H, const BwdPacked &pk, float scale,
-                                        int causal, int *sched, int *dev_status,
+                                        int causal, int *sched, int *dev_status, int fault_cta,
                                         cudaStream_t stream);
 cudaError_t launch_bwd_packed_main_d64(const CUtensorMap &tq64, const CUtensorMap &tk,
                                        const CUtensorMap &tv, const CUtensorMap &tdo64,
                                        const CUtensorMap &tdq, const CUtensorMap &tdk,
                                        const CUtensorMap &tdv, const float *vecs, void *dk,
                                        void *dv, int H, const BwdPacked &pk, float scale,
-                                       int causal, int *sched, int *dev_status,
+                                       int causal, int *sched, int *dev_status, int fault_cta,
                                        cudaStream_t stream);
 
 int decode_max_parts(int max_num_blocks_per_seq);
@@ -203,14 +203,15 @@ int packed_tile_tokens(int group);              // tokens of a 128-row query til
 int packed_blocks(int T, int S, int group);     // bound on the two-tile blocks of a call
 cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                               const PackedProblem &p, int d, bool f16, int *sched,
-                              int *dev_status, cudaStream_t stream);
+                              int *dev_status, int fault_cta, cudaStream_t stream);
 // Paged: the most partitions that a context is cut into, and the fp32 workspace that
 // they need (0 bytes when it is one).
 int paged_max_parts(int T, int S, int H, int Hk, int max_blocks);
 size_t paged_prefill_workspace_bytes(int T, int S, int H, int Hk, int max_blocks);
 cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
                                  const CUtensorMap &tv, const PackedProblem &p, float *workspace,
-                                 int *sched, int *dev_status, cudaStream_t stream);
+                                 int *sched, int *dev_status, int fault_cta,
+                                 cudaStream_t stream);
 
 // Gradients of the packed forward (bwd_packed.cu).  Workspace, in floats from
 // its start: the dQ accumulator [H][n_blocks * 128][d], those of dK and dV
@@ -235,6 +236,6 @@ struct PackedGrad {
   float scale;
 };
 cudaError_t launch_bwd_packed(const PackedGradMaps &m, const PackedGrad &p, float *ws, int *sched,
-                              int *dev_status, cudaStream_t stream);
+                              int *dev_status, int fault_cta, cudaStream_t stream);
 
 }  // namespace fattn

@@ -378,8 +378,8 @@ int fa_paged_decode_noalloc(const void *q, const void *k_cache, const void *v_ca
  *                  norm on that side.
  *   positions      int32 [num_tokens], any value (a turn is taken modulo its
  *                  period exactly, so far positions lose no accuracy).
- *   inv_freq       fp64 [rot_dim / 2] radians per position; null only when
- *                  rot_dim is 0.
+ *   inv_freq       fp64 [rot_dim / 2] radians per position, finite; null only
+ *                  when rot_dim is 0.
  *   d              64, 128 or 256;  rot_dim a multiple of 16 in [0, d] (else
  *                  FA_ERR_UNSUPPORTED).
  *   eps            finite and >= 0;  mscale finite (1 unless the frequencies
@@ -594,14 +594,15 @@ int fa_paged_prefill(const void *q, const void *k_cache, const void *v_cache,
  * fa_debug_inject_fault -- test hook for the device-side failure path.
  *
  * mode 1 arms the current device: the next tensor-core forward launched on
- * it (fa_forward, fa_forward_f16, fa_forward_masked or fa_forward_fp8, for
- * head dimension 64 or 128) makes its first CTA's TMA producer stop after
- * loading that CTA's first query tiles, as if a copy had been lost.  The MMA warp's bounded wait for the
+ * it (fa_forward, fa_forward_f16, fa_forward_masked, fa_forward_fp8,
+ * fa_forward_packed, fa_forward_packed_f16 or fa_paged_prefill, for head
+ * dimension 64 or 128) makes its first CTA's TMA producer stop at
+ * that CTA's first item, as if a copy had been lost.  The MMA warp's bounded wait for the
  * missing key tile then runs out (after about 2 s), the CTA unwinds (in-flight
  * copies and MMAs drained, tensor memory freed) and fa_device_status()
  * returns FA_ERR_TIMEOUT.  That launch's output is incomplete; the CUDA
  * context and the library stay usable.  mode 2 does the same to the next
- * fa_backward: its main kernel's first CTA loses the K and V copies of its
+ * fa_backward or fa_backward_packed: its main kernel's first CTA loses the K and V copies of its
  * first work item.  mode 0 disarms.  Returns FA_OK, or FA_ERR_INVALID_ARG
  * for another mode, or FA_ERR_NO_DEVICE.
  */

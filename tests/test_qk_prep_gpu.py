@@ -146,7 +146,8 @@ def slots_of(kind, T, nb, seed):
 
 
 @pytest.mark.parametrize("kind", ["scattered", "run", "offset_run", "runs", "padded"])
-@pytest.mark.parametrize("T,H,Hk", [(1, 4, 1), (16, 8, 2), (53, 6, 3), (700, 8, 8)])
+@pytest.mark.parametrize("T,H,Hk", [(1, 4, 1), (16, 8, 2), (53, 6, 3), (700, 8, 8), (1300, 2, 1),
+                                    (2501, 3, 1), (5003, 1, 1)])
 def test_cache_form(kind, T, H, Hk):
     nb = 2 * (T + 15) // 16 + 4
     q, k, v, pos, qw, kw = draw(T, H, Hk, 128, BF16, seed=T + len(kind), extra=1)
@@ -158,10 +159,10 @@ def test_cache_form(kind, T, H, Hk):
     qo = fa.qk_norm_rope_cache(q, k, v, pos, freq, slots.to(DEV), kc, vc, qw, kw)
     torch.cuda.synchronize()
     assert torch.equal(qo, qd)              # the dense form's values, bit for bit
-    for t, s in enumerate(slots.tolist()):
-        if 0 <= s < nb * 16:
-            want_k[s // 16, :, :, s % 16] = kd[t].cpu().view(Hk, 16, 8)
-            want_v[s // 16, :, :, s % 16] = v[t].cpu()
+    t = torch.nonzero((slots >= 0) & (slots < nb * 16)).flatten()
+    s = slots[t]
+    want_k[s // 16, :, :, s % 16] = kd.cpu()[t].view(-1, Hk, 16, 8)
+    want_v[s // 16, :, :, s % 16] = v.cpu()[t]
     assert torch.equal(kc.cpu(), want_k)    # and no other slot has changed
     assert torch.equal(vc.cpu(), want_v)
 
