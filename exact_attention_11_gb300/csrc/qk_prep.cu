@@ -546,8 +546,10 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks<T>) qk_prep_grad_kernel(
         }
         const float ss = row_sum<L>(sum_squares(v));
         const float wgx = row_sum<L>(sum2(fadd2(d0, d1)));
-        const float r = rsqrtf(ss * (1.f / D) + a.eps);
-        const float m = -r * r * (wgx * (1.f / D));
+        // (Without a row here: nothing, where 0 * rsqrt(eps = 0) would be NaN.  r * r
+        // alone could overflow.)
+        const float r = on ? rsqrtf(ss * (1.f / D) + a.eps) : 0.f;
+        const float m = -r * (r * (wgx * (1.f / D)));
         const uint64_t r2 = f2(r, r), m2 = f2(m, m);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

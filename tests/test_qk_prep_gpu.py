@@ -196,6 +196,71 @@ def test_cache_form_feeds_the_decode():
     assert np.abs(out.float().cpu().numpy() - want).max() <= 2e-2
 
 
+def test_cache_form_in_place():
+    T, H, Hk = 37, 6, 2
+    q, k, v, pos, qw, kw = draw(T, H, Hk, 128, BF16, seed=51)
+    freq, _ = fa.rope_frequencies(128, device=DEV)
+    slots = torch.arange(T, device=DEV)
+    kc, vc = caches(4, Hk, seed=52)
+    want = fa.qk_norm_rope_cache(q, k, v, pos, freq, slots, kc, vc, qw, kw)
+    x = q.contiguous()
+    got = fa.qk_norm_rope_cache(x, k, v, pos, freq, slots, kc, vc, qw, kw, q_out=x)
+    torch.cuda.synchronize()
+    assert got is x and torch.equal(x, want)
+
+
+def test_cache_form_same_slot_twice():
+    """Each stored value is one of the tokens' that name its slot; no other slot
+    changes."""
+    T, Hk, nb = 40, 2, 8
+    q, k, v, pos, qw, kw = draw(T, 3, Hk, 128, BF16, seed=53)
+    freq, _ = fa.rope_frequencies(128, device=DEV)
+    kc, vc = caches(nb, Hk, seed=54)
+    k0, v0 = kc.clone(), vc.clone()
+    slots = torch.randint(16, 16 + T // 2, (T,), generator=torch.Generator().manual_seed(55))
+    slots[20:30] = torch.arange(48, 53).repeat_interleave(2)
+    _, kd = fa.qk_norm_rope(q, k, pos, freq, qw, kw)
+    fa.qk_norm_rope_cache(q, k, v, pos, freq, slots.to(DEV), kc, vc, qw, kw)
+    torch.cuda.synchronize()
+    for s in range(nb * 16):
+        at = torch.nonzero(slots == s).flatten().to(DEV)
+        got_k, got_v = kc[s // 16, :, :, s % 16].flatten(1), vc[s // 16, :, :, s % 16]
+        if len(at) == 0:
+            at_k, at_v = k0[s // 16, :, :, s % 16].flatten(1)[None], v0[s // 16, :, :, s % 16][None]
+        else:
+            at_k, at_v = kd[at], v[at]
+        assert (at_k == got_k[None]).any(0).all() and (at_v == got_v[None]).any(0).all()
+
+
+def test_cache_form_far_slots():
+    """Caches of more than 2^32 values each: the last block, and two around the
+    place where a 32-bit index of values would turn over."""
+    Hk = 8
+    nb = (1 << 32) // (Hk * 16 * 128) + 3
+    T = 48
+    q, k, v, pos, qw, kw = draw(T, 8, Hk, 128, BF16, seed=56)
+    freq, _ = fa.rope_frequencies(128, device=DEV)
+    kc = torch.empty(nb, Hk, 16, 16, 8, dtype=BF16, device=DEV)
+    vc = torch.empty(nb, Hk, 128, 16, dtype=BF16, device=DEV)
+    blocks = torch.tensor([nb - 1, (1 << 31) // (Hk * 16 * 128), (1 << 32) // (Hk * 16 * 128)])
+    slots = (blocks[:, None] * 16 + torch.arange(16)).flatten().to(DEV)
+    kc[0], vc[0] = 3.0, 3.0
+    _, kd = fa.qk_norm_rope(q, k, pos, freq, qw, kw)
+    qo = fa.qk_norm_rope_cache(q, k, v, pos, freq, slots, kc, vc, qw, kw)
+    torch.cuda.synchronize()
+    b = blocks.to(DEV)
+    assert torch.equal(kc[b].permute(0, 3, 1, 2, 4).reshape(T, Hk, 128), kd)
+    assert torch.equal(vc[b].permute(0, 3, 1, 2).reshape(T, Hk, 128), v)
+    assert (kc[0] == 3).all() and (vc[0] == 3).all()
+    # ... and the chunk that reads them back equals the one from a small cache
+    bt = torch.tensor([[2, 0, 1]], device=DEV)
+    ctx, cu = torch.tensor([T], device=DEV).int(), torch.tensor([0, T], device=DEV).int()
+    far = fa.paged_prefill(qo, kc, vc, b[bt].int(), ctx, cu)
+    near = fa.paged_prefill(qo, kc[b].contiguous(), vc[b].contiguous(), bt.int(), ctx, cu)
+    torch.cuda.synchronize()
+    assert torch.equal(far, near)
+
+
 # ----------------------------------------------------------------- backward
 def check_backward(T, H, Hk, d, rot, dtype, pairs, norm, seed, mscale=1.0):
     q, k, _, pos, qw, kw = draw(T, H, Hk, d, dtype, seed)
@@ -235,6 +300,26 @@ def test_backward_many_tiles_repeats_exactly():
     b = check_backward(4001, 4, 2, 128, 128, BF16, False, "both", seed=3)
     for x, y in zip(a, b):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -130])
+@pytest.mark.parametrize("T,H,Hk", [(1, 1, 1), (13, 6, 2), (9, 3, 5)])
+def test_backward_without_eps(eps, T, H, Hk):
+    """Threads without a row add nothing to the weights' gradients; with an eps
+    below fp32's normal range a row of zeros keeps its gradient, r w g."""
+    q, k, _, pos, qw, kw = draw(T, H, Hk, 128, F32, seed=T)
+    freq, _ = fa.rope_frequencies(64, device=DEV)
+    if eps:
+        q[T // 2, 0] = 0.0
+    g = torch.Generator().manual_seed(T + 1)
+    dqo = 1e-3 * torch.randn(T, H, 128, generator=g).to(DEV)
+    dko = 1e-3 * torch.randn(T, Hk, 128, generator=g).to(DEV)
+    got = fa.qk_norm_rope_backward(dqo, dko, q, k, pos, freq, qw, kw, eps)
+    for x, dy, w, dx, dw in ((q, dqo, qw, got[0], got[2]), (k, dko, kw, got[1], got[3])):
+        want, size, want_w, size_w = ref.backward(dy.cpu(), x.cpu(), w.cpu(), pos.cpu(),
+                                                  freq.cpu(), eps, False, 1.0)
+        check(dx, want, size)
+        assert ((dw.cpu().double() - want_w).abs() <= 256 * 2.0 ** -24 * size_w).all()
 
 
 def test_backward_against_differences():
