@@ -582,6 +582,8 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_c
         raise ValueError("rot_dim must be even")
     if scaling not in (None, "linear", "ntk", "yarn") or not factor >= 1.0 or not base > 1.0:
         raise ValueError("scaling is None, 'linear', 'ntk' or 'yarn', factor >= 1 and base > 1")
+    if scaling == "yarn" and not (beta_fast > beta_slow and original_context > 0):
+        raise ValueError("beta_fast > beta_slow and original_context > 0")
     mscale = 1.0
     if scaling == "ntk" and rot_dim > 2:
         base = base * factor ** (rot_dim / (rot_dim - 2))
@@ -669,7 +671,8 @@ def qk_norm_rope_cache(q, k, v, positions, inv_freq, slots, k_cache, v_cache, q_
     """``qk_norm_rope`` for serving (bf16, d = 128): the prepared keys, and v
     [T,Hk,d] as it is, are written into the paged caches of ``paged_decode``
     and ``paged_prefill`` at slots (int64 [T]: block * block_size + offset; a
-    negative slot stores nothing).  Returns the prepared queries, dense."""
+    slot outside the cache, such as -1, stores nothing).  Returns the prepared
+    queries, dense; ``q_out`` may be q itself."""
     import torch
     T, H, Hk, d, dtype, suffix, dev, qs, ks, ptrs, rot = _prep_args(
         q, k, positions, inv_freq, q_weight, k_weight)

@@ -426,6 +426,8 @@ int fa_qk_norm_rope_fp32(const void *q, const void *k, const void *q_weight, con
  *                  all the same).  Slots in range must differ: where two tokens
  *                  name one slot, which of them each stored value comes from is
  *                  not specified.
+ *   q_out          bf16 [num_tokens, num_heads, head_size], dense; may be q
+ *                  itself where that is dense.
  *   k_cache        bf16 [num_blocks, num_kv_heads, head_size/8, block_size, 8].
  *   v_cache        bf16 [num_blocks, num_kv_heads, head_size, block_size].
  *   head_size      128;  block_size 16 (else FA_ERR_UNSUPPORTED).

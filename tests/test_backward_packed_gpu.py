@@ -13,7 +13,7 @@ import pytest
 import torch
 
 import exact_attention_11_gb300 as fa
-from test_forward_packed_gpu import draw
+from test_forward_packed_gpu import draw, draw_far
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -94,6 +94,20 @@ def test_every_length_up_to_two_blocks():
     for d in (64, 128):
         run(list(range(1, 258, 3)), 1, 1, d, True, seed=5)
         run(list(range(2, 258, 3)), 2, 1, d, False, seed=6)
+
+
+@pytest.mark.parametrize("Hk", [8, 32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_far_rows(d, Hk):
+    """Rows behind more than 2^31 values of q, o and the accumulators."""
+    H = 32
+    q, k, v, cu = draw_far(H, Hk, d, [300, 1, 77], seed=42)
+    o, lse = fa.forward_packed(q, k, v, cu)
+    do = torch.empty_like(o)
+    a = cu[0].item()
+    do[a:] = torch.randn(o[a:].shape, generator=torch.Generator().manual_seed(43)).to(BF16).to(DEV)
+    got = fa.backward_packed(q, k, v, o, lse, do, cu)
+    check(q, k, v, cu, o, lse, do, got, True)
 
 
 @pytest.mark.parametrize("d", [64, 128])

@@ -135,6 +135,25 @@ def test_matches_the_dense_forward():
     assert (lse.transpose(0, 1).reshape(H, B * N) - lse2).abs().max() <= 1e-5
 
 
+def draw_far(H, Hk, d, lens, seed):
+    """`lens` behind so many rows of no sequence that q and o have more than
+    2^31 values before them."""
+    before = (1 << 31) // (H * d) + 5
+    T = before + sum(lens)
+    qkv = torch.empty(T, H + 2 * Hk, d, dtype=BF16, device=DEV)
+    g = torch.Generator().manual_seed(seed)
+    qkv[before:] = torch.randn(T - before, H + 2 * Hk, d, generator=g).to(BF16).to(DEV)
+    cu = torch.tensor([before] + lens).cumsum(0).int().to(DEV)
+    return qkv[:, :H], qkv[:, H:H + Hk], qkv[:, H + Hk:], cu
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_far_rows(d):
+    q, k, v, cu = draw_far(32, 8, d, [300, 1, 77], seed=41)
+    o, lse = fa.forward_packed(q, k, v, cu)
+    check(q, k, v, cu, o, lse, True)
+
+
 def test_without_lse_and_empty():
     q, k, v, cu = draw([40], 2, 1, 64, BF16, seed=1)
     o, lse = fa.forward_packed(q, k, v, cu, want_lse=False)

@@ -135,3 +135,9 @@ def test_frequencies():
     for bad in (dict(rot_dim=3), dict(rot_dim=64, scaling="other"), dict(rot_dim=64, factor=0.5)):
         with pytest.raises(ValueError):
             fa.rope_frequencies(**bad)
+
+
+def test_frequencies_refuse_an_empty_ramp():
+    for bad in (dict(beta_slow=32.0), dict(original_context=0)):
+        with pytest.raises(ValueError):
+            fa.rope_frequencies(64, scaling="yarn", factor=4.0, **bad)
