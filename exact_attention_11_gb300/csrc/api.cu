@@ -51,6 +51,33 @@ EncodeTiledFn g_encode = nullptr;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// n zeroed ints that any stream may use at once: the first call on a device may be
+// one that is being captured into a graph, or on a stream that does not wait for
+// the legacy one, so they are cleared on a stream of their own, outside of any
+// capture, before this returns.
+int alloc_zeroed(int **p, size_t n) {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return FA_ERR_CUDA;
+  int rc = FA_ERR_CUDA;
+  int *mem = nullptr;
+  cudaStream_t s = nullptr;
+  if (cudaMalloc(&mem, n * sizeof(int)) != cudaSuccess) {
+    mem = nullptr;
+    rc = FA_ERR_NO_MEMORY;
+  } else if (cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess) {
+    if (cudaMemsetAsync(mem, 0, n * sizeof(int), s) == cudaSuccess &&
+        cudaStreamSynchronize(s) == cudaSuccess)
+      rc = FA_OK;
+    cudaStreamDestroy(s);
+  }
+  cudaThreadExchangeStreamCaptureMode(&mode);
+  if (rc == FA_OK)
+    *p = mem;
+  else if (mem != nullptr)
+    cudaFree(mem);
+  return rc;
+}
+
 // Resolves the current device and makes sure its state exists.
 int current_device(int *dev_out) {
   int dev = 0;
@@ -65,15 +92,11 @@ int current_device(int *dev_out) {
     st.checked = (major == 10 && minor == 3) ? 1 : -1;
   }
   if (st.checked < 0) return FA_ERR_NO_DEVICE;
-  if (st.status == nullptr) {
-    if (cudaMalloc(&st.status, sizeof(int)) != cudaSuccess) return FA_ERR_NO_MEMORY;
-    if (cudaMemset(st.status, 0, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
-  }
-  if (st.fwd_sched == nullptr) {
-    const size_t bytes = sizeof(int) * 2 * 2 * fattn::kFwdSchedSlots;
-    if (cudaMalloc(&st.fwd_sched, bytes) != cudaSuccess) return FA_ERR_NO_MEMORY;
-    if (cudaMemset(st.fwd_sched, 0, bytes) != cudaSuccess) return FA_ERR_CUDA;
-  }
+  int rc;
+  if (st.status == nullptr && (rc = alloc_zeroed(&st.status, 1)) != FA_OK) return rc;
+  if (st.fwd_sched == nullptr &&
+      (rc = alloc_zeroed(&st.fwd_sched, 2 * 2 * fattn::kFwdSchedSlots)) != FA_OK)
+    return rc;
   *dev_out = dev;
   return FA_OK;
 }
@@ -280,10 +303,12 @@ int cuda_status(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; 
 
 // The work-counter pair of a persistent-kernel launch.  Eager launches take
 // the first kFwdSchedSlots pairs round robin, so concurrent calls share one
-// only with the 64th call after them.  A launch captured into a CUDA graph
+// only with the kFwdSchedSlots-th call after them.  A launch captured into a CUDA graph
 // keeps its pair for every replay: it takes one of the other kFwdSchedSlots
-// pairs, never handed to an eager launch, shared only with the 64th captured
-// launch after it.  (A graph must not run concurrently with itself.)
+// pairs, never handed to an eager launch, shared only with the kFwdSchedSlots-th
+// captured launch after it: graphs of whole networks, some hundred launches each,
+// may be replayed at the same time.  (One graph must not run concurrently with
+// itself.)
 int *sched_slot(DeviceState &st, cudaStream_t s) {
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   bool captured = false;

@@ -21,7 +21,7 @@ cudaError_t launch_fwd_f32(const float *q, const float *k, const float *v, float
 // counter and the finished-CTA counter) that are zero before the launch; the
 // kernel leaves them zero.  Launches that may run at the same time need
 // different `sched` slots.
-constexpr int kFwdSchedSlots = 64;
+constexpr int kFwdSchedSlots = 32768;
 // fault_cta >= 0 makes that CTA's producer stop after its first Q loads (the
 // failure-path test); -1 in normal use.
 // f16 selects fp16 Q, K, V, O (tensor maps of CU_TENSOR_MAP_DATA_TYPE_FLOAT16).

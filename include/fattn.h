@@ -33,10 +33,12 @@
  * being captured into a CUDA graph cannot grow them and returns
  * FA_ERR_UNSUPPORTED instead, so run one call of the largest size before
  * capturing.  The forward kernels (fa_paged_prefill among them), the
- * backward's main kernel and the tensor-core grouped decode take a pair of work counters per launch: eager launches rotate through 64 pairs,
- * launches captured into a graph through 64 others that a graph keeps for
- * every replay; so at most 64 eager calls may be in flight on a device at
- * once, and a graph must not run concurrently with itself.
+ * backward's main kernel and the tensor-core grouped decode take a pair of
+ * work counters per launch: eager launches rotate through 32768 pairs,
+ * launches captured into a graph through 32768 others that a graph keeps for
+ * every replay; so at most 32768 eager calls may be in flight on a device at
+ * once, graphs that run at the same time must have been captured within 32768
+ * launches of each other, and a graph must not run concurrently with itself.
  */
 #ifndef FATTN_H_
 #define FATTN_H_

@@ -1,5 +1,9 @@
 """Packed prompts of different lengths with grouped heads against float64.
 Tolerances: packed_ref.check_forward."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -201,6 +205,59 @@ def test_captured_and_concurrent_calls():
             outs.append(fa.forward_packed(q, k, v, cu)[0])
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for x in outs)
+
+
+@pytest.mark.parametrize("call", ["forward_packed(q, k, v, cu)[0]",
+                                  "qk_norm_rope(q, k, pos, freq)[0]"])
+def test_first_call_of_a_process_is_captured(call):
+    """The library's state is set up inside the capture, and the graph works."""
+    code = f"""
+import torch, exact_attention_11_gb300 as fa
+g = torch.Generator().manual_seed(1)
+q = torch.randn(70, 4, 128, generator=g).bfloat16().cuda()
+k, v = (torch.randn(70, 2, 128, generator=g).bfloat16().cuda() for _ in range(2))
+cu = torch.tensor([0, 30, 70]).int().cuda()
+pos, freq = torch.arange(70).int().cuda(), fa.rope_frequencies(128, device="cuda")[0]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+    x = fa.{call}
+for _ in range(2):
+    x.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(x, fa.{call})
+assert fa.fa_device_status() == 0
+"""
+    run = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                         timeout=300, cwd=os.path.dirname(os.path.dirname(fa.__file__)))
+    assert run.returncode == 0, run.stderr[-2000:]
+
+
+def test_two_graphs_of_many_launches_at_once():
+    """Two graphs of 70 launches each, replayed on two streams at the same time:
+    no launch of one shares its work counters with one of the other."""
+    n, graphs = 70, []
+    for seed in (31, 32):
+        q, k, v, cu = draw([900, 300, 1100], 4, 2, 128, BF16, seed)
+        want, _ = fa.forward_packed(q, k, v, cu)
+        outs = torch.zeros(n, *q.shape, dtype=BF16, device=DEV)
+        torch.cuda.synchronize()
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=stream):
+            for i in range(n):
+                fa.forward_packed(q, k, v, cu, out=outs[i], want_lse=False)
+        graphs.append((graph, stream, outs, want, (q, k, v, cu)))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, stream, outs, _, _ in graphs:
+            with torch.cuda.stream(stream):
+                outs.zero_()
+                graph.replay()
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0
+    for _, _, outs, want, _ in graphs:
+        assert (outs == want[None]).all()
 
 
 def test_helper_refuses():
