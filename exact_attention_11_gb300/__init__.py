@@ -528,18 +528,23 @@ def _on_device(fn):
     the current device, and a caller's may be another one."""
     @functools.wraps(fn)
     def run(first, *args, **kwargs):
-        import torch
-        if first.is_cuda and first.get_device() != torch.cuda.current_device():
-            with torch.cuda.device(first.device):
+        dev = first.get_device()
+        if dev >= 0 and dev != _torch()._C._cuda_getDevice():
+            with _torch().cuda.device(dev):
                 return fn(first, *args, **kwargs)
         return fn(first, *args, **kwargs)
     return run
 
 
+@functools.lru_cache(None)
+def _torch():
+    import torch
+    return torch
+
+
 def _raw_stream(index):
     """Handle of the current torch stream of CUDA device ``index``."""
-    import torch
-    return torch._C._cuda_getCurrentRawStream(index)   # current_stream() builds an object first
+    return _torch()._C._cuda_getCurrentRawStream(index)   # current_stream() builds an object first
 
 
 def _rows(name, t, T, heads, d, dtype, dev):
@@ -614,7 +619,7 @@ def _prep_args(q, k, positions, inv_freq, q_weight, k_weight):
     dtype, dev = q.dtype, q.get_device()
     suffix = _prep_suffix(dtype)
     qs, ks = _rows("q", q, T, H, d, dtype, dev), _rows("k", k, T, Hk, d, dtype, dev)
-    i32, f64 = _dtypes()
+    i32, f64 = _torch().int32, _torch().float64
     ptrs = (q.data_ptr(), k.data_ptr(),
             None if q_weight is None else _dense("q_weight", q_weight, dtype, dev, d),
             None if k_weight is None else _dense("k_weight", k_weight, dtype, dev, d),
@@ -622,13 +627,8 @@ def _prep_args(q, k, positions, inv_freq, q_weight, k_weight):
     return T, H, Hk, d, dtype, suffix, dev, qs, ks, ptrs, 2 * inv_freq.numel()
 
 
-def _dtypes():
-    import torch
-    return torch.int32, torch.float64
-
-
 def _prep_suffix(dtype):
-    import torch
+    torch = _torch()
     if dtype == torch.bfloat16:
         return ""
     if dtype == torch.float16:
@@ -648,7 +648,7 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     positions int32 [T]; inv_freq fp64 [rot_dim/2] (``rope_frequencies``): the
     first rot_dim values of a head are rotated.  Returns (q_out, k_out), dense.
     Runs on the current torch stream."""
-    import torch
+    torch = _torch()
     T, H, Hk, d, dtype, suffix, dev, qs, ks, ptrs, rot = _prep_args(
         q, k, positions, inv_freq, q_weight, k_weight)
     if q_out is None:
@@ -673,7 +673,7 @@ def qk_norm_rope_cache(q, k, v, positions, inv_freq, slots, k_cache, v_cache, q_
     and ``paged_prefill`` at slots (int64 [T]: block * block_size + offset; a
     slot outside the cache, such as -1, stores nothing).  Returns the prepared
     queries, dense; ``q_out`` may be q itself."""
-    import torch
+    torch = _torch()
     T, H, Hk, d, dtype, suffix, dev, qs, ks, ptrs, rot = _prep_args(
         q, k, positions, inv_freq, q_weight, k_weight)
     if suffix != "":
@@ -712,7 +712,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight=No
     inputs.  The weights' gradients are fp32 [d], None where there is no
     weight.  ``workspace`` (optional) is a CUDA tensor of at least
     ``fa_qk_norm_rope_backward_workspace_bytes`` bytes."""
-    import torch
+    torch = _torch()
     T, H, Hk, d, dtype, suffix, dev, qs, ks, ptrs, rot = _prep_args(
         q, k, positions, inv_freq, q_weight, k_weight)
     if dq_out.shape != q.shape or dk_out.shape != k.shape:
@@ -739,7 +739,7 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight=No
 
 def _packed_args(q, k, v, cu_seqlens, dtypes):
     """Checks q, k, v and cu_seqlens of the packed calls."""
-    import torch
+    torch = _torch()
     T, H, d = q.shape
     Hk = k.shape[1] if k.dim() == 3 else -1
     dtype, dev = q.dtype, q.get_device()
@@ -765,7 +765,7 @@ def forward_packed(q, k, v, cu_seqlens, scale=None, causal=True, out=None, lse=N
     Returns (O [T,H,d], LSE fp32 [H,T] or None).  Rows of no sequence are not
     written (they are uninitialised in tensors made here).  Runs on the current
     torch stream."""
-    import torch
+    torch = _torch()
     T, H, Hk, d, S, dtype, dev, qs, ks, vs, cu = _packed_args(
         q, k, v, cu_seqlens, (torch.bfloat16, torch.float16))
     if scale is None:
@@ -796,7 +796,7 @@ def backward_packed(q, k, v, o, lse, dout, cu_seqlens, scale=None, causal=True, 
     (optional) is a CUDA tensor of at least
     ``fa_backward_packed_workspace_bytes`` bytes.  Rows of no sequence are not
     written.  Runs on the current torch stream."""
-    import torch
+    torch = _torch()
     T, H, Hk, d, S, dtype, dev, qs, ks, vs, cu = _packed_args(q, k, v, cu_seqlens,
                                                               (torch.bfloat16,))
     if o.shape != q.shape or dout.shape != q.shape:
@@ -814,7 +814,7 @@ def backward_packed(q, k, v, o, lse, dout, cu_seqlens, scale=None, causal=True, 
     lib = _lib or load()
     if workspace is None:
         nbytes = lib.fa_backward_packed_workspace_bytes(S, T, H, Hk, d)
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     else:
         nbytes = _workspace(workspace, dev)
     _check("fa_backward_packed", lib.fa_backward_packed(
@@ -834,7 +834,7 @@ def paged_prefill(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, s
     tensor of at least ``fa_paged_prefill_workspace_bytes`` bytes.  Returns out
     [T,H,128]; rows of no sequence are not written.  Runs on the current torch
     stream."""
-    import torch
+    torch = _torch()
     T, H, D = q.shape
     dtype, dev = q.dtype, q.get_device()
     if dtype != torch.bfloat16:
