@@ -5,7 +5,10 @@ The C ABI (``include/fattn.h``) is reached through ctypes.  The functions
 arguments as their C counterparts (device pointers as ints, sizes, a stream
 handle) and only marshal them; every step of the computation runs in the CUDA
 kernels of ``libfattn.so``.  ``forward``, ``backward`` and ``paged_decode`` are torch
-conveniences that allocate the outputs and pass the tensors' device pointers.
+conveniences that allocate the outputs and pass the tensors' device pointers; so
+are ``qk_norm_rope``, ``qk_norm_rope_cache``, ``qk_norm_rope_backward`` (norm and
+rotation of queries and keys), ``forward_packed``, ``backward_packed`` (prompts of
+different lengths) and ``paged_prefill`` (chunks of new tokens over a paged cache).
 
 There is no fallback: if ``libfattn.so`` is missing, cannot be loaded, or the
 device is not an sm_103 GPU, the calls raise.

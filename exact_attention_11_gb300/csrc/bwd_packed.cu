@@ -16,6 +16,14 @@
 //                        them), rounded to bf16 into the packed rows
 // Both side kernels are bound by HBM: they read o and dO once, write and read
 // the fp32 accumulators once and write the gradients once.
+//
+// Measured (16 query / 4 key/value heads): 4 documents of 5498 tokens in all, d = 128,
+// causal: 21 + 161 + 15 us, 197 for the call (the main kernel 1112 TFLOP/s, the side
+// kernels 5.4 and 6.7 TB/s); 16 documents of 2168 tokens, d = 64: 8 + 31 + 6, 45 us, of
+// which the main kernel's start and tail are half.  An item per query head and not per
+// group: with two to sixteen steps of a group an item, 50 - 59 us and 213 - 215.
+// Rounding: P and dS to bf16 before their products, as the dense kernels; sums and
+// accumulators fp32; each gradient once.
 #include <cuda_runtime.h>
 
 #include <cmath>
