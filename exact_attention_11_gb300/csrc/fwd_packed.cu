@@ -562,7 +562,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!(ok = __shfl_sync(~0u, ok, 0)) || !it.live) break;
-        claim();
         if (static_cast<int>(blockIdx.x) == a.fault_cta) {
           // Failure-path test: as if the item's copies were lost; the MMA warp's
           // bounded wait for them runs out.
@@ -591,6 +590,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n_max = max(it.n[0], it.n[1]);
         for (int j = 0; j < n_max; ++j) {
           const int tile = it.kt0 + j;
+          // The next item is claimed as late as its loads allow (an item held by a
+          // CTA that is busy is lost to the others: 2 sequences of 4096, 16 heads,
+          // 113 us when it was claimed at the start), decoded behind the last copy.
+          if (j == max(n_max - 2, 0)) claim();
           int pb = 0;
           if (PAGED) {
             if ((j & 3) == 0) {
@@ -626,17 +629,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                           v_bar);
           }
           ++e;
-          if (j == min(1, n_max - 1)) {
-            // With the ring filled: the next item.
-            w = claimed();
-            find();
-          }
         }
         if (!ok) break;
-        if (n_max == 0) {
-          w = claimed();
-          find();
-        }
+        if (n_max == 0) claim();
+        w = claimed();
+        find();
       }
       // (A claim in flight after an abort: its value is read before the exit
       // is counted.)
