@@ -59,6 +59,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -216,13 +217,15 @@ __device__ __forceinline__ Work work_of(const Args &a, const Seq &q) {
 // workspace, 1 KB each at an SM's share of the HBM rate) adds W c / p, and the SMs
 // end up to p apart, 0.7 p on average: p = sqrt(W c / 0.7) balances the two, at
 // least four key tiles; what is shorter than 1.5 p stays whole.  (Constants fitted
-// to a model of the schedule over nine mixes of chunks and contexts; halving or
-// doubling c costs up to 25% on one of them.)  `work`: key tiles of the call's
+// to a model of the schedule over nine mixes of chunks and contexts, then measured:
+// kFixed 2, 2.5, 3 takes 37.8, 36.3, 35.7 us for 16 drafts of up to 6 tokens over up to
+// 4096, but 186, 188, 197 us for 64 single tokens over 4096; with kFixed 1, kRow 0.01 or
+// 1 in place of 0.7 chunks of up to 1024 over up to 16384 take 131 - 135 us, not 102.)  `work`: key tiles of the call's
 // blocks, of one key/value head.  Each block of the sequence cuts its own key tiles
 // into that many.  (Roundings are spelled out: the merge kernel has to reach the
 // same number.)
 __device__ __forceinline__ int parts_of(const Args &a, const Seq &q, int tiles, int64_t work) {
-  constexpr float kFixed = 2.f, kRow = 0.02f, kLeast = 4.f;
+  constexpr float kFixed = 2.5f, kRow = 0.02f, kLeast = 4.f;
   if (a.n_split == 1) return 1;
   const float w = __fmul_rn(__ll2float_rn(work * a.Hk), 1.f / (152.f * 0.7f));
   const float c = __fmaf_rn(kRow, static_cast<float>(min(q.n, 2 * a.tpb) * a.G), kFixed);
@@ -889,9 +892,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st32(o_tmem + c * 32, ov);
           }
         }
-        // A row that has seen no key yet has m = -inf: 0 in its place gives
-        // its (all masked) scores p = 0 rather than NaN.
-        const float nmv = m == -INFINITY ? 0.f : -m;
+        // A row that has seen no key yet has m = -inf: a finite number in its place
+        // gives its (all masked) scores p = 0 rather than NaN.
+        const float nmv = fminf(-m, FLT_MAX);
         const uint64_t nm2 = f2(nmv, nmv);
         uint64_t sum2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
@@ -1156,7 +1159,7 @@ cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, cons
 int paged_max_parts(int T, int S, int H, int Hk, int max_blocks) {
   if (S > kCachedSeqs) return 1;
   const double tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;
-  const double least = std::fmax(4.0, std::sqrt(tiles * Hk / 152 * 2.0 / 0.7));
+  const double least = std::fmax(4.0, std::sqrt(tiles * Hk / 152 * 2.5 / 0.7));
   const double room = 256e6 / (sizeof(float) * (kDecodeHeadSize + 2.0) * T * H);
   const double n = std::fmin(std::fmin(tiles / least + 1, room), 32767);
   return n < 1 ? 1 : static_cast<int>(n);
