@@ -33,9 +33,10 @@
 //    search and hands the decoded item to the other roles.
 //  * The key tile that a sequence ends in also holds the next sequence's rows
 //    (packed) or whatever the cache slots past the context hold (paged).  Their
-//    scores are set to -inf, and since a zero weight does not cancel a NaN, a
-//    warp of the producer warpgroup clears their V rows in shared memory
-//    before P V may use that tile.
+//    scores are set to -inf, and since a zero weight does not cancel a NaN, the
+//    softmax warps that use that tile first clear their V rows in shared memory
+//    before they hand over P.  (A spare warp that did it, and had to follow every
+//    tile for its barriers' sake, cost 2% on long prompts.)
 //  * Paged K and V are read through the TMA views of the grouped decode
 //    (decode_gqa_tc.cu): K in no-swizzle core matrices, V^T in 32-byte-swizzle
 //    blocks of 16 tokens, both K-major B operands here.  Block ids outside the
@@ -113,15 +114,11 @@ enum : int {
   kBarItemFull = 13,   // + ring slot (2)
   kBarItemEmpty = 15,  // + ring slot (2)
   kBarFull = 17,       // + slot: the key or value tile has landed
-  kBarEmpty = kBarFull + kMaxSlots,   // + slot: its MMAs are done, the clearing warp has seen it
-  kBarFix = kBarEmpty + kMaxSlots,    // + slot: a ragged value tile has been cleared past the
-                                      // sequence; one barrier per slot, as a single one could be
-                                      // two phases ahead of the MMA warp's wait
-  kNumBars = kBarFix + kMaxSlots
+  kBarEmpty = kBarFull + kMaxSlots,   // + slot: its MMAs are done
+  kNumBars = kBarEmpty + kMaxSlots + 1   // (even: Misc, which follows, holds 8-byte values)
 };
-// Arrivals that free an item slot: the MMA thread, the V-clearing warp and the
-// eight softmax warps.
-constexpr int kItemConsumers = 1 + 1 + 8;
+// Arrivals that free an item slot: the MMA thread and the eight softmax warps.
+constexpr int kItemConsumers = 1 + 8;
 
 // A decoded work item.
 struct Item {
@@ -472,8 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(kBarDrain), 1);
     for (int s = 0; s < R; ++s) {
       mbar_init(bar(kBarFull + s), 1);
-      mbar_init(bar(kBarEmpty + s), 2);
-      mbar_init(bar(kBarFix + s), 1);
+      mbar_init(bar(kBarEmpty + s), 1);
     }
     misc->abort = 0;
     fence_barrier_init();
@@ -689,7 +685,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     idesc_pv, (!first || kk > 0) ? 1u : 0u);
       };
       int nq = 0, np[2] = {0, 0}, kv = 0;
-      uint32_t fix_parity = 0;   // bit: ring slot
       // First Q K^T of an item's tile t: takes the next Q tile.
       auto first_qk = [&](int t, int n, int kvi, int &qi) -> bool {
         qi = nq++;
@@ -707,16 +702,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (j == n - 1) mma_commit(bar(kBarODone + t));
         return true;
       };
-      // An item as the issuer sees it: key tiles of A and B, and which of them
-      // (counted from the item's first) is the sequence's ragged one.
+      // An item as the issuer sees it: key tiles of A and B.
       struct Step {
-        int live, n_a, n_b, ragged;
+        int live, n_a, n_b;
       };
       auto fetch = [&](int k, Step &x) -> bool {
         if (!take_item(k, false)) return false;
         const volatile Item &i = item_of(k);
         x.live = i.live, x.n_a = i.n[0], x.n_b = i.n[1];
-        x.ragged = ragged_tile(i.kv_len) - i.kt0;
         free_item(k, false);
         return true;
       };
@@ -737,12 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool fetched = false;
         for (int j = 0; j < n_max; ++j) {
           const int kvj = kv + j, ev = 2 * kvj + 1, sv = ev % R;
-          if (j == it.ragged) {
-            if (!(ok = mbar_wait(bar(kBarFix + sv), (fix_parity >> sv) & 1, abort_flag))) break;
-            fix_parity ^= 1u << sv;
-          } else if (!(ok = wait_full(ev))) {
-            break;
-          }
+          if (!(ok = wait_full(ev))) break;
           if (j < it.n_a) {
             if (!(ok = pv_step(0, it.n_a, j, kvj))) break;
             if (j + 1 < it.n_a && !(ok = qk(0, qa, kvj + 1, j + 2 == it.n_a))) break;
@@ -769,50 +757,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Drain: every MMA issued above has completed once this phase does.
       mma_commit(bar(kBarDrain));
       drain_wait(bar(kBarDrain), 0);
-    } else if (warp == 2) {
-      // ------------------------------------- V rows past the sequence's keys
-      int e = 0;
-      for (int k = 0; take_item(k, true); ++k) {
-        const volatile Item &it = item_of(k);
-        const int live = it.live, n_max = max(it.n[0], it.n[1]), kv_len = it.kv_len;
-        const int ragged = ragged_tile(kv_len) - it.kt0;
-        free_item(k, true);
-        if (!live) break;
-        // The warp follows every tile and takes part in freeing it, so that the
-        // ring cannot run past the phase that it waits for.
-        bool ok = true;
-        for (int j = 0; j < 2 * n_max; ++j, ++e) {
-          const int st = e % R;
-          if (!(ok = wait_warp(bar(kBarFull + st), (e / R) & 1, abort_flag))) break;
-          if (j == 2 * ragged + 1) {
-            uint8_t *v = smem + C::kRing + st * C::kTileBytes;
-            const int keep = kv_len % BN;
-            if (PAGED) {
-              // Only the block that the context ends in: the later ones of the
-              // tile were read as zeros.  V^T rows are 16 tokens (32 bytes), the
-              // two 16-byte halves of row r exchanged where r & 4.
-              const int blk = keep / kBlk, rest = keep % kBlk;
-              if (rest != 0)
-                for (int r = lane; r < D; r += 32) {
-                  uint16_t *row = reinterpret_cast<uint16_t *>(v + blk * 4096 + r * 32);
-                  for (int t = rest; t < kBlk; ++t)
-                    row[((((t >> 3) ^ (r >> 2)) & 1) << 3) + (t & 7)] = 0;
-                }
-            } else {
-              for (int i = lane; i < (BN - keep) * 8; i += 32)
-#pragma unroll
-                for (int b = 0; b < C::kBoxes; ++b)
-                  *reinterpret_cast<uint4 *>(v + b * C::kBoxBytes + (keep + (i >> 3)) * 128 +
-                                             (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(kBarFix + st));
-          }
-          if (lane == 0) mbar_arrive(bar(kBarEmpty + st));
-        }
-        if (!ok) break;
-      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -826,25 +770,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t c2 = f2(a.scale_log2, a.scale_log2);
     const int my_tok = r_local / a.G, my_head = r_local - my_tok * a.G;
     uint8_t *stg = smem + C::kStage + (t * 4 + quarter) * 4096;
-    int sc = 0, n_done = 0;
+    int sc = 0, n_done = 0, kv = 0;   // kv: key tiles of the items before
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!(ok = take_item(k, true))) break;
       const volatile Item &it = item_of(k);
-      const int live = it.live, n_mine = it.n[t], part = it.part;
-      const bool split = it.split != 0;
+      if (!it.live) break;
+      const int n_mine = it.n[t];
       // Keys below lim are visible to this row; a tile needs the test only
       // where it passes the limit of the query tile's first token.
-      const int tile_pos = it.pos0 + t * a.tpb, key0 = it.kt0 * BN;
-      const int lim = min(it.kv_len, tile_pos + my_tok + 1) - key0;
-      const int lim_first = min(it.kv_len, tile_pos + 1) - key0;
-      // This row's place in the output, [token][head]; -1: it holds no query.
-      const int row = it.row0 + t * a.tpb + my_tok, head = it.kvh * a.G + my_head;
-      const int my_out = my_tok < min(it.n_tok[t], a.tpb) ? row * a.H + head : -1;
-      free_item(k, true);
-      if (!live) break;
+      const int kv_len = it.kv_len, kt0 = it.kt0, tile_pos = it.pos0 + t * a.tpb;
+      const int lim = min(kv_len, tile_pos + my_tok + 1) - kt0 * BN;
+      const int lim_first = min(kv_len, tile_pos + 1) - kt0 * BN;
+      // Which of this query tile's steps clears V, and how many of V's rows stay:
+      // where both tiles visit the sequence's last key tile A does, whose P V goes first.
+      const int ragged = ragged_tile(kv_len) - kt0;
+      const int clear = ragged >= 0 && (t == 0 || it.n[0] <= ragged) ? ragged * BN + kv_len % BN : -1;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n_mine; ++j, ++sc) {
+        if (j == clear >> 7) {   // (-1: never)
+          const int e = 2 * (kv + j) + 1, st = e % R, keep = clear & (BN - 1);
+          if (!(ok = wait_warp(bar(kBarFull + st), (e / R) & 1, abort_flag))) break;
+          uint8_t *v = smem + C::kRing + st * C::kTileBytes;
+          if (PAGED) {
+            // Only the block that the context ends in: the later ones of the
+            // tile were read as zeros.  V^T rows are 16 tokens (32 bytes), the
+            // two 16-byte halves of row r exchanged where r & 4.
+            uint16_t *vr = reinterpret_cast<uint16_t *>(v + keep / kBlk * 4096 + r_local * 32);
+            for (int u = keep % kBlk; u % kBlk != 0; ++u)
+              vr[((((u >> 3) ^ (r_local >> 2)) & 1) << 3) + (u & 7)] = 0;
+          } else {
+            for (int i = r_local; i < (BN - keep) * 8; i += BM)
+#pragma unroll
+              for (int b = 0; b < C::kBoxes; ++b)
+                *reinterpret_cast<uint4 *>(v + b * C::kBoxBytes + (keep + (i >> 3)) * 128 +
+                                           (i & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();   // ahead of this warp's arrivals on PReady
+        }
         if (!(ok = wait_warp(bar(kBarSFull + t), sc & 1, abort_flag))) break;
         tc_fence_after();
         uint32_t sv[4][32];
@@ -922,6 +885,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = l * alpha + (sa.x + sa.y);
       }
       if (!ok) break;
+      // (Read here: the loop above has no registers to keep these.)
+      kv += max(it.n[0], it.n[1]);
+      const int part = PAGED && it.split ? it.part : -1;   // -1: the context is not cut
+      // This row's place in the output, [token][head]; -1: it holds no query.
+      const int row = it.row0 + t * a.tpb + my_tok, head = it.kvh * a.G + my_head;
+      const int my_out = my_tok < min(it.n_tok[t], a.tpb) ? row * a.H + head : -1;
+      free_item(k, true);
       // Epilogue, once the last P V is done.  A tile without key tiles writes
       // zeros if it has none at all, and nothing if other partitions have them.
       const bool some = n_mine > 0;
@@ -931,7 +901,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n_done;
         tc_fence_after();
       }
-      if (PAGED && split) {
+      if (PAGED && part >= 0) {
         // Unnormalised fp32 rows, a thread's own row from its registers (the few
         // rows of a split block do not repay staging them).
         const int64_t base = static_cast<int64_t>(part) * a.T * a.H;
