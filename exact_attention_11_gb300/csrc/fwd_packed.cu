@@ -819,8 +819,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((j + 1) * BN > lim_first) {
           const int lim_j = lim - j * BN;
 #pragma unroll
-          for (int c = 0; c < BN; ++c)
-            if (c >= lim_j) S_(c) = __float_as_uint(-INFINITY);
+          for (int w = 0; w < 4; ++w) {   // by bit masks: half the instructions of compares
+            const int n = lim_j - 32 * w;
+            const uint32_t bits = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (((bits >> c) & 1u) == 0u) sv[w][c] = __float_as_uint(-INFINITY);
+          }
         }
         float mx[4];
 #pragma unroll
