@@ -100,7 +100,7 @@ struct Cfg {
   static constexpr int kBar = kStage + (PAGED ? 0 : 8 * 4096);
   static constexpr int kAlloc = kBar + 3072;
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
-  static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 256 + D;
+  static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 384;   // O: S + 256
 };
 
 constexpr int kMaxSlots = 8;
@@ -133,6 +133,7 @@ struct Item {
   int n[2];          // key tiles of tiles A and B in this partition
   int part;          // partition
   int split;         // the rows go to the partition workspace
+  int clear[2];      // the step in which tile A's (B's) softmax clears V's last rows, or < 0
 };
 
 constexpr int kCachedSeqs = 112;
@@ -344,6 +345,10 @@ __device__ __forceinline__ bool decode_item(const Args &a, const Misc *m, int n_
   it.kt0 = it.part * size;
 #pragma unroll
   for (int t = 0; t < 2; ++t) it.n[t] = clampi(total[t] - it.kt0, 0, size);
+  // Where both tiles visit the sequence's ragged last key tile A clears its V, whose
+  // P V goes first.
+  it.clear[0] = q.kv_len % BN != 0 ? q.kv_len / BN - it.kt0 : -1;
+  it.clear[1] = it.n[0] <= it.clear[0] ? it.clear[0] : -1;
   return it.part == 0 || it.n[0] > 0 || it.n[1] > 0;
 }
 
@@ -413,11 +418,6 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t ph) {
   const uint64_t t0 = globaltimer_ns();
   while (!mbar_try_wait(bar, ph) && globaltimer_ns() - t0 < kWaitLimitNs) {
   }
-}
-
-// The key tile whose V holds rows past the sequence's keys, or -1.
-__device__ __forceinline__ int ragged_tile(int kv_len) {
-  return kv_len % BN != 0 ? kv_len / BN : -1;
 }
 
 template <int D, bool F16, bool PAGED>
@@ -763,44 +763,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ softmax
     const int t = (warp - 4) >> 2;                 // query tile: 0 = A, 1 = B
     const int quarter = warp & 3;                  // TMEM lanes 32*quarter .. +31
-    const int r_local = quarter * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t s_tmem = tmem + lane_off + (t ? C::kColS1 : C::kColS0);
-    const uint32_t o_tmem = tmem + lane_off + (t ? C::kColO1 : C::kColO0);
+    const uint32_t o_tmem = s_tmem + 256;
     const uint64_t c2 = f2(a.scale_log2, a.scale_log2);
-    const int my_tok = r_local / a.G, my_head = r_local - my_tok * a.G;
-    uint8_t *stg = smem + C::kStage + (t * 4 + quarter) * 4096;
-    int sc = 0, n_done = 0, kv = 0;   // kv: key tiles of the items before
+    // The loop over key tiles has no register to spare: what an item's start and end
+    // need is computed there, or read from the item again (8 prompts up to 4096: 189 us
+    // with eleven registers spilled, 184.5 with one).
+    auto row_in_tile = [&]() { return quarter * 32 + static_cast<int>(threadIdx.x & 31); };
+    int phases = 0;   // bit 0: S's phase, bit 1: O's
+    int kv = 0;       // key tiles of the items before
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!(ok = take_item(k, true))) break;
       const volatile Item &it = item_of(k);
       if (!it.live) break;
       const int n_mine = it.n[t];
-      // Keys below lim are visible to this row; a tile needs the test only
-      // where it passes the limit of the query tile's first token.
-      const int kv_len = it.kv_len, kt0 = it.kt0, tile_pos = it.pos0 + t * a.tpb;
-      const int lim = min(kv_len, tile_pos + my_tok + 1) - kt0 * BN;
-      const int lim_first = min(kv_len, tile_pos + 1) - kt0 * BN;
-      // Which of this query tile's steps clears V, and how many of V's rows stay:
-      // where both tiles visit the sequence's last key tile A does, whose P V goes first.
-      const int ragged = ragged_tile(kv_len) - kt0;
-      const int clear = ragged >= 0 && (t == 0 || it.n[0] <= ragged) ? ragged * BN + kv_len % BN : -1;
+      // Keys below lim are visible to this row (the first is key 0 of the partition).
+      const int lim = min(it.kv_len, it.pos0 + t * a.tpb + row_in_tile() / a.G + 1) - it.kt0 * BN;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < n_mine; ++j, ++sc) {
-        if (j == clear >> 7) {   // (-1: never)
-          const int e = 2 * (kv + j) + 1, st = e % R, keep = clear & (BN - 1);
+      for (int j = 0; j < n_mine; ++j, phases ^= 1) {
+        if (j == it.clear[t]) {
+          const int e = 2 * (kv + j) + 1, st = e % R, keep = it.kv_len % BN, r = row_in_tile();
           if (!(ok = wait_warp(bar(kBarFull + st), (e / R) & 1, abort_flag))) break;
           uint8_t *v = smem + C::kRing + st * C::kTileBytes;
           if (PAGED) {
             // Only the block that the context ends in: the later ones of the
             // tile were read as zeros.  V^T rows are 16 tokens (32 bytes), the
             // two 16-byte halves of row r exchanged where r & 4.
-            uint16_t *vr = reinterpret_cast<uint16_t *>(v + keep / kBlk * 4096 + r_local * 32);
+            uint16_t *vr = reinterpret_cast<uint16_t *>(v + keep / kBlk * 4096 + r * 32);
             for (int u = keep % kBlk; u % kBlk != 0; ++u)
-              vr[((((u >> 3) ^ (r_local >> 2)) & 1) << 3) + (u & 7)] = 0;
+              vr[((((u >> 3) ^ (r >> 2)) & 1) << 3) + (u & 7)] = 0;
           } else {
-            for (int i = r_local; i < (BN - keep) * 8; i += BM)
+            for (int i = r; i < (BN - keep) * 8; i += BM)
 #pragma unroll
               for (int b = 0; b < C::kBoxes; ++b)
                 *reinterpret_cast<uint4 *>(v + b * C::kBoxBytes + (keep + (i >> 3)) * 128 +
@@ -808,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();   // ahead of this warp's arrivals on PReady
         }
-        if (!(ok = wait_warp(bar(kBarSFull + t), sc & 1, abort_flag))) break;
+        if (!(ok = wait_warp(bar(kBarSFull + t), phases & 1, abort_flag))) break;
         tc_fence_after();
         uint32_t sv[4][32];
 #pragma unroll
@@ -816,8 +811,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_wait_ld(sv[c]);
 #define S_(c) sv[(c) >> 5][(c) & 31]
-        if ((j + 1) * BN > lim_first) {
-          const int lim_j = lim - j * BN;
+        const int lim_j = lim - j * BN;
+        if (__any_sync(~0u, lim_j < BN)) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {   // by bit masks: half the instructions of compares
             const int n = lim_j - 32 * w;
@@ -894,7 +889,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       kv += max(it.n[0], it.n[1]);
       const int part = PAGED && it.split ? it.part : -1;   // -1: the context is not cut
       // This row's place in the output, [token][head]; -1: it holds no query.
-      const int row = it.row0 + t * a.tpb + my_tok, head = it.kvh * a.G + my_head;
+      const int my_tok = row_in_tile() / a.G;
+      const int row = it.row0 + t * a.tpb + my_tok;
+      const int head = it.kvh * a.G + row_in_tile() - my_tok * a.G;
       const int my_out = my_tok < min(it.n_tok[t], a.tpb) ? row * a.H + head : -1;
       free_item(k, true);
       // Epilogue, once the last P V is done.  A tile without key tiles writes
@@ -902,8 +899,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool some = n_mine > 0;
       if (!some && part > 0) continue;
       if (some) {
-        if (!(ok = wait_warp(bar(kBarODone + t), n_done & 1, abort_flag))) break;
-        ++n_done;
+        if (!(ok = wait_warp(bar(kBarODone + t), (phases >> 1) & 1, abort_flag))) break;
+        phases ^= 2;
         tc_fence_after();
       }
       if (PAGED && part >= 0) {
@@ -926,6 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const float inv_l = l == 0.f ? 0.f : 1.f / l;
+      uint8_t *stg = smem + C::kStage + (t * 4 + quarter) * 4096;
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
         uint32_t ov[2][32];
