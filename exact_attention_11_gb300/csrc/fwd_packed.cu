@@ -51,10 +51,10 @@
 // 1.37; for chunks of one query tile that chain alone, 1.38 us a key tile; for a few
 // tokens over long contexts the 24 copies of a paged key tile and HBM; for short
 // prompts the start (5 us) and the chain of an SM's few items.  Measured: 8 prompts up
-// to 4096 tokens, 32 / 8 heads, d = 128, causal, 196 us (1393 TFLOP/s); one of 16384,
-// 8 / 1 heads, fp16, 340 us (1616); 32 prompts up to 200, 16 heads, d = 64, 18 us;
-// chunks of 4 x 1024 tokens over 8192, 375 us (1375 TFLOP/s), up to 1024 over up to
-// 16384, 108 us; 64 single tokens over 4096, 190 us (5.6 TB/s).
+// to 4096 tokens, 32 / 8 heads, d = 128, causal, 184 us (1478 TFLOP/s); one of 16384,
+// 8 / 1 heads, fp16, 330 us (1665); 32 prompts up to 200, 16 heads, d = 64, 17 us;
+// chunks of 4 x 1024 tokens over 8192, 355 us (1453 TFLOP/s), up to 1024 over up to
+// 16384, 97 us; 64 single tokens over 4096, 183 us (5.9 TB/s).
 // Rounding: P to the element type before P V, O once at the end; scores, maxima, sums,
 // partial rows and their merge are fp32.
 #include <cuda.h>
@@ -216,9 +216,9 @@ __device__ __forceinline__ Work work_of(const Args &a, const Seq &q) {
 // end up to p apart, 0.7 p on average: p = sqrt(W c / 0.7) balances the two, at
 // least four key tiles; what is shorter than 1.5 p stays whole.  (Constants fitted
 // to a model of the schedule over nine mixes of chunks and contexts, then measured:
-// kFixed 2, 2.5, 3 takes 37.8, 36.3, 35.7 us for 16 drafts of up to 6 tokens over up to
+// kFixed 2, 2.5, 3 took 37.8, 36.3, 35.7 us for 16 drafts of up to 6 tokens over up to
 // 4096, but 186, 188, 197 us for 64 single tokens over 4096; with kFixed 1, kRow 0.01 or
-// 1 in place of 0.7 chunks of up to 1024 over up to 16384 take 131 - 135 us, not 102.)  `work`: key tiles of the call's
+// 1 in place of 0.7 chunks of up to 1024 over up to 16384 took 131 - 135 us, not 102.)  `work`: key tiles of the call's
 // blocks, of one key/value head.  Each block of the sequence cuts its own key tiles
 // into that many.  (Roundings are spelled out: the merge kernel has to reach the
 // same number.)
@@ -591,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tile = it.kt0 + j;
           // The next item is claimed as late as its loads allow (an item held by a
           // CTA that is busy is lost to the others: 2 sequences of 4096, 16 heads,
-          // 113 us when it was claimed at the start), decoded behind the last copy.
+          // 113 us when it was claimed at the start, 94 so), decoded behind the last copy.
           if (j == max(n_max - 2, 0)) claim();
           int pb = 0;
           if (PAGED) {
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t c2 = f2(a.scale_log2, a.scale_log2);
     // The loop over key tiles has no register to spare: what an item's start and end
     // need is computed there, or read from the item again (8 prompts up to 4096: 189 us
-    // with eleven registers spilled, 184.5 with one).
+    // with eleven registers spilled, 184.5 with two).
     auto row_in_tile = [&]() { return quarter * 32 + static_cast<int>(threadIdx.x & 31); };
     int phases = 0;   // bit 0: S's phase, bit 1: O's
     int kv = 0;       // key tiles of the items before
