@@ -769,10 +769,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t c2 = f2(a.scale_log2, a.scale_log2);
     // The loop over key tiles has no register to spare: what an item's start and end
     // need is computed there, or read from the item again (8 prompts up to 4096: 189 us
-    // with eleven registers spilled, 184.5 with two).
+    // with eleven registers spilled, 183.5 with one).
     auto row_in_tile = [&]() { return quarter * 32 + static_cast<int>(threadIdx.x & 31); };
-    int phases = 0;   // bit 0: S's phase, bit 1: O's
-    int kv = 0;       // key tiles of the items before
+    int phases = 0;   // bit 0: S's phase, bit 1: O's; above: key tiles of the items before
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!(ok = take_item(k, true))) break;
@@ -784,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n_mine; ++j, phases ^= 1) {
         if (j == it.clear[t]) {
-          const int e = 2 * (kv + j) + 1, st = e % R, keep = it.kv_len % BN, r = row_in_tile();
+          const int e = 2 * ((phases >> 2) + j) + 1, st = e % R, keep = it.kv_len % BN, r = row_in_tile();
           if (!(ok = wait_warp(bar(kBarFull + st), (e / R) & 1, abort_flag))) break;
           uint8_t *v = smem + C::kRing + st * C::kTileBytes;
           if (PAGED) {
@@ -822,16 +821,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (((bits >> c) & 1u) == 0u) sv[w][c] = __float_as_uint(-INFINITY);
           }
         }
-        float mx[4];
+        float mx[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
           mx[i] = fmaxf(__uint_as_float(S_(2 * i)), __uint_as_float(S_(2 * i + 1)));
 #pragma unroll
-        for (int c = 8; c < BN; c += 8)
+        for (int c = 4; c < BN; c += 4)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 2; ++i)
             mx[i] = fmax3(mx[i], __uint_as_float(S_(c + 2 * i)), __uint_as_float(S_(c + 2 * i + 1)));
-        const float tmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+        const float tmax = fmaxf(mx[0], mx[1]) * a.scale_log2;
         float alpha = 1.f;
         if (tmax > m + kRescaleThreshold) {  // also true while m = -inf
           alpha = ex2_approx(m - tmax);
@@ -886,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       // (Read here: the loop above has no registers to keep these.)
-      kv += max(it.n[0], it.n[1]);
+      phases += 4 * max(it.n[0], it.n[1]);
       const int part = PAGED && it.split ? it.part : -1;   // -1: the context is not cut
       // This row's place in the output, [token][head]; -1: it holds no query.
       const int my_tok = row_in_tile() / a.G;
