@@ -153,13 +153,20 @@ int encode_e4m3_map(CUtensorMap *m, const void *base, int BH, int rows, int inne
 // extent is the largest int block id: which blocks are read comes from the
 // block tables, as in the plain decode.
 // (fa_paged_prefill knows the cache's block count and passes it: ids outside
-// the cache then read as zeros.)
+// the cache then read as zeros.  Its K view is one whole block a box, 4 KB:
+// d-groups before token halves, so that the halves' matrices land 2 KB apart
+// as two boxes of the decode's view do.)
 int encode_paged_kv_maps(CUtensorMap *tk, CUtensorMap *tv, const void *k_cache,
-                         const void *v_cache, int num_kv_heads, int num_blocks = 0x7fffffff) {
+                         const void *v_cache, int num_kv_heads, int num_blocks = 0x7fffffff,
+                         bool whole_blocks = false) {
   const cuuint64_t nb = (cuuint64_t)num_blocks, hk = (cuuint64_t)num_kv_heads;
-  const cuuint64_t kd[5] = {64, 2, 16, hk, nb};
-  const cuuint64_t ks[4] = {128, 256, 4096, 4096 * hk};
-  const cuuint32_t kb[5] = {64, 1, 16, 1, 1};
+  const cuuint64_t half_first[5] = {64, 2, 16, hk, nb}, half_last[5] = {64, 16, 2, hk, nb};
+  const cuuint64_t half_first_s[4] = {128, 256, 4096, 4096 * hk};
+  const cuuint64_t half_last_s[4] = {256, 128, 4096, 4096 * hk};
+  const cuuint32_t half_box[5] = {64, 1, 16, 1, 1}, block_box[5] = {64, 16, 2, 1, 1};
+  const cuuint64_t *kd = whole_blocks ? half_last : half_first;
+  const cuuint64_t *ks = whole_blocks ? half_last_s : half_first_s;
+  const cuuint32_t *kb = whole_blocks ? block_box : half_box;
   const cuuint64_t vd[4] = {16, 128, hk, nb};
   const cuuint64_t vs[3] = {32, 4096, 4096 * hk};
   const cuuint32_t vb[4] = {16, 128, 1, 1};
@@ -985,7 +992,8 @@ int fa_paged_prefill(const void *q, const void *k_cache, const void *v_cache,
                             fattn::packed_tile_tokens(group),
                             CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) != FA_OK)
     return rc;
-  if ((rc = encode_paged_kv_maps(&tk, &tv, k_cache, v_cache, num_kv_heads, num_blocks)) != FA_OK)
+  if ((rc = encode_paged_kv_maps(&tk, &tv, k_cache, v_cache, num_kv_heads, num_blocks,
+                                 true)) != FA_OK)
     return rc;
   fattn::PackedProblem p{};
   p.o = out, p.cu_seqlens = cu_seqlens, p.context_lens = context_lens;

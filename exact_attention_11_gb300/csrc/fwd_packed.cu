@@ -37,10 +37,10 @@
 //    softmax warps that use that tile first clear their V rows in shared memory
 //    before they hand over P.  (A spare warp that did it, and had to follow every
 //    tile for its barriers' sake, cost 2% on long prompts.)
-//  * Paged K and V are read through the TMA views of the grouped decode
-//    (decode_gqa_tc.cu): K in no-swizzle core matrices, V^T in 32-byte-swizzle
-//    blocks of 16 tokens, both K-major B operands here.  Block ids outside the
-//    cache read as zeros.
+//  * Paged K and V are read as in the grouped decode (decode_gqa_tc.cu): K in
+//    no-swizzle core matrices, V^T in 32-byte-swizzle blocks of 16 tokens, both
+//    K-major B operands here, one copy a block (K in two halves a block: 355 us for
+//    4 x 1024 tokens over 8192, not 345).  Block ids outside the cache read as zeros.
 //  * Few rows over long contexts do not fill the GPU, and a long context beside
 //    short ones would finish alone: a block's context is then cut into equal
 //    partitions (parts_of); each writes its unnormalised fp32 rows and (max, sum),
@@ -49,7 +49,7 @@
 // What bounds it: for long prompts the tensor pipe and the softmax chain (S out of
 // TMEM, exponentials, P back) of a two-tile step, 1.4 us where the MMAs alone take
 // 1.37; for chunks of one query tile that chain alone, 1.38 us a key tile; for a few
-// tokens over long contexts the 24 copies of a paged key tile and HBM; for short
+// tokens over long contexts the 16 copies of a paged key tile and HBM; for short
 // prompts the start (5 us) and the chain of an SM's few items.  Measured: 8 prompts up
 // to 4096 tokens, 32 / 8 heads, d = 128, causal, 184 us (1478 TFLOP/s); one of 16384,
 // 8 / 1 heads, fp16, 330 us (1665); 32 prompts up to 200, 16 heads, d = 64, 17 us;
@@ -605,10 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t k_dst = s_base + C::kRing + (e % R) * C::kTileBytes;
           const uint32_t k_bar = bar(kBarFull + e % R);
           if (PAGED) {
-            if (lane < kTileBlocks) {
+            if (lane < kTileBlocks)
               tma_load_5d(k_dst + lane * 4096, &tm_k, 0, 0, 0, it.kvh, pb, k_bar);
-              tma_load_5d(k_dst + lane * 4096 + 2048, &tm_k, 0, 1, 0, it.kvh, pb, k_bar);
-            }
           } else if (lane == 0) {
             for (int b = 0; b < C::kBoxes; ++b)
               tma_load_3d(k_dst + b * C::kBoxBytes, &tm_k, b * 64, it.kv0 + tile * BN, it.kvh,
