@@ -48,13 +48,13 @@
 //
 // What bounds it: for long prompts the tensor pipe and the softmax chain (S out of
 // TMEM, exponentials, P back) of a two-tile step, 1.4 us where the MMAs alone take
-// 1.37; for chunks of one query tile that chain alone, 1.38 us a key tile; for a few
+// 1.37; for chunks of one query tile that chain alone, 1.3 us a key tile; for a few
 // tokens over long contexts the 16 copies of a paged key tile and HBM; for short
 // prompts the start (5 us) and the chain of an SM's few items.  Measured: 8 prompts up
-// to 4096 tokens, 32 / 8 heads, d = 128, causal, 184 us (1478 TFLOP/s); one of 16384,
+// to 4096 tokens, 32 / 8 heads, d = 128, causal, 182 us (1497 TFLOP/s); one of 16384,
 // 8 / 1 heads, fp16, 330 us (1665); 32 prompts up to 200, 16 heads, d = 64, 17 us;
-// chunks of 4 x 1024 tokens over 8192, 355 us (1453 TFLOP/s), up to 1024 over up to
-// 16384, 97 us; 64 single tokens over 4096, 183 us (5.9 TB/s).
+// chunks of 4 x 1024 tokens over 8192, 345 us (1494 TFLOP/s), up to 1024 over up to
+// 16384, 93 us; 64 single tokens over 4096, 180 us (6.0 TB/s).
 // Rounding: P to the element type before P V, O once at the end; scores, maxima, sums,
 // partial rows and their merge are fp32.
 #include <cuda.h>
@@ -992,7 +992,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the partitions of the rows whose context was cut: gridDim.y blocks per
 // sequence (which end at once if it was not), one warp per (token, head), four
 // dimensions a lane.  By sequence, because a grid over all rows costs 40 us where few
-// are cut; 5 us for 16 chunks of up to 6 tokens, 32 heads, of which the rows' loads
+// are cut; 4 us for 16 chunks of up to 6 tokens, 32 heads, of which the rows' loads
 // are the smaller part and the launch and the chain of (max, sum) the larger.
 __global__ void __launch_bounds__(256) paged_merge_kernel(const Args a) {
   constexpr int D = kDecodeHeadSize;
