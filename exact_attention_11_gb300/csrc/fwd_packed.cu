@@ -81,6 +81,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units (see fwd_bf16.cu)
 constexpr int kBlk = kDecodeBlockSize;      // 16 tokens per cache block
 constexpr int kTileBlocks = BN / kBlk;      // 8 cache blocks per key tile
+constexpr int kBarArea = 3 * 1024;          // bytes of barriers, items and sequence bounds
 
 // Shared memory: two Q tile buffers, a ring of `kSlots` key or value tiles (K of
 // tile 0, V of tile 0, K of tile 1, ...), output staging (packed), barriers and
@@ -98,7 +99,7 @@ struct Cfg {
   static constexpr int kRing = kQ + 2 * kTileBytes;
   static constexpr int kStage = kRing + kSlots * kTileBytes;   // 8 x 4 KB
   static constexpr int kBar = kStage + (PAGED ? 0 : 8 * 4096);
-  static constexpr int kAlloc = kBar + 3072;
+  static constexpr int kAlloc = kBar + kBarArea;
   static_assert(kAlloc <= 227 * 1024, "shared memory budget");
   static constexpr uint32_t kColS0 = 0, kColS1 = 128, kColO0 = 256, kColO1 = 384;   // O: S + 256
 };
@@ -150,7 +151,7 @@ struct Misc {
   int key[kCachedSeqs];         // scratch of the sort
   int16_t n_parts[kCachedSeqs];
 };
-static_assert(8 * kNumBars + sizeof(Misc) <= 3072, "barrier area");
+static_assert(8 * kNumBars + sizeof(Misc) <= kBarArea, "barrier area");
 // Status latched when the dynamic shared memory does not start on a 1024-byte
 // boundary (the kernel then does nothing).
 constexpr int kDevBadSmemBase = -2;
