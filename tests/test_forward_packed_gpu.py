@@ -116,6 +116,27 @@ def test_sequences_do_not_mix(bad):
         assert torch.equal(o[rows], o2[rows]) and torch.equal(lse[:, rows], lse2[:, rows])
 
 
+@pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
+@pytest.mark.parametrize("H,Hk", [(2, 2), (8, 2), (6, 2), (40, 1)])
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+def test_bad_neighbours_of_every_last_tile(H, Hk, d, dtype, causal):
+    """Last key tiles that both query tiles of a block visit, that only the second
+    one does, and that end one key in, each followed by a sequence of NaN or Inf."""
+    lens = [200, 3, 129, 40, 257, 1, 385, 64, 5, 130, 66]
+    q, k, v, cu = draw(lens, H, Hk, d, dtype, seed=44)
+    o, lse = fa.forward_packed(q, k, v, cu, causal=causal)
+    ends = cu.tolist()
+    for bad in (float("nan"), float("-inf")):
+        for s in range(1, len(lens), 2):
+            for x in (q, k, v):
+                x[ends[s]:ends[s + 1]] = bad
+        o2, lse2 = fa.forward_packed(q, k, v, cu, causal=causal)
+        for s in range(0, len(lens), 2):
+            rows = slice(ends[s], ends[s + 1])
+            assert torch.equal(o[rows], o2[rows]) and torch.equal(lse[:, rows], lse2[:, rows])
+    check(q[:200], k[:200], v[:200], cu[:2], o[:200], lse[:, :200], causal)
+
+
 def test_scores_of_large_size():
     """Scores of magnitude 10^3: a running maximum that keeps growing."""
     q, k, v, cu = draw([300, 20], 2, 1, 128, BF16, seed=6)
