@@ -489,6 +489,8 @@ __global__ void __launch_bounds__(kThreads, kGradBlocks<T>) qk_prep_grad_kernel(
   constexpr int kHeads = kRows / kMaxTok;   // heads per round
   __shared__ __align__(16) float4 cs[2][kMaxTok * Table<L>::kStride];   // by tile parity
   __shared__ float sums[kThreads / 32][D];
+  // The kernel that joins the blocks' sums may be scheduled; it waits for this one.
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int l = threadIdx.x % L, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int c0, c1;
   chunks_of<HALF>(l, a.rot, c0, c1);
@@ -606,6 +608,7 @@ __global__ void __launch_bounds__(1024)
   const int n = is_k ? k_blocks : q_blocks;
   const float *src = partial + static_cast<int64_t>(is_k ? q_blocks : 0) * D + col;
   float *out = is_k ? dkw : dqw;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (out == nullptr) return;
   float v = 0.f;
 #pragma unroll 8
@@ -691,9 +694,17 @@ cudaError_t launch_grad_d(PrepGradArgs a, bool half, float *dqw, float *dkw, cud
   else
     qk_prep_grad_kernel<T, D, false><<<grid, kThreads, 0, stream>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess || a.partial == nullptr) return e;
-  qk_prep_grad_join_kernel<<<2 * D / 32, dim3(32, 32), 0, stream>>>(a.partial, a.q_blocks,
-                                                                    a.k_blocks, D, dqw, dkw);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * D / 32);
+  cfg.blockDim = dim3(32, 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, qk_prep_grad_join_kernel, static_cast<const float *>(a.partial),
+                            a.q_blocks, a.k_blocks, D, dqw, dkw);
 }
 
 template <typename T>
