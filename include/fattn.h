@@ -1,6 +1,7 @@
 /*
  * fattn.h -- C ABI of libfattn: exact scaled-dot-product attention on one
- * NVIDIA GB300 (sm_103a).
+ * NVIDIA GB300 (sm_103a), dense, packed and over a paged cache, and the norm
+ * and rotation of its queries and keys.
  *
  * Every call takes plain device pointers and sizes, enqueues its kernels on
  * `stream` and returns without synchronising.  Nothing here depends on any
