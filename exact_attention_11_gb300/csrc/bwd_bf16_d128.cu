@@ -264,15 +264,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_do);
       int nq = 0, ndo = 0, nkv = 0;   // halves (and K/V pairs) issued so far
       bool ok = true;
+      auto claim = [&]() { return static_cast<int>(gridDim.x) + atomicAdd(sched, 1); };
       for (int k = 0; ok; ++k) {
         const int islot = k & 1;
         if (!(ok = mbar_wait(bar(kBarItemEmpty + islot), ((k >> 1) & 1) ^ 1, abort_flag))) break;
-        int w = atomicAdd(sched, 1);
+        // The CTA's own first item, then claimed ones.
+        int w = k == 0 ? static_cast<int>(blockIdx.x) : claim();
         int4 entry = make_int4(0, 0, 0, 0);
         if (PACKED) {
           // Entries of length 0 end a sorted table, else are passed over.
           while (w < n_items && (entry = pk.table[w / BH]).y == 0)
-            w = pk.sorted ? n_items : atomicAdd(sched, 1);
+            w = pk.sorted ? n_items : claim();
           // (Offsets that decrease leave entries unwritten: whatever they hold, the
           // item stays inside the tensors.)
           entry.x = min(max(entry.x, 0), pk.tokens - 1);
