@@ -1044,12 +1044,15 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const Args a) {
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, off));
       mx = fmaxf(mx, m);
-      if (mx == -INFINITY) continue;                     // no key seen so far
-      const float f = ex2_approx(ml.x - mx), old = ex2_approx(m - mx);
+      // No score so far but NaN, which a maximum passes over, or -inf: the sums are NaN,
+      // which the row has to become, or 0.
+      const bool none = mx == -INFINITY;
+      const float f = none ? 0.f : ex2_approx(ml.x - mx), old = none ? 1.f : ex2_approx(m - mx);
       float sum = f * ml.y;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(~0u, sum, off);
       l = fmaf(l, old, sum);
+      if (none) continue;
       o.x *= old, o.y *= old, o.z *= old, o.w *= old;
       m = mx;
       const float *src = a.ws_o + (p0 * stride + row) * D + lane * 4;

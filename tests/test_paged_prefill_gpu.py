@@ -229,3 +229,18 @@ def test_helper_refuses():
     x = draw([1], [9000], 4, 2, seed=2)
     with pytest.raises(fa.FattnError):
         fa.paged_prefill(*x, workspace=small)
+
+
+@pytest.mark.parametrize("lens,ctx", [([3, 9], [40, 300]), ([1], [9000]), ([3, 2, 140], [9000, 5, 700]),
+                                      ([2], [40000])], ids=str)
+def test_a_nan_query_gives_a_nan_row(lens, ctx):
+    """Whether its context is cut into partitions or not; the other rows keep
+    their bits."""
+    q, kc, vc, bt, c, cu = draw(lens, ctx, 8, 2, seed=14, poison=False)
+    want = fa.paged_prefill(q, kc, vc, bt, c, cu)
+    q[0, 3, 5] = q[len(q) - 1, 6, 127] = float("nan")
+    out = fa.paged_prefill(q, kc, vc, bt, c, cu)
+    for row, head in ((0, 3), (len(q) - 1, 6)):
+        assert out[row, head].isnan().all()
+        out[row, head] = want[row, head]
+    assert torch.equal(out, want)
