@@ -529,13 +529,18 @@ def forward_fp8(x, scale=None, causal=False, out=None, lse=None, want_lse=True):
 def _on_device(fn):
     """Runs ``fn`` with its first tensor's device current: the C calls work on
     the current device, and a caller's may be another one."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def run(first, *args, **kwargs):
+    def run(*args, **kwargs):
+        first = args[0] if args else kwargs.get(name)
+        if first is None:
+            return fn(*args, **kwargs)      # a TypeError that names what is missing
         dev = first.get_device()
         if dev >= 0 and dev != _torch()._C._cuda_getDevice():
             with _torch().cuda.device(dev):
-                return fn(first, *args, **kwargs)
-        return fn(first, *args, **kwargs)
+                return fn(*args, **kwargs)
+        return fn(*args, **kwargs)
     return run
 
 

@@ -2,6 +2,7 @@
 import math
 
 import pytest
+import torch
 
 import exact_attention_11_gb300 as fa
 from exact_attention_11_gb300 import _build
@@ -100,3 +101,24 @@ def test_backward_workspace(lib):
     # one padded block: dQ of 4 heads, dK and dV of 2, vectors, table entry
     assert size(1, 10, 4, 2, 64) == 4 * (128 * 64 * (4 + 2 * 2) + 4 * 256 + 4)
     assert size(1, 10, 4, 4, 64) == 4 * (128 * 64 * 4 + 4 * 256 + 4)
+
+
+def test_helpers_take_every_argument_by_name():
+    """The checks are reached (CPU tensors are refused there), whatever the order."""
+    q, k = torch.zeros(3, 4, 128), torch.zeros(3, 2, 128)
+    pos, freq = torch.zeros(3, dtype=torch.int32), torch.zeros(32, dtype=torch.float64)
+    cu, lse = torch.tensor([0, 3], dtype=torch.int32), torch.zeros(4, 3)
+    kc, vc = torch.zeros(5, 2, 16, 16, 8), torch.zeros(5, 2, 128, 16)
+    prep = dict(positions=pos, inv_freq=freq, k=k, q=q)
+    for name, args in [
+            ("qk_norm_rope", prep),
+            ("qk_norm_rope_cache", dict(prep, v=k, slots=pos.long(), k_cache=kc, v_cache=vc)),
+            ("qk_norm_rope_backward", dict(prep, dk_out=k, dq_out=q)),
+            ("forward_packed", dict(cu_seqlens=cu, v=k, k=k, q=q)),
+            ("backward_packed", dict(cu_seqlens=cu, v=k, k=k, q=q, o=q, lse=lse, dout=q)),
+            ("paged_prefill", dict(q=q.bfloat16(), k_cache=kc, v_cache=vc, cu_seqlens=cu,
+                                   block_tables=cu[None], context_lens=cu[1:]))]:
+        with pytest.raises(ValueError):
+            getattr(fa, name)(**args)
+        with pytest.raises(TypeError, match="missing"):
+            getattr(fa, name)(**{a: x for a, x in args.items() if a not in ("q", "dq_out")})
