@@ -577,7 +577,7 @@ def _dense(name, t, dtype, dev, numel=None):
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_context=4096,
-                     beta_slow=1.0, beta_fast=32.0, device=None):
+                     beta_slow=1.0, beta_fast=32.0, device=None, ramp="index"):
     """Rotary frequencies (fp64 [rot_dim/2], radians per position) and the
     factor ``mscale`` that goes with them, for ``qk_norm_rope``.
 
@@ -586,8 +586,13 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_c
     (the base grows so that the lowest frequency is divided by factor and the
     highest stays) or "yarn" (by wavelength: frequencies that turn more than
     ``beta_fast`` times over the original context stay, those that turn less
-    than ``beta_slow`` times are divided by factor, linear in between; mscale
-    = 0.1 ln(factor) + 1).  mscale is 1 for the others."""
+    than ``beta_slow`` times are divided by factor, with a ramp between; mscale
+    = 0.1 ln(factor) + 1).  mscale is 1 for the others.
+
+    ``ramp`` of "yarn": "index", linear in the frequency's index between the
+    indices of beta_fast and beta_slow turns, rounded down and up -- what
+    models trained with YaRN use -- or "turns", linear in the number of turns,
+    as the method's paper writes it."""
     import math
 
     import torch
@@ -595,8 +600,12 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_c
         raise ValueError("rot_dim must be even")
     if scaling not in (None, "linear", "ntk", "yarn") or not factor >= 1.0 or not base > 1.0:
         raise ValueError("scaling is None, 'linear', 'ntk' or 'yarn', factor >= 1 and base > 1")
+    if ramp not in ("index", "turns"):
+        raise ValueError("ramp is 'index' or 'turns'")
     if scaling == "yarn" and not (beta_fast > beta_slow and original_context > 0):
         raise ValueError("beta_fast > beta_slow and original_context > 0")
+    if scaling == "yarn" and ramp == "index" and not beta_slow > 0:
+        raise ValueError("the ramp over the index needs beta_slow > 0")
     mscale = 1.0
     if scaling == "ntk" and rot_dim > 2:
         base = base * factor ** (rot_dim / (rot_dim - 2))
@@ -605,8 +614,16 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_c
     if scaling == "linear":
         freq = freq / factor
     elif scaling == "yarn":
-        turns = original_context * freq / (2 * math.pi)
-        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        if ramp == "turns":
+            turns = original_context * freq / (2 * math.pi)
+            keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        else:
+            def index(turns):   # whose frequency turns so often: base^(-2 i / rot_dim) context = 2 pi turns
+                return rot_dim * math.log(original_context / (2 * math.pi * turns)) / (2 * math.log(base))
+            first = max(math.floor(index(beta_fast)), 0)
+            last = min(math.ceil(index(beta_slow)), rot_dim - 1)
+            # (Bounds that meet, by the clamps, make a step.)
+            keep = 1.0 - ((i - first) / max(last - first, 1e-3)).clamp(0.0, 1.0)
         freq = freq * keep + freq / factor * (1.0 - keep)
         mscale = 0.1 * math.log(factor) + 1.0
     return freq.to(device), mscale

@@ -141,3 +141,36 @@ def test_frequencies_refuse_an_empty_ramp():
     for bad in (dict(beta_slow=32.0), dict(original_context=0)):
         with pytest.raises(ValueError):
             fa.rope_frequencies(64, scaling="yarn", factor=4.0, **bad)
+
+
+@pytest.mark.parametrize("rot,base,context,factor,beta_slow,beta_fast,first,last", [
+    (128, 10000.0, 4096, 4.0, 1.0, 32.0, 20, 46),      # 20.9 and 45.03 before rounding
+    (64, 10000.0, 4096, 16.0, 1.0, 32.0, 10, 23),      # 10.5, 22.5
+    (128, 1e6, 32768, 4.0, 1.0, 32.0, 23, 40),         # 23.6, 39.6
+    (64, 10000.0, 100, 2.0, 1.0, 32.0, 0, 10),         # clamped: no frequency turns 32 times
+    (64, 10000.0, 1 << 30, 2.0, 1.0, 32.0, 53, 63),    # 53.8, 65.9 (clamped at rot_dim - 1)
+])
+def test_yarn_ramps_over_the_index(rot, base, context, factor, beta_slow, beta_fast, first, last):
+    """Frequency i keeps its value up to `first`, is divided from `last` on and goes from
+    one to the other linearly in i between them, as models trained with YaRN have it.
+    (The bounds' comments give rot_dim ln(context / 2 pi beta) / 2 ln base.)"""
+    got, m = fa.rope_frequencies(rot, base, scaling="yarn", factor=factor,
+                                 original_context=context, beta_slow=beta_slow,
+                                 beta_fast=beta_fast)
+    for i, f in enumerate(got.tolist()):
+        plain = base ** (-2.0 * i / rot)
+        divided = min(max((i - first) / (last - first), 0.0), 1.0)
+        assert math.isclose(f, plain * (1.0 - divided + divided / factor), rel_tol=1e-14)
+    assert math.isclose(m, 0.1 * math.log(factor) + 1.0)
+
+
+def test_yarn_by_turns():
+    """The ramp that is linear in a frequency's turns over the original context."""
+    got, _ = fa.rope_frequencies(64, scaling="yarn", factor=4.0, ramp="turns")
+    for i, f in enumerate(got.tolist()):
+        plain = 10000.0 ** (-2.0 * i / 64)
+        keep = min(max((4096 * plain / (2 * math.pi) - 1.0) / 31.0, 0.0), 1.0)
+        assert math.isclose(f, plain * (keep + (1.0 - keep) / 4.0), rel_tol=1e-14)
+    for bad in (dict(ramp="other"), dict(beta_slow=0.0)):
+        with pytest.raises(ValueError):
+            fa.rope_frequencies(64, scaling="yarn", factor=4.0, **bad)
