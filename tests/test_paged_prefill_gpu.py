@@ -244,3 +244,29 @@ def test_a_nan_query_gives_a_nan_row(lens, ctx):
         assert out[row, head].isnan().all()
         out[row, head] = want[row, head]
     assert torch.equal(out, want)
+
+
+def test_bounds_written_just_before():
+    """cu_seqlens and context_lens that the kernel before the call writes, to other
+    values each time: main and merge kernel cut the contexts alike."""
+    q, kc, vc, bt, c, cu = draw([6, 1, 130], [9000, 900, 4100], 8, 2, seed=15, poison=False)
+    bt = torch.randint(0, len(kc), bt.shape, device=DEV).int()
+    bounds = [(c.clone(), cu.clone())]
+    for ctx, ends in (((900, 8000, 150), (0, 6, 7, 137)), ((5000, 40, 4096), (0, 1, 130, 137)),
+                      ((0, 9000, 9000), (0, 0, 3, 90))):
+        bounds.append((torch.tensor(ctx, device=DEV).int(), torch.tensor(ends, device=DEV).int()))
+    want = []
+    for x, y in bounds:
+        torch.cuda.synchronize()
+        want.append(fa.paged_prefill(q, kc, vc, bt, x, y, out=torch.zeros(q.shape, dtype=BF16, device=DEV)))
+        check(q, kc, vc, bt, x, y, want[-1])
+    outs = [torch.zeros_like(want[0]) for _ in range(64)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        c.copy_(bounds[i % 4][0])
+        cu.copy_(bounds[i % 4][1])
+        fa.paged_prefill(q, kc, vc, bt, c, cu, out=out)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0
+    for i, out in enumerate(outs):
+        assert torch.equal(out, want[i % 4])
