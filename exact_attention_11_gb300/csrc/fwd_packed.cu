@@ -891,6 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int row = it.row0 + t * a.tpb + my_tok;
       const int head = it.kvh * a.G + row_in_tile() - my_tok * a.G;
       const int my_out = my_tok < min(it.n_tok[t], a.tpb) ? row * a.H + head : -1;
+      const bool sees = min(it.kv_len, it.pos0 + t * a.tpb + my_tok + 1) > 0;
       free_item(k, true);
       // Epilogue, once the last P V is done.  A tile without key tiles writes
       // zeros if it has none at all, and nothing if other partitions have them.
@@ -920,7 +921,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (my_out >= 0) a.ws_ml[base + my_out] = make_float2(m, l);
         continue;
       }
-      const float inv_l = l == 0.f ? 0.f : 1.f / l;
+      const float inv_l = 1.f / l;
       uint8_t *stg = smem + C::kStage + (t * 4 + quarter) * 4096;
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
@@ -939,8 +940,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           v.y = pack2<F16>(__uint_as_float(c8[2]) * inv_l, __uint_as_float(c8[3]) * inv_l);
           v.z = pack2<F16>(__uint_as_float(c8[4]) * inv_l, __uint_as_float(c8[5]) * inv_l);
           v.w = pack2<F16>(__uint_as_float(c8[6]) * inv_l, __uint_as_float(c8[7]) * inv_l);
-          // A row that saw no key is zero whatever its accumulator holds.
-          if (l == 0.f) v = make_uint4(0u, 0u, 0u, 0u);
+          // A row that sees no key is zero whatever its accumulator holds.  Packed, a
+          // query sees itself at least: a sum of 0 means scores that are all -inf, NaN
+          // (as inv_l makes it; without the select the compiler's registers cost 1%).
+          if (PAGED ? !sees : l == 0.f)
+            v = PAGED ? make_uint4(0u, 0u, 0u, 0u) : make_uint4(~0u, ~0u, ~0u, ~0u);
           if (!PAGED)
             *reinterpret_cast<uint4 *>(stg + lane * 128 + ((q ^ (lane & 7)) * 16)) = v;
           else if (my_out >= 0)
@@ -961,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!PAGED && a.lse != nullptr && my_out >= 0)
         a.lse[static_cast<int64_t>(my_out % a.H) * a.T + my_out / a.H] =
-            l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+            (m + __log2f(l)) * 0.6931471805599453f;
     }
   }
 
@@ -1058,7 +1062,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const Args a) {
         o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
       }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = parts == 0 ? 0.f : 1.f / l;        // a query that sees no key: zeros
     uint2 w;
     w.x = pack_bf16x2(o.x * inv, o.y * inv);
     w.y = pack_bf16x2(o.z * inv, o.w * inv);

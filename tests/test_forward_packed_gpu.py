@@ -317,3 +317,23 @@ def test_after_norm_and_rotation():
     assert ((qr.cpu().double() - want).abs() <= qk_prep_ref.bound(want, size, BF16)).all()
     o, lse = fa.forward_packed(qr, kr, v, cu)
     check(qr, kr, v, cu, o, lse, True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False], ids=["causal", "full"])
+def test_scores_of_minus_infinity(d, causal):
+    """A query of -inf against positive keys: softmax of scores that are all -inf is
+    NaN, as in the dense forward, and not a row of zeros; the other rows keep their bits."""
+    q, k, v, cu = draw([1, 300, 40], 4, 2, d, BF16, seed=15)
+    k.abs_()
+    want, lse0 = fa.forward_packed(q, k, v, cu, causal=causal)
+    rows = ((0, 1), (1, 3), (200, 0), (len(q) - 1, 2))
+    for row, head in rows:
+        q[row, head, 7] = float("-inf")
+    o, lse = fa.forward_packed(q, k, v, cu, causal=causal)
+    for row, head in rows:
+        assert o[row, head].isnan().all() and not lse[head, row].isfinite()
+        o[row, head], lse[head, row] = want[row, head], lse0[head, row]
+    assert torch.equal(o, want) and torch.equal(lse, lse0)
+    x = torch.ones(1, 1, 5, d, dtype=BF16, device=DEV)
+    assert fa.forward(x * float("-inf"), x, x, causal=causal)[0].isnan().all()

@@ -270,3 +270,25 @@ def test_bounds_written_just_before():
     assert fa.fa_device_status() == 0
     for i, out in enumerate(outs):
         assert torch.equal(out, want[i % 4])
+
+
+@pytest.mark.parametrize("lens,ctx", [([3, 9], [40, 300]), ([1], [9000]), ([3, 7, 140], [9000, 5, 700]),
+                                      ([2], [40000])], ids=str)
+def test_scores_of_minus_infinity(lens, ctx):
+    """Over whole and cut contexts NaN, as in the packed forward; zeros only for a
+    query that sees no key (the second sequence's first two of [3, 7, 140])."""
+    q, kc, vc, bt, c, cu = draw(lens, ctx, 8, 2, seed=16, poison=False)
+    kc.abs_()
+    want = fa.paged_prefill(q, kc, vc, bt, c, cu)
+    rows = [(0, 3), (len(q) - 1, 6)]
+    if lens == [3, 7, 140]:
+        assert (want[3:5] == 0).all() and (want[5] != 0).any()
+        q[3, 1, 9] = float("-inf")
+        rows.append((6, 1))
+    for row, head in rows:
+        q[row, head, 9] = float("-inf")
+    out = fa.paged_prefill(q, kc, vc, bt, c, cu)
+    for row, head in rows:
+        assert out[row, head].isnan().all()
+        out[row, head] = want[row, head]
+    assert torch.equal(out, want)
