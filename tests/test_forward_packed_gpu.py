@@ -337,3 +337,17 @@ def test_scores_of_minus_infinity(d, causal):
     assert torch.equal(o, want) and torch.equal(lse, lse0)
     x = torch.ones(1, 1, 5, d, dtype=BF16, device=DEV)
     assert fa.forward(x * float("-inf"), x, x, causal=causal)[0].isnan().all()
+
+
+@pytest.mark.parametrize("H,Hk,dtype", [(8, 1, F16), (2, 2, BF16)], ids=["8on1-fp16", "2-bf16"])
+def test_a_prompt_of_16384(H, Hk, dtype):
+    """The whole of it, by slices of query rows."""
+    n, d = 16384, 128
+    q, k, v, cu = draw([n], H, Hk, d, dtype, seed=16)
+    o, lse = fa.forward_packed(q, k, v, cu)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status() == 0
+    for a in range(0, n, 512):
+        r = slice(a, a + 512)
+        x = ref.sequence(q[r], k[:a + 512], v[:a + 512], d ** -0.5, torch.arange(a, a + 512, device=DEV))
+        ref.check_forward(o[r], lse[:, r], x, d ** -0.5, dtype)

@@ -292,3 +292,35 @@ def test_scores_of_minus_infinity(lens, ctx):
         assert out[row, head].isnan().all()
         out[row, head] = want[row, head]
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("lens,ctx", [([1], [40000]), ([2, 1], [40000, 20001]), ([2], [33000])], ids=str)
+@pytest.mark.parametrize("H,Hk", [(8, 1), (8, 2), (3, 3)])
+def test_more_partitions_than_lanes(lens, ctx, H, Hk):
+    """More than 32 partitions: the merge's later rounds.  Each head has one key that
+    its scores favour, the even heads' among the first 32 partitions, the odd heads'
+    behind them, so that what is carried over is scaled down as well as kept."""
+    mb = max((c + 15) // 16 for c in ctx) + 1
+    rows = fa.fa_paged_prefill_workspace_bytes(len(lens), sum(lens), H, Hk, mb) // (130 * 4)
+    assert rows // (sum(lens) * H) > 32
+    q, kc, vc, bt, c, cu = draw(lens, ctx, H, Hk, seed=17)
+    for s, (n, at) in enumerate(zip(ctx, cu.tolist())):
+        for h in range(H):
+            tok = 100 + 130 * h if h % 2 == 0 else n - 150 - 130 * h
+            # |q|^2 / sqrt(d) is about 11: e^11 of some 40000 keys' e^0.5
+            kc[bt[s, tok // 16].item(), h * Hk // H, :, tok % 16] = q[at, h].view(16, 8)
+    out = fa.paged_prefill(q, kc, vc, bt, c, cu)
+    check(q, kc, vc, bt, c, cu, out)
+
+
+@pytest.mark.parametrize("S", [112, 113])
+@pytest.mark.parametrize("long_at", [0, 60])
+def test_long_context_among_many_sequences(S, long_at):
+    """Contexts are cut up to 112 sequences and whole beyond."""
+    ctx = [1 + 37 * i % 500 for i in range(S)]
+    ctx[long_at] = 20000
+    lens = [1 + i % 2 if c > 1 else 1 for i, c in enumerate(ctx)]
+    T, mb = sum(lens), 20000 // 16 + 1
+    assert (fa.fa_paged_prefill_workspace_bytes(S, T, 4, 2, mb) > 0) == (S <= 112)
+    run(lens, ctx, 4, 2, seed=S)
+    run(lens, ctx, 3, 1, seed=S + 1)
