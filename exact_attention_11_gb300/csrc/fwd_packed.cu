@@ -54,7 +54,7 @@
 // to 4096 tokens, 32 / 8 heads, d = 128, causal, 182 us (1497 TFLOP/s); one of 16384,
 // 8 / 1 heads, fp16, 330 us (1665); 32 prompts up to 200, 16 heads, d = 64, 17 us;
 // chunks of 4 x 1024 tokens over 8192, 345 us (1494 TFLOP/s), up to 1024 over up to
-// 16384, 93 us; 64 single tokens over 4096, 180 us (6.0 TB/s).
+// 16384, 94 us; 64 single tokens over 4096, 180 us (6.0 TB/s).
 // Rounding: P to the element type before P V, O once at the end; scores, maxima, sums,
 // partial rows and their merge are fp32.
 #include <cuda.h>
@@ -216,13 +216,14 @@ __device__ __forceinline__ Work work_of(const Args &a, const Seq &q) {
 // workspace, 1 KB each at an SM's share of the HBM rate) adds W c / p, and the SMs
 // end up to p apart, 0.7 p on average: p = sqrt(W c / 0.7) balances the two, at
 // least four key tiles; what is shorter than 1.5 p stays whole.  (Constants fitted
-// to a model of the schedule over nine mixes of chunks and contexts, then measured:
-// kFixed 2, 2.5, 3 took 37.8, 36.3, 35.7 us for 16 drafts of up to 6 tokens over up to
-// 4096, but 186, 188, 197 us for 64 single tokens over 4096; with kFixed 1, kRow 0.01 or
-// 1 in place of 0.7 chunks of up to 1024 over up to 16384 took 131 - 135 us, not 102.)  `work`: key tiles of the call's
-// blocks, of one key/value head.  Each block of the sequence cuts its own key tiles
-// into that many.  (Roundings are spelled out: the merge kernel has to reach the
-// same number.)
+// to a model of the schedule over nine mixes of chunks and contexts, then measured on
+// an earlier form of the kernel, so only the ratios count: against kFixed 2.5, 2 and 3
+// took 1.04 and 0.98 of the time for 16 drafts of up to 6 tokens over up to 4096, but
+// 0.99 and 1.05 for 64 single tokens over 4096; kFixed 1, kRow 0.01 or 1 in place of 0.7
+// took 1.3 for chunks of up to 1024 over up to 16384.)  `work`: key tiles of the call's
+// blocks, of one key/value head.  Each block of the sequence cuts its own key tiles into
+// that many.  (Roundings are spelled out: the merge kernel has to reach the same
+// number.)
 __device__ __forceinline__ int parts_of(const Args &a, const Seq &q, int tiles, int64_t work) {
   constexpr float kFixed = 2.5f, kRow = 0.02f, kLeast = 4.f;
   if (a.n_split == 1) return 1;
@@ -319,7 +320,7 @@ __device__ __forceinline__ bool decode_item(const Args &a, const Misc *m, int n_
       it.part = blk - x * parts;
       blk = x;
     }
-  } else {   // contexts are not cut here: there are items enough
+  } else {   // contexts are not cut here, and items come in the sequences' order
     const int vb = u / a.Hk;
     it.kvh = u - vb * a.Hk;
     s = warp_search(a.S, vb, [&](int i) { return seq_begin(a, i) / tb + i; });
@@ -1147,7 +1148,9 @@ cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, cons
 // The most partitions of a context, from what the host knows (the longest one's
 // bound): as parts_of reckons for a sequence of one token that is alone, and no more
 // than a workspace of 256 MB holds -- with that many rows the blocks fill the GPU.
-// Beyond kCachedSeqs sequences nothing is cut.
+// Beyond kCachedSeqs sequences, whose bounds and numbering do not fit the barrier area,
+// nothing is cut: a long context among short ones is then one chain of its key tiles
+// (131072 tokens among 1024s, 32 / 8 heads: 169 us with 112 sequences, 1350 with 113).
 int paged_max_parts(int T, int S, int H, int Hk, int max_blocks) {
   if (S > kCachedSeqs) return 1;
   const double tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;

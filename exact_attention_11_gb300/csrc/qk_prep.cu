@@ -39,7 +39,10 @@
 // (launch and two dependent loads), 4099 tokens 24.4 us (4.1 TB/s; V's transposition 3
 // us of it); dense fp16, 16384 tokens, 16 + 16 heads, d = 64: 26.6 us (5.1 TB/s; a copy
 // by the same loads and stores runs 13% faster); backward, 8192 tokens, 32 + 8 heads:
-// 54.5 us (4.6 TB/s).  What is left are issue slots: 50 - 60% busy.
+// 54.5 us (4.6 TB/s).  Neither DRAM (28% and 52% busy into the cache and backward) nor
+// the issue slots (55% and 50%) are full: what is left is latency, into the cache a
+// block's angle table, barrier and first rows in series, backward the rows that 24 warps
+// an SM keep in flight.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -513,9 +513,10 @@ int fa_qk_norm_rope_backward_fp32(const void *dq_out, const void *dk_out, const 
  *                 outside the tensors is read or written.)
  *   num_heads     a multiple of num_kv_heads, at most 128 times it.
  *   d             64 or 128 (else FA_ERR_UNSUPPORTED).
- * One sequence's NaN or Inf does not reach another's rows.  Rounding, scale,
- * alignment and errors as for fa_forward; num_seqs or total_tokens equal to 0
- * does nothing.
+ * One sequence's NaN or Inf does not reach another's rows; a NaN or Inf in v may
+ * reach rows of its own sequence that do not see it (a weight of 0 does not cancel
+ * it), as in fa_forward.  Rounding, scale, alignment and errors as for fa_forward;
+ * num_seqs or total_tokens equal to 0 does nothing.
  * fa_forward_packed_f16: the same with fp16 q, k, v and o (as fa_forward_f16).
  */
 int fa_forward_packed(const void *q, const void *k, const void *v, void *o, float *lse,
@@ -542,10 +543,11 @@ int fa_forward_packed_f16(const void *q, const void *k, const void *v, void *o, 
  *   workspace     device memory of at least fa_backward_packed_workspace_bytes
  *                 bytes, 16-byte aligned, scratch during the call; calls whose
  *                 work overlaps on the GPU need separate ones.
- * One sequence's NaN or Inf does not reach another's gradients.  Rounding and
- * errors as for fa_backward: products accumulate in fp32, P and dS are rounded to
- * bf16 before their products; dQ, and with grouped heads dK and dV, are summed in
- * fp32 with atomic adds, so their last bits may vary from run to run.
+ * One sequence's NaN or Inf does not reach another's gradients (its own as for
+ * fa_forward_packed).  Rounding and errors as for fa_backward: products accumulate
+ * in fp32, P and dS are rounded to bf16 before their products; dQ, and with grouped
+ * heads dK and dV, are summed in fp32 with atomic adds, so their last bits may vary
+ * from run to run.
  */
 unsigned long long fa_backward_packed_workspace_bytes(int num_seqs, int total_tokens,
                                                       int num_heads, int num_kv_heads, int d);
@@ -581,10 +583,19 @@ int fa_backward_packed(const void *q, const void *k, const void *v, const void *
  *                 bytes (0: may be NULL), 16-byte aligned, scratch during the
  *                 call; calls that may run at the same time need separate ones.
  *                 It holds the partial rows of long contexts that are cut into
- *                 partitions when the chunks alone do not fill the GPU.
+ *                 partitions when the chunks alone do not fill the GPU.  Contexts
+ *                 are cut in calls of up to 112 sequences, into no more partitions
+ *                 than 256 MB of partial rows of the whole call hold; where they
+ *                 are not, one block walks a context, 1.2 us per 128 tokens.  So a
+ *                 context that is much longer than the others belongs in a call of
+ *                 at most 112 sequences (one of 131072 tokens among single tokens
+ *                 over 1024, 32 / 8 heads: 169 us with 112, 1350 us with 113) and
+ *                 apart from whole prompts (beside one of 8192 tokens 1290 us; in two
+ *                 calls 324 and 108).
  *   num_heads     a multiple of num_kv_heads, at most 128 times it.
- * Cache slots past a context may hold any bits.  Results are the same from call
- * to call, bit for bit.  num_seqs or total_tokens equal to 0 does nothing.
+ * Cache slots past a context may hold any bits; NaN and Inf inside one as for
+ * fa_forward_packed.  Results are the same from call to call, bit for bit.
+ * num_seqs or total_tokens equal to 0 does nothing.
  */
 unsigned long long fa_paged_prefill_workspace_bytes(int num_seqs, int total_tokens, int num_heads,
                                                     int num_kv_heads, int max_num_blocks_per_seq);
@@ -624,7 +635,8 @@ int fa_device_status(void);
 
 /* Frees the library-owned per-device state on the current device, after
  * synchronising the device.  No libfattn call may be enqueued or captured
- * concurrently with it. */
+ * concurrently with it, and a graph captured before it must not be replayed
+ * after it (its kernels' work counters are freed with the rest). */
 void fa_release(void);
 
 /* Library version as major*10000 + minor*100 + patch. */
