@@ -618,8 +618,9 @@ def rope_frequencies(rot_dim, base=10000.0, scaling=None, factor=1.0, original_c
             turns = original_context * freq / (2 * math.pi)
             keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
         else:
-            def index(turns):   # whose frequency turns so often: base^(-2 i / rot_dim) context = 2 pi turns
-                return rot_dim * math.log(original_context / (2 * math.pi * turns)) / (2 * math.log(base))
+            def index(turns):   # i of base^(-2 i / rot_dim) original_context = 2 pi turns
+                far = original_context / (2 * math.pi * turns)
+                return rot_dim * math.log(far) / (2 * math.log(base))
             first = max(math.floor(index(beta_fast)), 0)
             last = min(math.ceil(index(beta_slow)), rot_dim - 1)
             # (Bounds that meet, by the clamps, make a step.)
