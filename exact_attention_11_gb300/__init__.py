@@ -32,7 +32,9 @@ __all__ = ["fa_forward", "fa_forward_f16", "fa_forward_masked", "forward_masked"
            "qk_norm_rope_cache", "qk_norm_rope_backward", "fa_forward_packed",
            "fa_forward_packed_f16", "forward_packed", "fa_backward_packed",
            "fa_backward_packed_workspace_bytes", "backward_packed", "fa_paged_prefill",
-           "fa_paged_prefill_workspace_bytes", "paged_prefill",
+           "fa_paged_prefill_workspace_bytes", "paged_prefill", "fa_forward_packed_window",
+           "fa_forward_packed_window_f16", "forward_packed_window", "fa_paged_prefill_window",
+           "fa_paged_prefill_window_workspace_bytes", "paged_prefill_window",
            "fa_device_status", "fa_release", "forward", "paged_decode", "FattnError",
            "library_path", "load"]
 
@@ -93,6 +95,11 @@ EXPORTS = {
                                                                _vp], _i),
     "fa_paged_prefill_workspace_bytes": ([_i] * 5, ctypes.c_ulonglong),
     "fa_paged_prefill": ([_vp] * 7 + [_i] * 8 + [_ll, _f, _vp, ctypes.c_ulonglong, _vp], _i),
+    "fa_forward_packed_window": ([_vp] * 6 + [_i] * 5 + [_ll] * 3 + [_f, _i, _i, _vp], _i),
+    "fa_forward_packed_window_f16": ([_vp] * 6 + [_i] * 5 + [_ll] * 3 + [_f, _i, _i, _vp], _i),
+    "fa_paged_prefill_window_workspace_bytes": ([_i] * 7, ctypes.c_ulonglong),
+    "fa_paged_prefill_window": ([_vp] * 7 + [_i] * 8 + [_ll, _f, _i, _i, _vp, ctypes.c_ulonglong,
+                                                        _vp], _i),
     "fa_status_string": ([_i], ctypes.c_char_p),
     "fa_device_status": ([], _i),
     "fa_release": ([], None),
@@ -299,6 +306,38 @@ def fa_paged_prefill(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens
         q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out, num_seqs, total_tokens,
         num_heads, num_kv_heads, head_size, block_size, num_blocks, max_num_blocks_per_seq,
         q_stride, scale, workspace, workspace_bytes, stream))
+
+
+def fa_forward_packed_window(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads,
+                             num_kv_heads, d, q_stride, k_stride, v_stride, scale, window, sinks,
+                             stream) -> int:
+    return _check("fa_forward_packed_window", load().fa_forward_packed_window(
+        q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads, num_kv_heads, d, q_stride,
+        k_stride, v_stride, scale, window, sinks, stream))
+
+
+def fa_forward_packed_window_f16(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads,
+                                 num_kv_heads, d, q_stride, k_stride, v_stride, scale, window,
+                                 sinks, stream) -> int:
+    return _check("fa_forward_packed_window_f16", load().fa_forward_packed_window_f16(
+        q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads, num_kv_heads, d, q_stride,
+        k_stride, v_stride, scale, window, sinks, stream))
+
+
+def fa_paged_prefill_window_workspace_bytes(num_seqs, total_tokens, num_heads, num_kv_heads,
+                                            max_num_blocks_per_seq, window, sinks) -> int:
+    return int(load().fa_paged_prefill_window_workspace_bytes(
+        num_seqs, total_tokens, num_heads, num_kv_heads, max_num_blocks_per_seq, window, sinks))
+
+
+def fa_paged_prefill_window(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out,
+                            num_seqs, total_tokens, num_heads, num_kv_heads, head_size,
+                            block_size, num_blocks, max_num_blocks_per_seq, q_stride, scale,
+                            window, sinks, workspace, workspace_bytes, stream) -> int:
+    return _check("fa_paged_prefill_window", load().fa_paged_prefill_window(
+        q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out, num_seqs, total_tokens,
+        num_heads, num_kv_heads, head_size, block_size, num_blocks, max_num_blocks_per_seq,
+        q_stride, scale, window, sinks, workspace, workspace_bytes, stream))
 
 
 def fa_status_string(status: int) -> str:
@@ -791,6 +830,29 @@ def forward_packed(q, k, v, cu_seqlens, scale=None, causal=True, out=None, lse=N
     Returns (O [T,H,d], LSE fp32 [H,T] or None).  Rows of no sequence are not
     written (they are uninitialised in tensors made here).  Runs on the current
     torch stream."""
+    return _forward_packed("fa_forward_packed", q, k, v, cu_seqlens, scale, out, lse, want_lse,
+                           int(causal))
+
+
+@_on_device
+def forward_packed_window(q, k, v, cu_seqlens, window, sinks=0, scale=None, out=None, lse=None,
+                          want_lse=True):
+    """``forward_packed`` with a sliding window: a query at position p of its
+    sequence sees keys j <= p with j > p - window, or j < sinks (the sequence's
+    first tokens, which stay visible).  window >= 1, sinks >= 0."""
+    return _forward_packed("fa_forward_packed_window", q, k, v, cu_seqlens, scale, out, lse,
+                           want_lse, *_window_args(window, sinks))
+
+
+def _window_args(window, sinks):
+    """Checks a window and a number of first tokens; lengths past 2^30, which no
+    sequence has, as 2^30."""
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be at least 1 and sinks at least 0")
+    return min(int(window), 1 << 30), min(int(sinks), 1 << 30)
+
+
+def _forward_packed(name, q, k, v, cu_seqlens, scale, out, lse, want_lse, *mask):
     torch = _torch()
     T, H, Hk, d, S, dtype, dev, qs, ks, vs, cu = _packed_args(
         q, k, v, cu_seqlens, (torch.bfloat16, torch.float16))
@@ -805,12 +867,11 @@ def forward_packed(q, k, v, cu_seqlens, scale=None, causal=True, out=None, lse=N
     if T == 0 or S == 0:
         return out, lse
     lib = _lib or load()
-    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o_ptr, lse_ptr, cu, S, T, H, Hk, d, qs, ks,
-            vs, scale, int(causal), _raw_stream(dev))
     if dtype == torch.float16:
-        _check("fa_forward_packed_f16", lib.fa_forward_packed_f16(*args))
-    else:
-        _check("fa_forward_packed", lib.fa_forward_packed(*args))
+        name += "_f16"
+    _check(name, getattr(lib, name)(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o_ptr, lse_ptr, cu, S, T, H, Hk, d, qs, ks, vs,
+        scale, *mask, _raw_stream(dev)))
     return out, lse
 
 
@@ -860,6 +921,26 @@ def paged_prefill(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, s
     tensor of at least ``fa_paged_prefill_workspace_bytes`` bytes.  Returns out
     [T,H,128]; rows of no sequence are not written.  Runs on the current torch
     stream."""
+    return _paged_prefill("fa_paged_prefill", q, k_cache, v_cache, block_tables, context_lens,
+                          cu_seqlens, scale, out, workspace)
+
+
+@_on_device
+def paged_prefill_window(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, window,
+                         sinks=0, scale=None, out=None, workspace=None):
+    """``paged_prefill`` with a sliding window: a query at position p (the last of
+    a sequence at context_lens[s] - 1) sees tokens j <= p with j > p - window, or
+    j < sinks.  window >= 1, sinks >= 0.  Table entries of blocks that no query of
+    the chunk sees are not used and may hold anything.  ``workspace`` (optional)
+    is a CUDA tensor of at least ``fa_paged_prefill_window_workspace_bytes``
+    bytes."""
+    return _paged_prefill("fa_paged_prefill_window", q, k_cache, v_cache, block_tables,
+                          context_lens, cu_seqlens, scale, out, workspace,
+                          *_window_args(window, sinks))
+
+
+def _paged_prefill(name, q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, scale, out,
+                   workspace, *mask):
     torch = _torch()
     T, H, D = q.shape
     dtype, dev = q.dtype, q.get_device()
@@ -887,10 +968,10 @@ def paged_prefill(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, s
     if workspace is not None:
         nbytes = _workspace(workspace, dev)
     else:
-        nbytes = lib.fa_paged_prefill_workspace_bytes(S, T, H, Hk, mb)
+        nbytes = getattr(lib, name + "_workspace_bytes")(S, T, H, Hk, mb, *mask)
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    _check("fa_paged_prefill", lib.fa_paged_prefill(
-        *ptrs, out_ptr, S, T, H, Hk, D, bs, nb, mb, qs, scale, _ptr(workspace), nbytes,
+    _check(name, getattr(lib, name)(
+        *ptrs, out_ptr, S, T, H, Hk, D, bs, nb, mb, qs, scale, *mask, _ptr(workspace), nbytes,
         _raw_stream(dev)))
     return out

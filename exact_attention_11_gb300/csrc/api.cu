@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <atomic>
@@ -849,9 +850,22 @@ int acquire_sched(cudaStream_t s, int mode, int **sched, int **status, int *faul
   return FA_OK;
 }
 
+// What a query sees: all keys up to its own (`causal`; else all), or of those the last
+// `window` and the first `sinks` (window > 0).
+struct Visible {
+  int causal, window, sinks;
+};
+constexpr Visible all_keys(int causal) { return {causal ? 1 : 0, 0, 0}; }
+// A window and first tokens; lengths past 2^30 see what 2^30 sees (sequences are shorter).
+int window_keys(int window, int sinks, Visible *out) {
+  if (window <= 0 || sinks < 0) return FA_ERR_INVALID_ARG;
+  *out = {1, std::min(window, 1 << 30), std::min(sinks, 1 << 30)};
+  return FA_OK;
+}
+
 int forward_packed(const void *q, const void *k, const void *v, void *o, float *lse,
                    const int *cu_seqlens, int S, int T, int H, int Hk, int d, long long q_stride,
-                   long long k_stride, long long v_stride, float scale, int causal,
+                   long long k_stride, long long v_stride, float scale, const Visible &see,
                    fa_stream_t stream, bool f16) {
   int rc = check_packed(q, k, v, o, lse, cu_seqlens, S, T, H, Hk, d, q_stride, k_stride, v_stride,
                         scale);
@@ -871,7 +885,8 @@ int forward_packed(const void *q, const void *k, const void *v, void *o, float *
   if ((rc = encode_rows_map(&tv, v, T, Hk, d, v_stride, true, 128, 1, dt)) != FA_OK) return rc;
   fattn::PackedProblem p{};
   p.o = o, p.lse = lse, p.cu_seqlens = cu_seqlens;
-  p.S = S, p.T = T, p.H = H, p.Hk = Hk, p.causal = causal ? 1 : 0, p.scale = scale;
+  p.S = S, p.T = T, p.H = H, p.Hk = Hk, p.scale = scale;
+  p.causal = see.causal, p.window = see.window, p.sinks = see.sinks;
   return cuda_status(
       fattn::launch_fwd_packed(tq, tk, tv, p, d, f16, sched, status, fault_cta, s));
 }
@@ -882,8 +897,8 @@ int fa_forward_packed(const void *q, const void *k, const void *v, void *o, floa
                       int num_kv_heads, int d, long long q_stride, long long k_stride,
                       long long v_stride, float scale, int causal, fa_stream_t stream) {
   return forward_packed(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads,
-                        num_kv_heads, d, q_stride, k_stride, v_stride, scale, causal, stream,
-                        false);
+                        num_kv_heads, d, q_stride, k_stride, v_stride, scale, all_keys(causal),
+                        stream, false);
 }
 
 int fa_forward_packed_f16(const void *q, const void *k, const void *v, void *o, float *lse,
@@ -891,8 +906,32 @@ int fa_forward_packed_f16(const void *q, const void *k, const void *v, void *o, 
                           int num_kv_heads, int d, long long q_stride, long long k_stride,
                           long long v_stride, float scale, int causal, fa_stream_t stream) {
   return forward_packed(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads,
-                        num_kv_heads, d, q_stride, k_stride, v_stride, scale, causal, stream,
-                        true);
+                        num_kv_heads, d, q_stride, k_stride, v_stride, scale, all_keys(causal),
+                        stream, true);
+}
+
+int fa_forward_packed_window(const void *q, const void *k, const void *v, void *o, float *lse,
+                             const int *cu_seqlens, int num_seqs, int total_tokens,
+                             int num_heads, int num_kv_heads, int d, long long q_stride,
+                             long long k_stride, long long v_stride, float scale, int window,
+                             int sinks, fa_stream_t stream) {
+  Visible see;
+  const int rc = window_keys(window, sinks, &see);
+  if (rc != FA_OK) return rc;
+  return forward_packed(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads,
+                        num_kv_heads, d, q_stride, k_stride, v_stride, scale, see, stream, false);
+}
+
+int fa_forward_packed_window_f16(const void *q, const void *k, const void *v, void *o, float *lse,
+                                 const int *cu_seqlens, int num_seqs, int total_tokens,
+                                 int num_heads, int num_kv_heads, int d, long long q_stride,
+                                 long long k_stride, long long v_stride, float scale, int window,
+                                 int sinks, fa_stream_t stream) {
+  Visible see;
+  const int rc = window_keys(window, sinks, &see);
+  if (rc != FA_OK) return rc;
+  return forward_packed(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads,
+                        num_kv_heads, d, q_stride, k_stride, v_stride, scale, see, stream, true);
 }
 
 unsigned long long fa_backward_packed_workspace_bytes(int num_seqs, int total_tokens,
@@ -957,12 +996,13 @@ unsigned long long fa_paged_prefill_workspace_bytes(int num_seqs, int total_toke
       total_tokens, num_seqs, num_heads, num_kv_heads, max_num_blocks_per_seq));
 }
 
-int fa_paged_prefill(const void *q, const void *k_cache, const void *v_cache,
-                     const int *block_tables, const int *context_lens, const int *cu_seqlens,
-                     void *out, int num_seqs, int total_tokens, int num_heads, int num_kv_heads,
-                     int head_size, int block_size, int num_blocks, int max_num_blocks_per_seq,
-                     long long q_stride, float scale, void *workspace,
-                     unsigned long long workspace_bytes, fa_stream_t stream) {
+namespace {
+int paged_prefill(const void *q, const void *k_cache, const void *v_cache,
+                  const int *block_tables, const int *context_lens, const int *cu_seqlens,
+                  void *out, int num_seqs, int total_tokens, int num_heads, int num_kv_heads,
+                  int head_size, int block_size, int num_blocks, int max_num_blocks_per_seq,
+                  long long q_stride, float scale, const Visible &see, void *workspace,
+                  unsigned long long workspace_bytes, fa_stream_t stream) {
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_seqlens || !out)
     return FA_ERR_INVALID_ARG;
   if (num_blocks <= 0 || max_num_blocks_per_seq <= 0) return FA_ERR_INVALID_ARG;
@@ -978,7 +1018,8 @@ int fa_paged_prefill(const void *q, const void *k_cache, const void *v_cache,
   if ((rc = check_token_stride(q_stride, num_heads, head_size, 2)) != FA_OK) return rc;
   if (num_seqs == 0 || total_tokens == 0) return FA_OK;
   const size_t need = fattn::paged_prefill_workspace_bytes(total_tokens, num_seqs, num_heads,
-                                                           num_kv_heads, max_num_blocks_per_seq);
+                                                           num_kv_heads, max_num_blocks_per_seq,
+                                                           see.window, see.sinks);
   if (need > 0) {
     if (!workspace || workspace_bytes < need) return FA_ERR_INVALID_ARG;
     if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
@@ -999,9 +1040,52 @@ int fa_paged_prefill(const void *q, const void *k_cache, const void *v_cache,
   p.o = out, p.cu_seqlens = cu_seqlens, p.context_lens = context_lens;
   p.block_tables = block_tables;
   p.S = num_seqs, p.T = total_tokens, p.H = num_heads, p.Hk = num_kv_heads;
-  p.max_blocks = max_num_blocks_per_seq, p.num_blocks = num_blocks, p.causal = 1, p.scale = scale;
+  p.max_blocks = max_num_blocks_per_seq, p.num_blocks = num_blocks, p.scale = scale;
+  p.causal = see.causal, p.window = see.window, p.sinks = see.sinks;
   return cuda_status(fattn::launch_paged_prefill(tq, tk, tv, p, static_cast<float *>(workspace),
                                                  sched, status, fault_cta, s));
+}
+}  // namespace
+
+int fa_paged_prefill(const void *q, const void *k_cache, const void *v_cache,
+                     const int *block_tables, const int *context_lens, const int *cu_seqlens,
+                     void *out, int num_seqs, int total_tokens, int num_heads, int num_kv_heads,
+                     int head_size, int block_size, int num_blocks, int max_num_blocks_per_seq,
+                     long long q_stride, float scale, void *workspace,
+                     unsigned long long workspace_bytes, fa_stream_t stream) {
+  return paged_prefill(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out, num_seqs,
+                       total_tokens, num_heads, num_kv_heads, head_size, block_size, num_blocks,
+                       max_num_blocks_per_seq, q_stride, scale, all_keys(1), workspace,
+                       workspace_bytes, stream);
+}
+
+unsigned long long fa_paged_prefill_window_workspace_bytes(int num_seqs, int total_tokens,
+                                                           int num_heads, int num_kv_heads,
+                                                           int max_num_blocks_per_seq, int window,
+                                                           int sinks) {
+  Visible see;
+  if (num_seqs <= 0 || total_tokens <= 0 || max_num_blocks_per_seq <= 0) return 0;
+  if (check_packed_sizes(num_seqs, total_tokens, num_heads, num_kv_heads) != FA_OK) return 0;
+  if (window_keys(window, sinks, &see) != FA_OK) return 0;
+  return static_cast<unsigned long long>(fattn::paged_prefill_workspace_bytes(
+      total_tokens, num_seqs, num_heads, num_kv_heads, max_num_blocks_per_seq, see.window,
+      see.sinks));
+}
+
+int fa_paged_prefill_window(const void *q, const void *k_cache, const void *v_cache,
+                            const int *block_tables, const int *context_lens,
+                            const int *cu_seqlens, void *out, int num_seqs, int total_tokens,
+                            int num_heads, int num_kv_heads, int head_size, int block_size,
+                            int num_blocks, int max_num_blocks_per_seq, long long q_stride,
+                            float scale, int window, int sinks, void *workspace,
+                            unsigned long long workspace_bytes, fa_stream_t stream) {
+  Visible see;
+  const int rc = window_keys(window, sinks, &see);
+  if (rc != FA_OK) return rc;
+  return paged_prefill(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out, num_seqs,
+                       total_tokens, num_heads, num_kv_heads, head_size, block_size, num_blocks,
+                       max_num_blocks_per_seq, q_stride, scale, see, workspace, workspace_bytes,
+                       stream);
 }
 
 int fa_device_status(void) {

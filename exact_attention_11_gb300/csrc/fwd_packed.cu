@@ -63,6 +63,7 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "kernels.h"
 #include "packed.cuh"
@@ -137,11 +138,20 @@ struct Item {
   int clear[2];      // the step in which tile A's (B's) softmax clears V's last rows, or < 0
 };
 
+// kWindow: a block visits a list of key tiles: those of the sequence's first tokens,
+// then those from the first key that its first token sees on.  Entry x of the list is
+// tile x, or x + skip from entry `at` on; a tile of both comes once.
+struct Gap {
+  int at, skip;
+  __device__ int tile(int x) const { return x >= at ? x + skip : x; }
+};
+
 constexpr int kCachedSeqs = 112;
 struct Misc {
   uint32_t tmem_base;
   int abort;
   Item item[2];
+  Gap gap[2];                   // kWindow: of the items
   int2 seq[kCachedSeqs + 1];    // (first row, context length)
   // By weight of their items, lightest first: the sequences, their partitions, and
   // the items of those before ([S]: of all).
@@ -156,6 +166,10 @@ static_assert(8 * kNumBars + sizeof(Misc) <= kBarArea, "barrier area");
 // boundary (the kernel then does nothing).
 constexpr int kDevBadSmemBase = -2;
 
+// What a query sees: all keys of its sequence up to its own (or, packed, all of
+// them); or of those a window and the sequence's first tokens.
+enum : int { kAll = 0, kWindow = 1 };
+
 struct Args {
   uint16_t *o;
   float *lse;                   // [H][T] or null
@@ -169,10 +183,22 @@ struct Args {
   int n_vblocks, n_split, causal;   // n_split: most partitions of a context
   float scale_log2;
 };
+// What a form's kernels need besides.  (Not in Args: the kernels of all keys spill two
+// registers more when the parameters grow past 512 bytes.)
+struct WindowArgs : Args {
+  int window, sinks;            // up to 2^30 each
+};
+template <int FORM>
+using FormArgs = std::conditional_t<FORM == kWindow, WindowArgs, Args>;
 
 // Key tiles that `n` tokens, the last of which sees key `last` last, visit.
 __device__ __forceinline__ int tiles_for(int n, int last, int kv_len) {
   return n > 0 ? (max(0, min(kv_len, last + 1)) + BN - 1) / BN : 0;
+}
+
+// The lowest n bits, none for n <= 0 and all for n >= 32.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
 }
 
 // A query that sees every key of its sequence.
@@ -203,12 +229,27 @@ __device__ __forceinline__ Seq global_seq(const Args &a, int s) {
   return make_seq(a, PAGED, seq_begin(a, s), seq_begin(a, s + 1), PAGED ? a.context_lens[s] : 0);
 }
 
+// The gap in the list of a block whose first token is at position pos.
+template <int FORM>
+__device__ __forceinline__ Gap gap_of(const FormArgs<FORM> &a, int pos) {
+  if constexpr (FORM == kWindow) {
+    const int first = max(pos - a.window + 1, 0) / BN;
+    const int at = min((a.sinks + BN - 1) / BN, first);
+    return {at, first - at};
+  }
+  return {0, 0};
+}
+
 // Work of a sequence: key tiles of its last block, and blocks.
 struct Work {
   int tiles, blocks;
 };
-__device__ __forceinline__ Work work_of(const Args &a, const Seq &q) {
-  return {tiles_for(q.n, q.pos + q.n - 1, q.kv_len), (q.n + 2 * a.tpb - 1) / (2 * a.tpb)};
+template <int FORM>
+__device__ __forceinline__ Work work_of(const FormArgs<FORM> &a, const Seq &q) {
+  Work w = {tiles_for(q.n, q.pos + q.n - 1, q.kv_len), (q.n + 2 * a.tpb - 1) / (2 * a.tpb)};
+  if (FORM == kWindow)
+    w.tiles = max(w.tiles - gap_of<FORM>(a, q.pos + max(w.blocks - 1, 0) * 2 * a.tpb).skip, 0);
+  return w;
 }
 
 // Partitions.  With W key tiles of work per SM cut into partitions of p, a
@@ -245,8 +286,8 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 
 // Sorts the sequences and numbers their items (one warp): Misc::seq -> order, parts,
 // first.  Run once by a cold instruction cache: short code, not unrolled.
-template <bool PAGED>
-__device__ __forceinline__ void number_items(const Args &a, Misc *m) {
+template <bool PAGED, int FORM>
+__device__ __forceinline__ void number_items(const FormArgs<FORM> &a, Misc *m) {
   const int lane = threadIdx.x & 31;
   auto seq = [&](int i) {
     return make_seq(a, PAGED, m->seq[i].x, m->seq[i + 1].x, m->seq[i].y);
@@ -255,7 +296,7 @@ __device__ __forceinline__ void number_items(const Args &a, Misc *m) {
   if (PAGED && a.n_split > 1) {
 #pragma unroll 1
     for (int i = lane; i < a.S; i += 32) {
-      const Work w = work_of(a, seq(i));
+      const Work w = work_of<FORM>(a, seq(i));
       work += static_cast<int64_t>(w.tiles) * w.blocks;
     }
     work = warp_sum(work);
@@ -264,7 +305,7 @@ __device__ __forceinline__ void number_items(const Args &a, Misc *m) {
 #pragma unroll 1
   for (int i = lane; i < a.S; i += 32) {
     const Seq q = seq(i);
-    const int tiles = work_of(a, q).tiles;
+    const int tiles = work_of<FORM>(a, q).tiles;
     const int parts = PAGED ? parts_of(a, q, tiles, work) : 1;
     const int size = PAGED ? part_size(tiles, parts) : tiles;
     m->key[i] = min(size, (1 << 23) - 1) * 128 + i;
@@ -279,7 +320,7 @@ __device__ __forceinline__ void number_items(const Args &a, Misc *m) {
     for (int j = 0; j < a.S; ++j) rank += m->key[j] < key ? 1 : 0;
     m->order[rank] = static_cast<uint8_t>(i);
     m->parts[rank] = m->n_parts[i];
-    m->first[rank] = work_of(a, seq(i)).blocks * m->n_parts[i] * a.Hk;
+    m->first[rank] = work_of<FORM>(a, seq(i)).blocks * m->n_parts[i] * a.Hk;
   }
   __syncwarp();
   int carry = 0;
@@ -301,9 +342,9 @@ __device__ __forceinline__ void number_items(const Args &a, Misc *m) {
 
 // Item w of n_items (whole warp); false if it has no work.  m: the numbered
 // sequences, or null.
-template <bool PAGED>
-__device__ __forceinline__ bool decode_item(const Args &a, const Misc *m, int n_items, int w,
-                                            Item &it) {
+template <bool PAGED, int FORM>
+__device__ __forceinline__ bool decode_item(const FormArgs<FORM> &a, const Misc *m, int n_items,
+                                            int w, Item &it, Gap &gap) {
   const int tb = 2 * a.tpb, u = n_items - 1 - w;
   int s, blk, parts = 1;
   Seq q;
@@ -336,11 +377,12 @@ __device__ __forceinline__ bool decode_item(const Args &a, const Misc *m, int n_
   it.pos0 = q.pos + tok0;
   it.kv_len = q.kv_len;
   it.kv0 = PAGED ? s : q.begin;
+  gap = gap_of<FORM>(a, it.pos0);
   int total[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     it.n_tok[t] = clampi(q.n - tok0 - t * a.tpb, 0, a.tpb);
-    total[t] = tiles_for(it.n_tok[t], it.pos0 + t * a.tpb + it.n_tok[t] - 1, q.kv_len);
+    total[t] = tiles_for(it.n_tok[t], it.pos0 + t * a.tpb + it.n_tok[t] - 1, q.kv_len) - gap.skip;
   }
   const int size = part_size(max(total[0], total[1]), parts);
   it.split = parts > 1;
@@ -348,8 +390,8 @@ __device__ __forceinline__ bool decode_item(const Args &a, const Misc *m, int n_
 #pragma unroll
   for (int t = 0; t < 2; ++t) it.n[t] = clampi(total[t] - it.kt0, 0, size);
   // Where both tiles visit the sequence's ragged last key tile A clears its V, whose
-  // P V goes first.
-  it.clear[0] = q.kv_len % BN != 0 ? q.kv_len / BN - it.kt0 : -1;
+  // P V goes first.  (It lies behind the gap: no earlier than the window's first tile.)
+  it.clear[0] = q.kv_len % BN != 0 ? q.kv_len / BN - gap.skip - it.kt0 : -1;
   it.clear[1] = it.n[0] <= it.clear[0] ? it.clear[0] : -1;
   return it.part == 0 || it.n[0] > 0 || it.n[1] > 0;
 }
@@ -422,11 +464,11 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t ph) {
   }
 }
 
-template <int D, bool F16, bool PAGED>
+template <int D, bool F16, bool PAGED, int FORM>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_packed_kernel(const __grid_constant__ CUtensorMap tm_q,
                       const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const Args a) {
+                      const __grid_constant__ CUtensorMap tm_v, const FormArgs<FORM> a) {
   using C = Cfg<D, PAGED>;
   static_assert(!PAGED || (D == 128 && !F16), "the paged cache is bf16, d = 128");
   constexpr int R = C::kSlots;
@@ -507,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tm_v);
       }
       if (cached) {
-        number_items<PAGED>(a, misc);
+        number_items<PAGED, FORM>(a, misc);
       }
       const Misc *numbered = cached ? misc : nullptr;
       const int n_items = cached ? misc->first[a.S] : a.n_vblocks * a.Hk;
@@ -521,12 +563,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto claimed = [&]() { return __shfl_sync(~0u, w_claim, 0); };
       // The next item with work at or after w, claiming on; live = 0 at the end.
       Item nxt;
+      Gap nxt_gap;
       int nxt_id = 0;           // paged: block id of the item's block `lane`
-      auto ids_of = [&](const Item &it, int tile) -> int {
-        // Lane i: block i of the four key tiles from `tile` on; past the
-        // context, a block that the cache does not have (reads as zeros).
-        const int b = tile * kTileBlocks + lane;
+      auto ids_of = [&](const Item &it, const Gap &gap, int x) -> int {
+        // Lane i: block i of the four key tiles from entry x on; past the context, or
+        // where no token of the item sees it, a block that the cache does not have
+        // (reads as zeros).
+        const int b = FORM == kWindow
+                          ? gap.tile(x + lane / kTileBlocks) * kTileBlocks + lane % kTileBlocks
+                          : x * kTileBlocks + lane;
         if (b >= (it.kv_len + kBlk - 1) / kBlk) return a.num_blocks;
+        if constexpr (FORM == kWindow)
+          if (b * kBlk >= a.sinks && b * kBlk + kBlk - 1 <= it.pos0 - a.window)
+            return a.num_blocks;
         return a.block_tables[static_cast<int64_t>(it.kv0) * a.max_blocks + b];
       };
       auto find = [&]() {
@@ -535,11 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             nxt.live = 0;
             return;
           }
-          if (decode_item<PAGED>(a, numbered, n_items, w, nxt)) break;
+          if (decode_item<PAGED, FORM>(a, numbered, n_items, w, nxt, nxt_gap)) break;
           claim();
           w = claimed();
         }
-        if (PAGED) nxt_id = ids_of(nxt, nxt.kt0);
+        if (PAGED) nxt_id = ids_of(nxt, nxt_gap, nxt.kt0);
       };
       // Waits (lane 0) for ring slot e % R to be free and announces its copy.
       auto open_slot = [&]() -> bool {
@@ -553,12 +602,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       find();
       for (int k = 0; ok; ++k) {
         const Item it = nxt;
+        const Gap gap = nxt_gap;
         int ids = nxt_id, ids_next = 0;
         const int slot = k & 1;
         if (lane == 0) {
           ok = mbar_wait(bar(kBarItemEmpty + slot), ((k >> 1) & 1) ^ 1, abort_flag);
           if (ok) {
             misc->item[slot] = it;
+            if (FORM == kWindow) misc->gap[slot] = gap;
             mbar_arrive(bar(kBarItemFull + slot));
           }
         }
@@ -590,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const int n_max = max(it.n[0], it.n[1]);
         for (int j = 0; j < n_max; ++j) {
-          const int tile = it.kt0 + j;
+          const int tile = FORM == kWindow ? gap.tile(it.kt0 + j) : it.kt0 + j;
           // The next item is claimed as late as its loads allow (an item held by a
           // CTA that is busy is lost to the others: 2 sequences of 4096, 16 heads,
           // 113 us when it was claimed at the start, 94 so), decoded behind the last copy.
@@ -599,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (PAGED) {
             if ((j & 3) == 0) {
               if (j > 0) ids = ids_next;
-              if (j + 4 < n_max) ids_next = ids_of(it, tile + 4);
+              if (j + 4 < n_max) ids_next = ids_of(it, gap, it.kt0 + j + 4);
             }
             pb = __shfl_sync(~0u, ids, (j & 3) * kTileBlocks + (lane & 7));
           }
@@ -779,7 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!it.live) break;
       const int n_mine = it.n[t];
       // Keys below lim are visible to this row (the first is key 0 of the partition).
-      const int lim = min(it.kv_len, it.pos0 + t * a.tpb + row_in_tile() / a.G + 1) - it.kt0 * BN;
+      const int lim = min(it.kv_len, it.pos0 + t * a.tpb + row_in_tile() / a.G + 1) -
+                      (FORM == kWindow ? 0 : it.kt0 * BN);
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n_mine; ++j, phases ^= 1) {
         if (j == it.clear[t]) {
@@ -810,8 +862,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_wait_ld(sv[c]);
 #define S_(c) sv[(c) >> 5][(c) & 31]
+        if constexpr (FORM == kWindow) {
+          // lim counts from key 0; keys from lim - window on, or below `sinks`, are
+          // visible.  (A row that holds a query sees its own position: lim is that + 1.)
+          const volatile Gap &gap = misc->gap[k & 1];
+          const int x = it.kt0 + j, base = (x + (x >= gap.at ? gap.skip : 0)) * BN;
+          const int lim_j = lim - base, low_j = lim_j - a.window, first_j = a.sinks - base;
+          if (__any_sync(~0u, lim_j < BN || low_j > max(first_j, 0))) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t bits = low_bits(lim_j - 32 * w) & (~low_bits(low_j - 32 * w) |
+                                                                low_bits(first_j - 32 * w));
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (((bits >> c) & 1u) == 0u) sv[w][c] = __float_as_uint(-INFINITY);
+            }
+          }
+        }
         const int lim_j = lim - j * BN;
-        if (__any_sync(~0u, lim_j < BN)) {
+        if (FORM != kWindow && __any_sync(~0u, lim_j < BN)) {
 #pragma unroll
           for (int w = 0; w < 4; ++w) {   // by bit masks: half the instructions of compares
             const int n = lim_j - 32 * w;
@@ -993,7 +1062,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // dimensions a lane.  By sequence, because a grid over all rows costs 40 us where few
 // are cut; 4 us for 16 chunks of up to 6 tokens, 32 heads, of which the rows' loads
 // are the smaller part and the launch and the chain of (max, sum) the larger.
-__global__ void __launch_bounds__(256) paged_merge_kernel(const Args a) {
+template <int FORM>
+__global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a) {
   constexpr int D = kDecodeHeadSize;
   // The next kernel of the stream may be scheduled: it waits for this grid.
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1009,14 +1079,14 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const Args a) {
   if (threadIdx.x < 32) {
     int64_t work = 0;
     for (int i = lane; i < a.S; i += 32) {
-      const Work w = work_of(a, global_seq<true>(a, i));
+      const Work w = work_of<FORM>(a, global_seq<true>(a, i));
       work += static_cast<int64_t>(w.tiles) * w.blocks;
     }
     work = warp_sum(work);
     const Seq q = global_seq<true>(a, blockIdx.x);
     if (lane == 0) {
       shared_seq = q;
-      shared_cut = parts_of(a, q, work_of(a, q).tiles, work);
+      shared_cut = parts_of(a, q, work_of<FORM>(a, q).tiles, work);
     }
   }
   __syncthreads();
@@ -1028,9 +1098,10 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const Args a) {
     const int i = x / a.H;                               // token of the sequence
     const int64_t row = static_cast<int64_t>(q.begin) * a.H + x;
     // The block's last token sets the partitions' size, the row's own those it is in.
-    const int last = min((i / (2 * a.tpb) + 1) * 2 * a.tpb, q.n) - 1;
-    const int size = part_size(tiles_for(1, q.pos + last, q.kv_len), cut);
-    const int parts = (tiles_for(1, q.pos + i, q.kv_len) + size - 1) / size;
+    const int block = i / (2 * a.tpb), last = min((block + 1) * 2 * a.tpb, q.n) - 1;
+    const int skip = gap_of<FORM>(a, q.pos + block * 2 * a.tpb).skip;
+    const int size = part_size(tiles_for(1, q.pos + last, q.kv_len) - skip, cut);
+    const int parts = (tiles_for(1, q.pos + i, q.kv_len) - skip + size - 1) / size;
     // 32 partitions at a time, lane p holding partition p's (max, sum): their rows'
     // loads do not wait for one another.
     float m = -INFINITY, l = 0.f;
@@ -1078,14 +1149,14 @@ cudaError_t sm_count(int *n) {
   return e;
 }
 
-template <int D, bool F16, bool PAGED>
-cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, Args a,
-                   cudaStream_t stream) {
+template <int D, bool F16, bool PAGED, int FORM>
+cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                   const FormArgs<FORM> &a, cudaStream_t stream) {
   using C = Cfg<D, PAGED>;
   int sms = 0;
   cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(fwd_packed_kernel<D, F16, PAGED>,
+  e = cudaFuncSetAttribute(fwd_packed_kernel<D, F16, PAGED, FORM>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
   if (e != cudaSuccess) return e;
   const int64_t n_items = static_cast<int64_t>(a.n_vblocks) * a.n_split * a.Hk;   // a bound
@@ -1099,13 +1170,24 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, fwd_packed_kernel<D, F16, PAGED>, tq, tk, tv, a);
+  e = cudaLaunchKernelEx(&cfg, fwd_packed_kernel<D, F16, PAGED, FORM>, tq, tk, tv, a);
   if (e != cudaSuccess || !PAGED || a.n_split == 1) return e;
   // Eight blocks an SM in all, spread over the sequences (at most kCachedSeqs).
   cfg.gridDim = dim3(static_cast<unsigned>(a.S), static_cast<unsigned>(8 * sms / a.S));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel, a);
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<FORM>, a);
+}
+
+template <int FORM>
+cudaError_t launch_packed_form(const CUtensorMap &tq, const CUtensorMap &tk,
+                               const CUtensorMap &tv, const FormArgs<FORM> &a, int d, bool f16,
+                               cudaStream_t stream) {
+  if (d == 64)
+    return f16 ? launch<64, true, false, FORM>(tq, tk, tv, a, stream)
+               : launch<64, false, false, FORM>(tq, tk, tv, a, stream);
+  return f16 ? launch<128, true, false, FORM>(tq, tk, tv, a, stream)
+             : launch<128, false, false, FORM>(tq, tk, tv, a, stream);
 }
 
 Args args_of(const PackedProblem &p, int *sched, int *dev_status, int fault_cta) {
@@ -1128,6 +1210,13 @@ Args args_of(const PackedProblem &p, int *sched, int *dev_status, int fault_cta)
   return a;
 }
 
+WindowArgs window_args(const Args &a, const PackedProblem &p) {
+  WindowArgs w;
+  static_cast<Args &>(w) = a;
+  w.window = p.window, w.sinks = p.sinks;
+  return w;
+}
+
 }  // namespace
 
 int packed_tile_tokens(int group) { return BM / group; }
@@ -1138,11 +1227,8 @@ cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, cons
                               const PackedProblem &p, int d, bool f16, int *sched,
                               int *dev_status, int fault_cta, cudaStream_t stream) {
   const Args a = args_of(p, sched, dev_status, fault_cta);
-  if (d == 64)
-    return f16 ? launch<64, true, false>(tq, tk, tv, a, stream)
-               : launch<64, false, false>(tq, tk, tv, a, stream);
-  return f16 ? launch<128, true, false>(tq, tk, tv, a, stream)
-             : launch<128, false, false>(tq, tk, tv, a, stream);
+  if (p.window == 0) return launch_packed_form<kAll>(tq, tk, tv, a, d, f16, stream);
+  return launch_packed_form<kWindow>(tq, tk, tv, window_args(a, p), d, f16, stream);
 }
 
 // The most partitions of a context, from what the host knows (the longest one's
@@ -1151,17 +1237,22 @@ cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, cons
 // Beyond kCachedSeqs sequences, whose bounds and numbering do not fit the barrier area,
 // nothing is cut: a long context among short ones is then one chain of its key tiles
 // (131072 tokens among 1024s, 32 / 8 heads: 169 us with 112 sequences, 1350 with 113).
-int paged_max_parts(int T, int S, int H, int Hk, int max_blocks) {
+int paged_max_parts(int T, int S, int H, int Hk, int max_blocks, int window, int sinks) {
   if (S > kCachedSeqs) return 1;
-  const double tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;
+  double tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;
+  // With a window, a block's list of key tiles is that long at most.
+  if (window > 0)
+    tiles = std::fmin(tiles, (window + 2.0 * packed_tile_tokens(H / Hk)) / BN + 2 +
+                                 (sinks + BN - 1) / BN);
   const double least = std::fmax(4.0, std::sqrt(tiles * Hk / 152 * 2.5 / 0.7));
   const double room = 256e6 / (sizeof(float) * (kDecodeHeadSize + 2.0) * T * H);
   const double n = std::fmin(std::fmin(tiles / least + 1, room), 32767);
   return n < 1 ? 1 : static_cast<int>(n);
 }
 
-size_t paged_prefill_workspace_bytes(int T, int S, int H, int Hk, int max_blocks) {
-  const int n = paged_max_parts(T, S, H, Hk, max_blocks);
+size_t paged_prefill_workspace_bytes(int T, int S, int H, int Hk, int max_blocks, int window,
+                                     int sinks) {
+  const int n = paged_max_parts(T, S, H, Hk, max_blocks, window, sinks);
   if (n == 1) return 0;
   return static_cast<size_t>(n) * T * H * (kDecodeHeadSize + 2) * sizeof(float);
 }
@@ -1171,14 +1262,15 @@ cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
                                  int *sched, int *dev_status, int fault_cta,
                                  cudaStream_t stream) {
   Args a = args_of(p, sched, dev_status, fault_cta);
-  const int n = paged_max_parts(p.T, p.S, p.H, p.Hk, p.max_blocks);
+  const int n = paged_max_parts(p.T, p.S, p.H, p.Hk, p.max_blocks, p.window, p.sinks);
   if (n > 1) {
     a.n_split = n;
     a.ws_o = workspace;
     a.ws_ml = reinterpret_cast<float2 *>(workspace + static_cast<size_t>(n) * p.T * p.H *
                                                          kDecodeHeadSize);
   }
-  return launch<128, false, true>(tq, tk, tv, a, stream);
+  if (p.window == 0) return launch<128, false, true, kAll>(tq, tk, tv, a, stream);
+  return launch<128, false, true, kWindow>(tq, tk, tv, window_args(a, p), stream);
 }
 
 }  // namespace fattn

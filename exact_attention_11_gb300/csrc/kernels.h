@@ -198,6 +198,9 @@ struct PackedProblem {
   const int *cu_seqlens, *context_lens, *block_tables;
   int S, T, H, Hk, max_blocks, num_blocks, causal;
   float scale;
+  // A query at position p sees keys j <= p with j > p - window or j < sinks (both up to
+  // 2^30); window 0: all keys up to its own (packed and not causal: all).
+  int window, sinks;
 };
 int packed_tile_tokens(int group);              // tokens of a 128-row query tile
 int packed_blocks(int T, int S, int group);     // bound on the two-tile blocks of a call
@@ -206,8 +209,9 @@ cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, cons
                               int *dev_status, int fault_cta, cudaStream_t stream);
 // Paged: the most partitions that a context is cut into, and the fp32 workspace that
 // they need (0 bytes when it is one).
-int paged_max_parts(int T, int S, int H, int Hk, int max_blocks);
-size_t paged_prefill_workspace_bytes(int T, int S, int H, int Hk, int max_blocks);
+int paged_max_parts(int T, int S, int H, int Hk, int max_blocks, int window = 0, int sinks = 0);
+size_t paged_prefill_workspace_bytes(int T, int S, int H, int Hk, int max_blocks, int window = 0,
+                                     int sinks = 0);
 cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
                                  const CUtensorMap &tv, const PackedProblem &p, float *workspace,
                                  int *sched, int *dev_status, int fault_cta,

@@ -607,6 +607,57 @@ int fa_paged_prefill(const void *q, const void *k_cache, const void *v_cache,
                      unsigned long long workspace_bytes, fa_stream_t stream);
 
 /*
+ * Attention with a sliding window: a query at position p of its sequence sees key j
+ * iff
+ *     j <= p  and  (j > p - window  or  j < sinks):
+ * the last `window` keys up to its own, and the sequence's first `sinks` keys, which
+ * stay visible (attention sinks).  window >= 1, sinks >= 0 (else FA_ERR_INVALID_ARG);
+ * a window as long as the sequence is the causal mask.  Work and memory traffic are
+ * those of the visible key tiles: 128 keys from the first key that a block of queries
+ * sees on, and the tiles of the first keys.
+ *
+ * fa_forward_packed_window, fa_forward_packed_window_f16 -- fa_forward_packed (causal)
+ * and fa_forward_packed_f16 with this mask; every other argument, layout, rounding and
+ * error as there.
+ */
+int fa_forward_packed_window(const void *q, const void *k, const void *v, void *o, float *lse,
+                             const int *cu_seqlens, int num_seqs, int total_tokens,
+                             int num_heads, int num_kv_heads, int d, long long q_stride,
+                             long long k_stride, long long v_stride, float scale, int window,
+                             int sinks, fa_stream_t stream);
+int fa_forward_packed_window_f16(const void *q, const void *k, const void *v, void *o, float *lse,
+                                 const int *cu_seqlens, int num_seqs, int total_tokens,
+                                 int num_heads, int num_kv_heads, int d, long long q_stride,
+                                 long long k_stride, long long v_stride, float scale, int window,
+                                 int sinks, fa_stream_t stream);
+
+/*
+ * fa_paged_prefill_window -- fa_paged_prefill with this mask: chunks of any length,
+ * single tokens included, over the paged cache.  Query i of sequence s has position
+ * context_lens[s] - n + i; positions before 0 (a context shorter than its chunk) see
+ * nothing and get zero rows.
+ *
+ * The table entries of blocks that no query of the chunk sees -- every token of theirs
+ * is `sinks` or later and at most (position of the chunk's first query) - window -- are
+ * not used: such blocks may have been given back, and their entries may hold anything
+ * (-1, or a block that now belongs to another sequence).  Table column t / block_size
+ * stays that of token t.  Everything else, the workspace among it (its size from
+ * fa_paged_prefill_window_workspace_bytes), as for fa_paged_prefill; contexts of up to
+ * 112 sequences are cut into partitions here too.
+ */
+unsigned long long fa_paged_prefill_window_workspace_bytes(int num_seqs, int total_tokens,
+                                                           int num_heads, int num_kv_heads,
+                                                           int max_num_blocks_per_seq, int window,
+                                                           int sinks);
+int fa_paged_prefill_window(const void *q, const void *k_cache, const void *v_cache,
+                            const int *block_tables, const int *context_lens,
+                            const int *cu_seqlens, void *out, int num_seqs, int total_tokens,
+                            int num_heads, int num_kv_heads, int head_size, int block_size,
+                            int num_blocks, int max_num_blocks_per_seq, long long q_stride,
+                            float scale, int window, int sinks, void *workspace,
+                            unsigned long long workspace_bytes, fa_stream_t stream);
+
+/*
  * fa_debug_inject_fault -- test hook for the device-side failure path.
  *
  * mode 1 arms the current device: the next tensor-core forward launched on
