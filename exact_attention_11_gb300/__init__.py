@@ -33,7 +33,9 @@ __all__ = ["fa_forward", "fa_forward_f16", "fa_forward_masked", "forward_masked"
            "fa_forward_packed_f16", "forward_packed", "fa_backward_packed",
            "fa_backward_packed_workspace_bytes", "backward_packed", "fa_paged_prefill",
            "fa_paged_prefill_workspace_bytes", "paged_prefill", "fa_forward_packed_window",
-           "fa_forward_packed_window_f16", "forward_packed_window", "fa_paged_prefill_window",
+           "fa_forward_packed_window_f16", "forward_packed_window", "fa_backward_packed_window",
+           "fa_backward_packed_window_workspace_bytes", "backward_packed_window",
+           "fa_paged_prefill_window",
            "fa_paged_prefill_window_workspace_bytes", "paged_prefill_window",
            "fa_device_status", "fa_release", "forward", "paged_decode", "FattnError",
            "library_path", "load"]
@@ -97,6 +99,9 @@ EXPORTS = {
     "fa_paged_prefill": ([_vp] * 7 + [_i] * 8 + [_ll, _f, _vp, ctypes.c_ulonglong, _vp], _i),
     "fa_forward_packed_window": ([_vp] * 6 + [_i] * 5 + [_ll] * 3 + [_f, _i, _i, _vp], _i),
     "fa_forward_packed_window_f16": ([_vp] * 6 + [_i] * 5 + [_ll] * 3 + [_f, _i, _i, _vp], _i),
+    "fa_backward_packed_window_workspace_bytes": ([_i] * 7, ctypes.c_ulonglong),
+    "fa_backward_packed_window": ([_vp] * 10 + [_i] * 5 + [_ll] * 3
+                                  + [_f, _i, _i, _vp, ctypes.c_ulonglong, _vp], _i),
     "fa_paged_prefill_window_workspace_bytes": ([_i] * 7, ctypes.c_ulonglong),
     "fa_paged_prefill_window": ([_vp] * 7 + [_i] * 8 + [_ll, _f, _i, _i, _vp, ctypes.c_ulonglong,
                                                         _vp], _i),
@@ -322,6 +327,22 @@ def fa_forward_packed_window_f16(q, k, v, o, lse, cu_seqlens, num_seqs, total_to
     return _check("fa_forward_packed_window_f16", load().fa_forward_packed_window_f16(
         q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads, num_kv_heads, d, q_stride,
         k_stride, v_stride, scale, window, sinks, stream))
+
+
+def fa_backward_packed_window_workspace_bytes(num_seqs, total_tokens, num_heads, num_kv_heads, d,
+                                              window, sinks) -> int:
+    return int(load().fa_backward_packed_window_workspace_bytes(
+        num_seqs, total_tokens, num_heads, num_kv_heads, d, window, sinks))
+
+
+def fa_backward_packed_window(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, num_seqs,
+                              total_tokens, num_heads, num_kv_heads, d, q_stride, k_stride,
+                              v_stride, scale, window, sinks, workspace, workspace_bytes,
+                              stream) -> int:
+    return _check("fa_backward_packed_window", load().fa_backward_packed_window(
+        q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, num_seqs, total_tokens, num_heads,
+        num_kv_heads, d, q_stride, k_stride, v_stride, scale, window, sinks, workspace,
+        workspace_bytes, stream))
 
 
 def fa_paged_prefill_window_workspace_bytes(num_seqs, total_tokens, num_heads, num_kv_heads,
@@ -883,6 +904,24 @@ def backward_packed(q, k, v, o, lse, dout, cu_seqlens, scale=None, causal=True, 
     (optional) is a CUDA tensor of at least
     ``fa_backward_packed_workspace_bytes`` bytes.  Rows of no sequence are not
     written.  Runs on the current torch stream."""
+    return _backward_packed("fa_backward_packed", q, k, v, o, lse, dout, cu_seqlens, scale,
+                            workspace, (), int(causal))
+
+
+@_on_device
+def backward_packed_window(q, k, v, o, lse, dout, cu_seqlens, window, sinks=0, scale=None,
+                           workspace=None):
+    """Gradients (dQ, dK, dV) of the bf16 ``forward_packed_window``, as
+    ``backward_packed``; ``o`` and ``lse`` are what it returned for the same q, k,
+    v, cu_seqlens, window, sinks and scale.  ``workspace`` (optional) is a CUDA
+    tensor of at least ``fa_backward_packed_window_workspace_bytes`` bytes."""
+    mask = _window_args(window, sinks)
+    return _backward_packed("fa_backward_packed_window", q, k, v, o, lse, dout, cu_seqlens, scale,
+                            workspace, mask, *mask)
+
+
+def _backward_packed(name, q, k, v, o, lse, dout, cu_seqlens, scale, workspace, sizes, *mask):
+    """``sizes``: what the workspace depends on besides the tensors' sizes."""
     torch = _torch()
     T, H, Hk, d, S, dtype, dev, qs, ks, vs, cu = _packed_args(q, k, v, cu_seqlens,
                                                               (torch.bfloat16,))
@@ -900,13 +939,13 @@ def backward_packed(q, k, v, o, lse, dout, cu_seqlens, scale=None, causal=True, 
         return dq, dk, dv
     lib = _lib or load()
     if workspace is None:
-        nbytes = lib.fa_backward_packed_workspace_bytes(S, T, H, Hk, d)
+        nbytes = getattr(lib, name + "_workspace_bytes")(S, T, H, Hk, d, *sizes)
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     else:
         nbytes = _workspace(workspace, dev)
-    _check("fa_backward_packed", lib.fa_backward_packed(
+    _check(name, getattr(lib, name)(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), *ins, dq.data_ptr(), dk.data_ptr(),
-        dv.data_ptr(), cu, S, T, H, Hk, d, qs, ks, vs, scale, int(causal), workspace.data_ptr(),
+        dv.data_ptr(), cu, S, T, H, Hk, d, qs, ks, vs, scale, *mask, workspace.data_ptr(),
         nbytes, _raw_stream(dev)))
     return dq, dk, dv
 

@@ -55,6 +55,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "bwd_tile.cuh"
 #include "kernels.h"
@@ -123,6 +124,7 @@ struct Misc {
   int abort;
   int item[2];
   int4 seq[2];          // PACKED: the item's entry of the block table
+  int2 range[2];        // kWindow: its first query block and their number
 };
 static_assert(kNumBars * 8 + sizeof(Misc) <= 512 && kNumBars % 2 == 0, "barrier area");
 
@@ -165,6 +167,11 @@ struct BwdItem {
     jb = e.w;
     steps((N + BQ - 1) / BQ, causal);
   }
+  __device__ void set_steps(int first, int n) {
+    i_first = first;
+    n_steps = n;
+    n_halves = 2 * n;
+  }
   __device__ void steps(int n_qb, int causal) {
     k0 = jb * BM;
     i_first = causal ? jb : 0;
@@ -173,7 +180,13 @@ struct BwdItem {
   }
 };
 
-template <bool PACKED>
+// What the kernel runs on: [B, H, N, d] tensors, packed sequences, or packed sequences
+// with a window.
+enum : int { kDense = 0, kPacked = 1, kWindow = 2 };
+template <int KIND>
+using Extra = std::conditional_t<KIND == kWindow, BwdWindow, BwdPacked>;
+
+template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_pipe_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -182,7 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __nv_bfloat16 *__restrict__ dk, __nv_bfloat16 *__restrict__ dv, int N, int BH,
                     float scale, int causal, int *__restrict__ sched, int fault_cta,
                     int *__restrict__ dev_status, const __grid_constant__ CUtensorMap tm_dk,
-                    const __grid_constant__ CUtensorMap tm_dv, const BwdPacked pk) {
+                    const __grid_constant__ CUtensorMap tm_dv, const Extra<KIND> pk) {
+  constexpr bool PACKED = KIND != kDense, WINDOW = KIND == kWindow;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t s_base = smem_u32(smem);
   if ((s_base & 1023u) != 0) {
@@ -196,7 +210,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // PACKED: BH is the number of query heads; vecs and the accumulators count
   // padded blocks.
   const int n_qb = PACKED ? pk.n_blocks : (N + BQ - 1) / BQ;
-  const int n_items = n_qb * BH;
+  int n_items = n_qb * BH;
+  if constexpr (WINDOW) n_items = pk.entries * BH;
 
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
@@ -246,6 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (PACKED) {
       const volatile int *e = reinterpret_cast<const volatile int *>(&misc->seq[slot]);
       it.decode_packed(w, make_int4(e[0], e[1], e[2], e[3]), BH, pk.group, causal);
+      const volatile int *r = reinterpret_cast<const volatile int *>(&misc->range[slot]);
+      if (WINDOW) it.set_steps(r[0], r[1]);
     } else {
       it.decode(w, BH, n_qb, causal, N);
     }
@@ -264,6 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_do);
       int nq = 0, ndo = 0, nkv = 0;   // halves (and K/V pairs) issued so far
       bool ok = true;
+      int n_entries = 0;
+      if constexpr (WINDOW) n_entries = *pk.count;
       auto claim = [&]() { return static_cast<int>(gridDim.x) + atomicAdd(sched, 1); };
       for (int k = 0; ok; ++k) {
         const int islot = k & 1;
@@ -271,10 +290,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The CTA's own first item, then claimed ones.
         int w = k == 0 ? static_cast<int>(blockIdx.x) : claim();
         int4 entry = make_int4(0, 0, 0, 0);
+        int2 range = make_int2(0, 0);
         if (PACKED) {
+          auto in_table = [&](int x) { return WINDOW && x / BH >= n_entries ? n_items : x; };
+          w = in_table(w);
           // Entries of length 0 end a sorted table, else are passed over.
           while (w < n_items && (entry = pk.table[w / BH]).y == 0)
-            w = pk.sorted ? n_items : claim();
+            w = pk.sorted ? n_items : in_table(claim());
+          if constexpr (WINDOW)
+            if (w < n_items) range = pk.range[w / BH];
           // (Offsets that decrease leave entries unwritten: whatever they hold, the
           // item stays inside the tensors.)
           entry.x = min(max(entry.x, 0), pk.tokens - 1);
@@ -283,14 +307,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           entry.z = min(max(entry.z, 0), max(pk.n_blocks - n_kb, 0));
           entry.w = min(max(entry.w, 0), n_kb - 1);
           misc->seq[islot] = entry;
+          if (WINDOW) {
+            range.x = min(max(range.x, 0), n_kb - 1);
+            range.y = min(max(range.y, 1), n_kb - range.x);
+            misc->range[islot] = range;
+          }
         }
         misc->item[islot] = w;
         mbar_arrive(bar(kBarItemFull + islot));
         if (w >= n_items) break;
         BwdItem it;
-        if (PACKED)
+        if (PACKED) {
           it.decode_packed(w, entry, BH, pk.group, causal);
-        else
+          if (WINDOW) it.set_steps(range.x, range.y);
+        } else
           it.decode(w, BH, n_qb, causal, N);
         const int h_base = nq;
         // Q / dO half h of the item (with its [LSE2 | D] vectors on QFull).
@@ -540,11 +570,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Masking is needed only where a key of this warp is past N or, on the
         // diagonal block, later than a query (warp-uniform).
         const bool diag = causal && (q0 < it.k0 + BM) && (q0 + BH_ > it.k0);
-        const bool masked = diag || (it.k0 + quarter * 32 + 31 >= it.N);
+        bool masked = diag || (it.k0 + quarter * 32 + 31 >= it.N);
+        uint64_t see = 0;
+        if constexpr (WINDOW) {
+          // ... or, unless it is one of the first, too far before one.
+          const int key_w = it.k0 + quarter * 32;
+          masked |= q0 + BH_ - 1 - key_w >= pk.window && key_w + 31 >= pk.sinks;
+          if (masked) see = bwd_tile::near_queries(key, q0, it.N, pk.window, pk.sinks);
+        }
         if (masked)
-          bwd_tile::chunks<true>(R, vec, ds_buf, r, key, q0, it.N, diag, c2);
+          bwd_tile::chunks<WINDOW ? 2 : 1>(R, vec, ds_buf, r, key, q0, it.N, diag, see, c2);
         else
-          bwd_tile::chunks<false>(R, vec, ds_buf, r, key, q0, it.N, diag, c2);
+          bwd_tile::chunks<0>(R, vec, ds_buf, r, key, q0, it.N, diag, see, c2);
         tmem_wait_st();
         fence_proxy_async_smem();
         tc_fence_before();
@@ -609,8 +646,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarEpiDone));
-      if (PACKED && pk.group > 1) {
-        // Another query head of the group adds to the same rows: fp32 boxes of
+      bool shared = PACKED && pk.group > 1;
+      if constexpr (WINDOW) shared = shared || it.k0 < pk.split;
+      if (shared) {
+        // Another query head of the group (kWindow: or another item of the block of
+        // first keys) adds to the same rows: fp32 boxes of
         // 32 rows x 32 columns into the accumulator (dK there still unscaled).
         // Rows past the sequence fall on its padding.
 #pragma unroll
@@ -689,21 +729,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool PACKED>
+template <int KIND>
 cudaError_t launch_main(const CUtensorMap &tq64, const CUtensorMap &tk, const CUtensorMap &tv,
                         const CUtensorMap &tdo64, const CUtensorMap &tdq, const float *vecs,
                         void *dk, void *dv, int BH, int N, float scale, int causal, int *sched,
                         int fault_cta, int *dev_status, cudaStream_t stream,
-                        const CUtensorMap &tdk, const CUtensorMap &tdv, const BwdPacked &pk) {
-  cudaError_t e = cudaFuncSetAttribute(bwd_pipe_kernel<PACKED>,
+                        const CUtensorMap &tdk, const CUtensorMap &tdv, const Extra<KIND> &pk) {
+  cudaError_t e = cudaFuncSetAttribute(bwd_pipe_kernel<KIND>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   int dev = 0, n_sm = 0;
   if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return e;
-  const int n_qb = PACKED ? pk.n_blocks : (N + BQ - 1) / BQ;
-  const long long n_items = static_cast<long long>(n_qb) * BH;
+  long long n_items = KIND == kDense ? (N + BQ - 1) / BQ : pk.n_blocks;
+  if constexpr (KIND == kWindow) n_items = pk.entries;
+  n_items *= BH;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(n_items < n_sm ? n_items : n_sm));
   cfg.blockDim = dim3(kThreads);
@@ -714,7 +755,7 @@ cudaError_t launch_main(const CUtensorMap &tq64, const CUtensorMap &tk, const CU
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, bwd_pipe_kernel<PACKED>, tq64, tk, tv, tdo64, tdq, vecs,
+  return cudaLaunchKernelEx(&cfg, bwd_pipe_kernel<KIND>, tq64, tk, tv, tdo64, tdq, vecs,
                             reinterpret_cast<__nv_bfloat16 *>(dk),
                             reinterpret_cast<__nv_bfloat16 *>(dv), N, BH, scale, causal, sched,
                             fault_cta, dev_status, tdk, tdv, pk);
@@ -727,7 +768,7 @@ cudaError_t launch_bwd_main_d128(const CUtensorMap &tq64, const CUtensorMap &tk,
                                  const CUtensorMap &tdq, const float *vecs, void *dk, void *dv,
                                  int BH, int N, float scale, int causal, int *sched,
                                  int fault_cta, int *dev_status, cudaStream_t stream) {
-  return launch_main<false>(tq64, tk, tv, tdo64, tdq, vecs, dk, dv, BH, N, scale, causal, sched,
+  return launch_main<kDense>(tq64, tk, tv, tdo64, tdq, vecs, dk, dv, BH, N, scale, causal, sched,
                             fault_cta, dev_status, stream, tdq, tdq, BwdPacked{});
 }
 
@@ -738,7 +779,18 @@ cudaError_t launch_bwd_packed_main_d128(const CUtensorMap &tq64, const CUtensorM
                                         void *dv, int H, const BwdPacked &pk, float scale,
                                         int causal, int *sched, int *dev_status, int fault_cta,
                                         cudaStream_t stream) {
-  return launch_main<true>(tq64, tk, tv, tdo64, tdq, vecs, dk, dv, H, 0, scale, causal, sched,
+  return launch_main<kPacked>(tq64, tk, tv, tdo64, tdq, vecs, dk, dv, H, 0, scale, causal, sched,
+                           fault_cta, dev_status, stream, tdk, tdv, pk);
+}
+
+cudaError_t launch_bwd_window_main_d128(const CUtensorMap &tq64, const CUtensorMap &tk,
+                                        const CUtensorMap &tv, const CUtensorMap &tdo64,
+                                        const CUtensorMap &tdq, const CUtensorMap &tdk,
+                                        const CUtensorMap &tdv, const float *vecs, void *dk,
+                                        void *dv, int H, const BwdWindow &pk, float scale,
+                                        int *sched, int *dev_status, int fault_cta,
+                                        cudaStream_t stream) {
+  return launch_main<kWindow>(tq64, tk, tv, tdo64, tdq, vecs, dk, dv, H, 0, scale, 1, sched,
                            fault_cta, dev_status, stream, tdk, tdv, pk);
 }
 

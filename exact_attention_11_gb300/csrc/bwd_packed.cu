@@ -26,6 +26,7 @@
 // accumulators fp32; each gradient once.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -53,7 +54,33 @@ struct SideArgs {
   __nv_bfloat16 *dq, *dk, *dv;
   int S, T, H, Hk, n_blocks;
   float scale;
+  // A window: the main kernel's query blocks per entry of the table, and their count.
+  int2 *range;
+  int *count;
+  int entries, split, window, sinks;
 };
+
+// A window: key block jb is seen by the query blocks from its own to `reach` further;
+// if it holds first tokens, by all later ones too, which are items of their own (entries
+// of kFar query blocks or more): one item of the whole sequence would end the call alone.
+constexpr int kFar = 8;
+__host__ __device__ __forceinline__ int reach(int window) {
+  return (BQ - 2 + window) / BQ;
+}
+__host__ __device__ __forceinline__ int far_steps(int window) {
+  const int r = reach(window) + 1;
+  return r > kFar ? r : kFar;
+}
+// Entries for the far query blocks of key block jb, of a sequence of `blocks`.
+__device__ __forceinline__ int far_entries(const SideArgs &a, int jb, int blocks) {
+  const int step = far_steps(a.window);
+  return jb * BQ < a.split ? (max(blocks - 1 - jb - reach(a.window), 0) + step - 1) / step : 0;
+}
+__device__ __forceinline__ int far_entries(const SideArgs &a, int blocks) {
+  int n = 0;
+  for (int jb = 0; jb < blocks && jb * BQ < a.split; ++jb) n += far_entries(a, jb, blocks);
+  return n;
+}
 
 __device__ __forceinline__ int first_block(const SideArgs &a, int s) {
   return clampi(a.cu_seqlens[s], 0, a.T) / BQ + s;
@@ -61,7 +88,7 @@ __device__ __forceinline__ int first_block(const SideArgs &a, int s) {
 
 // One block of 256 threads per (padded block, head); heads H .. H + Hk - 1
 // stand for the key/value heads' accumulators.
-template <int D>
+template <int D, bool WINDOW>
 __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
   // The main kernel may be scheduled once every block of this one has begun.
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -77,33 +104,74 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
     local = blk - begin / BQ - s;
   }
   const bool live = s >= 0 && local * BQ < n;
+  // A window: the entry's query blocks, up to the last that sees the key block (all
+  // of them, where it holds first tokens and nothing is split off).
+  auto put_range = [&](int at, int last) {
+    if (WINDOW) a.range[at] = make_int2(local, max(last - local + 1, 1));
+  };
+  const int blocks = (n + BQ - 1) / BQ;
+  const int last = WINDOW ? min(local + reach(a.window), blocks - 1) : 0;
   if (h == 0 && a.S > kSortedSeqs) {
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
       a.table[blk] = live ? make_int4(begin, n, blk - local, local) : make_int4(0, 0, 0, 0);
+      put_range(blk, local * BQ < a.sinks ? blocks - 1 : last);
+      if (WINDOW && blk == 0) *a.count = a.n_blocks;
+    }
   } else if (h == 0) {
     // The block's place in the table: behind the blocks of longer sequences (of
     // equal ones, those before it); an unused block, behind all used ones.
     int before = 0;
+    int used = 0, far_before = 0, far = 0;   // a window: entries of all sequences, far ones
     for (int j = threadIdx.x; j < a.S; j += 256) {
       const int b = clampi(a.cu_seqlens[j], 0, a.T);
       const int len = clampi(a.cu_seqlens[j + 1], b, a.T) - b;
       const int blocks = (len + BQ - 1) / BQ;
+      const bool longer = len > n || (len == n && j < s);
       if (live)
-        before += (len > n || (len == n && j < s)) ? blocks : 0;
+        before += longer ? blocks : 0;
       else   // all used blocks, less those numbered before this one
         before += blocks - clampi(blk - b / BQ - j, 0, blocks);
+      if (WINDOW) {
+        const int f = far_entries(a, blocks);
+        used += blocks, far += f, far_before += longer ? f : 0;
+      }
     }
-    __shared__ int sum[8];
+    auto add_up = [&](int x, int *sum) {
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) before += __shfl_xor_sync(~0u, before, off);
-    if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = before;
+      for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(~0u, x, off);
+      if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = x;
+    };
+    __shared__ int sum[WINDOW ? 32 : 8];
+    add_up(before, sum);
+    if constexpr (WINDOW) add_up(used, sum + 8), add_up(far_before, sum + 16), add_up(far, sum + 24);
     __syncthreads();
     if (threadIdx.x == 0) {
-      before = 0;
-      for (int u = 0; u < 8; ++u) before += sum[u];
+      auto total = [&](const int *x) {
+        int n = 0;
+        for (int u = 0; u < 8; ++u) n += x[u];
+        return n;
+      };
+      before = total(sum);
       // (Offsets that decrease may lead anywhere: stay inside the table.)
       const int at = clampi(live ? before + local : before + blk, 0, a.n_blocks - 1);
-      a.table[at] = live ? make_int4(begin, n, blk - local, local) : make_int4(0, 0, 0, 0);
+      if (!WINDOW || live)
+        a.table[at] = live ? make_int4(begin, n, blk - local, local) : make_int4(0, 0, 0, 0);
+      if constexpr (WINDOW) {
+        // The used entries come first, then the far ones.
+        used = total(sum + 8);
+        if (blk == 0) *a.count = min(used + total(sum + 24), a.entries);
+        if (live) {
+          put_range(at, local * BQ < a.sinks && a.split == 0 ? blocks - 1 : last);
+          int to = used + total(sum + 16);
+          for (int jb = 0; jb < local; ++jb) to += far_entries(a, jb, blocks);
+          const int step = far_steps(a.window), n_far = far_entries(a, local, blocks);
+          for (int f = 0; f < n_far; ++f) {
+            const int first = last + 1 + f * step, x = clampi(to + f, 0, a.entries - 1);
+            a.table[x] = make_int4(begin, n, blk - local, local);
+            a.range[x] = make_int2(first, min(step, blocks - first));
+          }
+        }
+      }
     }
   }
   if (!live) return;
@@ -112,6 +180,7 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
   const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
   constexpr int kRounds = BQ / kRows;
   if (h >= a.H) {
+    if (WINDOW && a.H == a.Hk && local * BQ >= a.split) return;   // stored, not added up
 #pragma unroll
     for (int u = 0; u < kRounds; ++u) {
       const int64_t at =
@@ -163,7 +232,7 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
 }
 
 // One block per token: its rows of every head, eight values a thread.
-template <int D>
+template <int D, bool WINDOW>
 __global__ void __launch_bounds__(256) packed_out_kernel(const SideArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int L = D / 8;
@@ -174,7 +243,9 @@ __global__ void __launch_bounds__(256) packed_out_kernel(const SideArgs a) {
   const int begin = clampi(a.cu_seqlens[s], 0, a.T);
   const int64_t rows = static_cast<int64_t>(a.n_blocks) * BQ;
   const int64_t acc_row = static_cast<int64_t>(begin / BQ + s) * BQ + tok - begin;
-  const int n = (a.H + (a.dk_acc != nullptr ? 2 * a.Hk : 0)) * L;
+  bool shared = a.dk_acc != nullptr;
+  if (WINDOW && a.H == a.Hk) shared = shared && (tok - begin) / BQ * BQ < a.split;
+  const int n = (a.H + (shared ? 2 * a.Hk : 0)) * L;
   for (int i = threadIdx.x; i < n; i += 256) {
     int h = i / L;
     const int c = i % L * 8;
@@ -199,23 +270,32 @@ __global__ void __launch_bounds__(256) packed_out_kernel(const SideArgs a) {
   }
 }
 
-template <int D>
+template <int D, bool WINDOW>
 cudaError_t launch_d(const PackedGradMaps &m, const PackedGrad &p, const SideArgs &a, int *sched,
                      int *dev_status, int fault_cta, cudaStream_t stream) {
   const int heads = p.H + (a.dk_acc != nullptr ? p.Hk : 0);
-  packed_prep_kernel<D><<<static_cast<unsigned>(a.n_blocks * heads), 256, 0, stream>>>(a);
+  packed_prep_kernel<D, WINDOW><<<static_cast<unsigned>(a.n_blocks * heads), 256, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  BwdPacked pk;
+  BwdWindow pk;
   pk.table = a.table;
   pk.tokens = a.T;
   pk.sorted = a.S <= kSortedSeqs;
   pk.n_blocks = a.n_blocks;
   pk.group = p.H / p.Hk;
   pk.kv_heads = p.Hk;
-  auto main_kernel = D == 128 ? launch_bwd_packed_main_d128 : launch_bwd_packed_main_d64;
-  e = main_kernel(m.q, m.k, m.v, m.dout, m.dq_acc, m.dk_acc, m.dv_acc, a.vecs, p.dk, p.dv, p.H, pk,
-                  p.scale, p.causal, sched, dev_status, fault_cta, stream);
+  if (WINDOW) {
+    pk.sorted = 0;   // (an entry of length 0 does not end it: the count does)
+    pk.range = a.range, pk.count = a.count, pk.entries = a.entries, pk.split = a.split;
+    pk.window = a.window, pk.sinks = a.sinks;
+    auto main_kernel = D == 128 ? launch_bwd_window_main_d128 : launch_bwd_window_main_d64;
+    e = main_kernel(m.q, m.k, m.v, m.dout, m.dq_acc, m.dk_acc, m.dv_acc, a.vecs, p.dk, p.dv, p.H,
+                    pk, p.scale, sched, dev_status, fault_cta, stream);
+  } else {
+    auto main_kernel = D == 128 ? launch_bwd_packed_main_d128 : launch_bwd_packed_main_d64;
+    e = main_kernel(m.q, m.k, m.v, m.dout, m.dq_acc, m.dk_acc, m.dv_acc, a.vecs, p.dk, p.dv, p.H,
+                    pk, p.scale, p.causal, sched, dev_status, fault_cta, stream);
+  }
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.T));
@@ -226,35 +306,46 @@ cudaError_t launch_d(const PackedGradMaps &m, const PackedGrad &p, const SideArg
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, packed_out_kernel<D>, a);
+  return cudaLaunchKernelEx(&cfg, packed_out_kernel<D, WINDOW>, a);
 }
 
 }  // namespace
 
-PackedGradLayout packed_grad_layout(int T, int S, int H, int Hk, int d) {
-  PackedGradLayout l;
+PackedGradLayout packed_grad_layout(int T, int S, int H, int Hk, int d, int window, int sinks) {
+  PackedGradLayout l{};
   l.n_blocks = T / BQ + S;
+  l.entries = l.n_blocks;
+  // Up to eight blocks of first tokens are split: with more there are items enough, and
+  // their far parts would fill the table.  Only the longest sequences have far parts.
+  if (window > 0 && window < T && S <= kSortedSeqs && sinks <= 8 * BQ) {
+    l.split = sinks;
+    const long long most = T / (BQ * (reach(window) + 1)) + 1;   // sequences with far parts
+    l.entries += (sinks + BQ - 1) / BQ * (T / (BQ * far_steps(window)) + 2 * std::min<long long>(S, most) + 1);
+  }
+  l.shared = H != Hk || l.split > 0;
   const size_t rows = static_cast<size_t>(l.n_blocks) * BQ;
-  const size_t shared = H != Hk ? rows * Hk * d : 0;
+  const size_t shared = l.shared ? rows * Hk * d : 0;
   l.dk_acc = rows * H * d;
   l.dv_acc = l.dk_acc + shared;
   l.vecs = l.dv_acc + shared;
   l.table = l.vecs + static_cast<size_t>(l.n_blocks) * H * 2 * BQ;
-  l.bytes = sizeof(float) * (l.table + static_cast<size_t>(l.n_blocks) * 4);
+  l.range = l.table + static_cast<size_t>(l.entries) * 4;
+  l.count = l.range + (window > 0 ? static_cast<size_t>(l.entries) * 2 : 0);
+  l.bytes = sizeof(float) * (l.count + (window > 0 ? 1 : 0));
   return l;
 }
 
 cudaError_t launch_bwd_packed(const PackedGradMaps &m, const PackedGrad &p, float *ws, int *sched,
                               int *dev_status, int fault_cta, cudaStream_t stream) {
-  const PackedGradLayout l = packed_grad_layout(p.T, p.S, p.H, p.Hk, p.d);
+  const PackedGradLayout l = packed_grad_layout(p.T, p.S, p.H, p.Hk, p.d, p.window, p.sinks);
   SideArgs a{};
   a.o = static_cast<const __nv_bfloat16 *>(p.o);
   a.dout = static_cast<const __nv_bfloat16 *>(p.dout);
   a.lse = p.lse;
   a.cu_seqlens = p.cu_seqlens;
   a.dq_acc = ws;
-  a.dk_acc = p.H != p.Hk ? ws + l.dk_acc : nullptr;
-  a.dv_acc = p.H != p.Hk ? ws + l.dv_acc : nullptr;
+  a.dk_acc = l.shared ? ws + l.dk_acc : nullptr;
+  a.dv_acc = l.shared ? ws + l.dv_acc : nullptr;
   a.vecs = ws + l.vecs;
   a.table = reinterpret_cast<int4 *>(ws + l.table);
   a.dq = static_cast<__nv_bfloat16 *>(p.dq);
@@ -262,8 +353,16 @@ cudaError_t launch_bwd_packed(const PackedGradMaps &m, const PackedGrad &p, floa
   a.dv = static_cast<__nv_bfloat16 *>(p.dv);
   a.S = p.S, a.T = p.T, a.H = p.H, a.Hk = p.Hk, a.n_blocks = l.n_blocks;
   a.scale = p.scale;
-  return p.d == 128 ? launch_d<128>(m, p, a, sched, dev_status, fault_cta, stream)
-                    : launch_d<64>(m, p, a, sched, dev_status, fault_cta, stream);
+  if (p.window > 0) {
+    a.range = reinterpret_cast<int2 *>(ws + l.range);
+    a.count = reinterpret_cast<int *>(ws + l.count);
+    a.entries = static_cast<int>(l.entries), a.split = l.split;
+    a.window = p.window, a.sinks = p.sinks;
+    return p.d == 128 ? launch_d<128, true>(m, p, a, sched, dev_status, fault_cta, stream)
+                      : launch_d<64, true>(m, p, a, sched, dev_status, fault_cta, stream);
+  }
+  return p.d == 128 ? launch_d<128, false>(m, p, a, sched, dev_status, fault_cta, stream)
+                    : launch_d<64, false>(m, p, a, sched, dev_status, fault_cta, stream);
 }
 
 }  // namespace fattn

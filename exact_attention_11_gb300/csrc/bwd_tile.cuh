@@ -18,13 +18,14 @@ constexpr int kSubQ = 64;   // queries per sub-tile
 // P^T and dS^T of one 32-query chunk (columns ch*32 .. +31 of the sub-tile)
 // for this lane's key row r.  vec holds [-LSE2 x 64 | -D x 64]; c2 =
 // scale*log2e in both halves.  Returns both as packed bf16 pairs and stores
-// dS^T row r to shared memory (128-byte swizzle).  With MASKED, P = 0 for
+// dS^T row r to shared memory (128-byte swizzle).  With MASKED = 1, P = 0 for
 // keys >= N and, when diag (the causal diagonal block), for keys later than
-// the query.
-template <bool MASKED>
+// the query; with MASKED = 2, for the queries whose bit in `see` (of the
+// sub-tile's 64) is 0.
+template <int MASKED>
 __device__ __forceinline__ void chunk(uint32_t R, int ch, const float *vec, uint8_t *ds_buf, int r,
-                                      int key, int q0, int N, bool diag, uint64_t c2,
-                                      uint32_t (&pk)[16], uint32_t (&dsk)[16]) {
+                                      int key, int q0, int N, bool diag, uint64_t see,
+                                      uint64_t c2, uint32_t (&pk)[16], uint32_t (&dsk)[16]) {
   uint32_t sv[32], dp[32];
   tmem_ld32(R + ch * 32, sv);
   tmem_ld32(R + 64 + ch * 32, dp);
@@ -40,10 +41,16 @@ __device__ __forceinline__ void chunk(uint32_t R, int ch, const float *vec, uint
     const float2 x23 = f2_split(ffma2(f2(__uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3])),
                                       c2, nl.y));
     float p[4] = {ex2_approx(x01.x), ex2_approx(x01.y), ex2_approx(x23.x), ex2_approx(x23.y)};
-    if (MASKED) {
+    if (MASKED == 1) {
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         if (key >= N || (diag && key > q0 + ch * 32 + e + u)) p[u] = 0.f;
+    }
+    if (MASKED == 2) {
+      const uint32_t bits = static_cast<uint32_t>(see >> (32 * ch));
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (((bits >> (e + u)) & 1u) == 0u) p[u] = 0.f;
     }
     const uint64_t p01 = f2(p[0], p[1]), p23 = f2(p[2], p[3]);
     const float2 g01 = f2_split(fmul2(
@@ -70,16 +77,26 @@ __device__ __forceinline__ void chunk(uint32_t R, int ch, const float *vec, uint
 // packed bf16 pairs (queries 2c, 2c+1 in column c): chunk 1 (S columns 32-63)
 // goes first so that dS^T of chunk 1 may overwrite S columns 48-63 at once;
 // P^T of chunk 1 waits in registers until chunk 0 has read columns 0-31.
-template <bool MASKED>
+template <int MASKED>
 __device__ __forceinline__ void chunks(uint32_t R, const float *vec, uint8_t *ds_buf, int r,
-                                       int key, int q0, int N, bool diag, uint64_t c2) {
+                                       int key, int q0, int N, bool diag, uint64_t see,
+                                       uint64_t c2) {
   uint32_t pk1[16], dsk1[16], pk0[16], dsk0[16];
-  chunk<MASKED>(R, 1, vec, ds_buf, r, key, q0, N, diag, c2, pk1, dsk1);
+  chunk<MASKED>(R, 1, vec, ds_buf, r, key, q0, N, diag, see, c2, pk1, dsk1);
   tmem_st16(R + 48, dsk1);
-  chunk<MASKED>(R, 0, vec, ds_buf, r, key, q0, N, diag, c2, pk0, dsk0);
+  chunk<MASKED>(R, 0, vec, ds_buf, r, key, q0, N, diag, see, c2, pk0, dsk0);
   tmem_st16(R + 0, pk0);
   tmem_st16(R + 16, pk1);
   tmem_st16(R + 32, dsk0);
+}
+
+// Bits of the sub-tile's 64 queries q0 .. q0 + 63 that see `key`: those from the key
+// on, the next `window` of them only unless the key is one of the first `sinks`.
+__device__ __forceinline__ uint64_t near_queries(int key, int q0, int N, int window, int sinks) {
+  const int lo = min(max(key - q0, 0), kSubQ);
+  const int hi = key >= N ? 0 : key < sinks ? kSubQ : min(max(key - q0 + window, 0), kSubQ);
+  const uint64_t below = hi >= kSubQ ? ~0ull : (1ull << hi) - 1;
+  return lo >= kSubQ ? 0ull : below & (~0ull << lo);
 }
 
 }  // namespace bwd_tile

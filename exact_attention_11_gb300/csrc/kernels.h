@@ -113,6 +113,14 @@ struct BwdPacked {
   const int4 *table;
   int n_blocks, group, kv_heads, tokens, sorted;
 };
+// With a window: `count` entries (of at most `entries`) are used, each with the query
+// blocks that its item visits (first, number) in `range`.  The key blocks that begin
+// below `split` are in several items, which add dK and dV to the accumulators.
+struct BwdWindow : BwdPacked {
+  const int2 *range;
+  const int *count;
+  int entries, split, window, sinks;
+};
 cudaError_t launch_bwd_packed_main_d128(const CUtensorMap &tq64, const CUtensorMap &tk,
                                         const CUtensorMap &tv, const CUtensorMap &tdo64,
                                         const CUtensorMap &tdq, const CUtensorMap &tdk,
@@ -126,6 +134,21 @@ cudaError_t launch_bwd_packed_main_d64(const CUtensorMap &tq64, const CUtensorMa
                                        const CUtensorMap &tdv, const float *vecs, void *dk,
                                        void *dv, int H, const BwdPacked &pk, float scale,
                                        int causal, int *sched, int *dev_status, int fault_cta,
+                                       cudaStream_t stream);
+
+cudaError_t launch_bwd_window_main_d128(const CUtensorMap &tq64, const CUtensorMap &tk,
+                                        const CUtensorMap &tv, const CUtensorMap &tdo64,
+                                        const CUtensorMap &tdq, const CUtensorMap &tdk,
+                                        const CUtensorMap &tdv, const float *vecs, void *dk,
+                                        void *dv, int H, const BwdWindow &pk, float scale,
+                                        int *sched, int *dev_status, int fault_cta,
+                                        cudaStream_t stream);
+cudaError_t launch_bwd_window_main_d64(const CUtensorMap &tq64, const CUtensorMap &tk,
+                                       const CUtensorMap &tv, const CUtensorMap &tdo64,
+                                       const CUtensorMap &tdq, const CUtensorMap &tdk,
+                                       const CUtensorMap &tdv, const float *vecs, void *dk,
+                                       void *dv, int H, const BwdWindow &pk, float scale,
+                                       int *sched, int *dev_status, int fault_cta,
                                        cudaStream_t stream);
 
 int decode_max_parts(int max_num_blocks_per_seq);
@@ -219,13 +242,16 @@ cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
 
 // Gradients of the packed forward (bwd_packed.cu).  Workspace, in floats from
 // its start: the dQ accumulator [H][n_blocks * 128][d], those of dK and dV
-// [Hk][..][d] (where heads share them), [-LSE2 | -D] per head and block, the
-// block table.
+// [Hk][..][d] (where several items add to them), [-LSE2 | -D] per head and block,
+// the block table (`entries` of 4; with a window, of 2 more, then their count).
 struct PackedGradLayout {
-  int n_blocks;
-  size_t dk_acc, dv_acc, vecs, table, bytes;
+  int n_blocks, split;        // split: see BwdWindow
+  long long entries;
+  bool shared;                // there are dK and dV accumulators
+  size_t dk_acc, dv_acc, vecs, table, range, count, bytes;
 };
-PackedGradLayout packed_grad_layout(int T, int S, int H, int Hk, int d);
+PackedGradLayout packed_grad_layout(int T, int S, int H, int Hk, int d, int window = 0,
+                                    int sinks = 0);
 // q, dout: maps {d, T, H} with boxes of 64 x bwd_qdo_box_rows(d) x 1; k, v
 // {d, T, Hk}, 64 x 128 x 1; the accumulators' fp32 maps as for launch_bwd_bf16.
 struct PackedGradMaps {
@@ -238,6 +264,7 @@ struct PackedGrad {
   const int *cu_seqlens;
   int S, T, H, Hk, d, causal;
   float scale;
+  int window, sinks;          // as in PackedProblem
 };
 cudaError_t launch_bwd_packed(const PackedGradMaps &m, const PackedGrad &p, float *ws, int *sched,
                               int *dev_status, int fault_cta, cudaStream_t stream);

@@ -632,6 +632,25 @@ int fa_forward_packed_window_f16(const void *q, const void *k, const void *v, vo
                                  int sinks, fa_stream_t stream);
 
 /*
+ * fa_backward_packed_window -- gradients of fa_forward_packed_window (bf16): those of
+ * fa_backward_packed, restricted to the pairs that the mask leaves.  o and lse are what
+ * fa_forward_packed_window returned for the same inputs, window and sinks; the workspace
+ * has at least fa_backward_packed_window_workspace_bytes bytes.  dK and dV of the blocks
+ * of 128 keys that hold first tokens are summed in fp32 with atomic adds too (all others
+ * as in fa_backward_packed), up to sinks = 1024.
+ */
+unsigned long long fa_backward_packed_window_workspace_bytes(int num_seqs, int total_tokens,
+                                                             int num_heads, int num_kv_heads,
+                                                             int d, int window, int sinks);
+int fa_backward_packed_window(const void *q, const void *k, const void *v, const void *o,
+                              const void *dout, const float *lse, void *dq, void *dk, void *dv,
+                              const int *cu_seqlens, int num_seqs, int total_tokens,
+                              int num_heads, int num_kv_heads, int d, long long q_stride,
+                              long long k_stride, long long v_stride, float scale, int window,
+                              int sinks, void *workspace, unsigned long long workspace_bytes,
+                              fa_stream_t stream);
+
+/*
  * fa_paged_prefill_window -- fa_paged_prefill with this mask: chunks of any length,
  * single tokens included, over the paged cache.  Query i of sequence s has position
  * context_lens[s] - n + i; positions before 0 (a context shorter than its chunk) see
