@@ -37,6 +37,8 @@ __all__ = ["fa_forward", "fa_forward_f16", "fa_forward_masked", "forward_masked"
            "fa_backward_packed_window_workspace_bytes", "backward_packed_window",
            "fa_paged_prefill_window",
            "fa_paged_prefill_window_workspace_bytes", "paged_prefill_window",
+           "fa_paged_prefill_shared", "fa_paged_prefill_shared_workspace_bytes",
+           "paged_prefill_shared",
            "fa_device_status", "fa_release", "forward", "paged_decode", "FattnError",
            "library_path", "load"]
 
@@ -105,6 +107,9 @@ EXPORTS = {
     "fa_paged_prefill_window_workspace_bytes": ([_i] * 7, ctypes.c_ulonglong),
     "fa_paged_prefill_window": ([_vp] * 7 + [_i] * 8 + [_ll, _f, _i, _i, _vp, ctypes.c_ulonglong,
                                                         _vp], _i),
+    "fa_paged_prefill_shared_workspace_bytes": ([_i] * 6, ctypes.c_ulonglong),
+    "fa_paged_prefill_shared": ([_vp] * 9 + [_i] * 9 + [_ll, _f, _vp, ctypes.c_ulonglong, _vp],
+                                _i),
     "fa_status_string": ([_i], ctypes.c_char_p),
     "fa_device_status": ([], _i),
     "fa_release": ([], None),
@@ -359,6 +364,23 @@ def fa_paged_prefill_window(q, k_cache, v_cache, block_tables, context_lens, cu_
         q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out, num_seqs, total_tokens,
         num_heads, num_kv_heads, head_size, block_size, num_blocks, max_num_blocks_per_seq,
         q_stride, scale, window, sinks, workspace, workspace_bytes, stream))
+
+
+def fa_paged_prefill_shared_workspace_bytes(num_seqs, total_tokens, num_groups, num_heads,
+                                            num_kv_heads, max_num_blocks_per_seq) -> int:
+    return int(load().fa_paged_prefill_shared_workspace_bytes(
+        num_seqs, total_tokens, num_groups, num_heads, num_kv_heads, max_num_blocks_per_seq))
+
+
+def fa_paged_prefill_shared(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens,
+                            cu_groups, prefix_lens, out, num_seqs, total_tokens, num_groups,
+                            num_heads, num_kv_heads, head_size, block_size, num_blocks,
+                            max_num_blocks_per_seq, q_stride, scale, workspace, workspace_bytes,
+                            stream) -> int:
+    return _check("fa_paged_prefill_shared", load().fa_paged_prefill_shared(
+        q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, cu_groups, prefix_lens, out,
+        num_seqs, total_tokens, num_groups, num_heads, num_kv_heads, head_size, block_size,
+        num_blocks, max_num_blocks_per_seq, q_stride, scale, workspace, workspace_bytes, stream))
 
 
 def fa_status_string(status: int) -> str:
@@ -978,8 +1000,40 @@ def paged_prefill_window(q, k_cache, v_cache, block_tables, context_lens, cu_seq
                           *_window_args(window, sinks))
 
 
-def _paged_prefill(name, q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, scale, out,
-                   workspace, *mask):
+@_on_device
+def paged_prefill_shared(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, cu_groups,
+                         prefix_lens, scale=None, out=None, workspace=None):
+    """``paged_prefill`` for sequences that share the cache blocks of a long prefix,
+    which is read once for a whole group: sequences cu_groups[g] ..
+    cu_groups[g+1] - 1 (int32 [groups + 1] on the device) have the same first
+    prefix_lens[g] tokens (int32 [groups]; rounded down to whole blocks), in the
+    blocks that each of their rows of ``block_tables`` begins with (not checked).
+    The output is that of ``paged_prefill`` for the same tables, up to the order of
+    fp32 sums; a sequence whose new tokens do not all lie behind the prefix shares
+    nothing.  ``workspace`` (optional) is a CUDA tensor of at least
+    ``fa_paged_prefill_shared_workspace_bytes`` bytes."""
+    torch = _torch()
+    T, H, Hk, S, mb, nb, bs, dev, qs, scale, out, ptrs, out_ptr = _chunk_args(
+        q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, scale, out)
+    P = prefix_lens.numel()
+    groups = (_dense("cu_groups", cu_groups, torch.int32, dev, P + 1),
+              _dense("prefix_lens", prefix_lens, torch.int32, dev))
+    if T == 0 or S == 0:
+        return out
+    lib = _lib or load()
+    if workspace is not None:
+        nbytes = _workspace(workspace, dev)
+    else:
+        nbytes = lib.fa_paged_prefill_shared_workspace_bytes(S, T, P, H, Hk, mb)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    _check("fa_paged_prefill_shared", lib.fa_paged_prefill_shared(
+        *ptrs, *groups, out_ptr, S, T, P, H, Hk, q.shape[2], bs, nb, mb, qs, scale,
+        workspace.data_ptr(), nbytes, _raw_stream(dev)))
+    return out
+
+
+def _chunk_args(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, scale, out):
+    """Checks what the chunk helpers share and makes the output."""
     torch = _torch()
     T, H, D = q.shape
     dtype, dev = q.dtype, q.get_device()
@@ -1001,6 +1055,13 @@ def _paged_prefill(name, q, k_cache, v_cache, block_tables, context_lens, cu_seq
     if out is None:
         out = torch.empty((T, H, D), dtype=dtype, device=q.device)
     out_ptr = _dense("out", out, dtype, dev, T * H * D)
+    return T, H, Hk, S, mb, nb, bs, dev, qs, scale, out, ptrs, out_ptr
+
+
+def _paged_prefill(name, q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, scale, out,
+                   workspace, *mask):
+    T, H, Hk, S, mb, nb, bs, dev, qs, scale, out, ptrs, out_ptr = _chunk_args(
+        q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, scale, out)
     if T == 0 or S == 0:
         return out
     lib = _lib or load()
@@ -1009,8 +1070,8 @@ def _paged_prefill(name, q, k_cache, v_cache, block_tables, context_lens, cu_seq
     else:
         nbytes = getattr(lib, name + "_workspace_bytes")(S, T, H, Hk, mb, *mask)
         if nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            workspace = _torch().empty(nbytes, dtype=_torch().uint8, device=q.device)
     _check(name, getattr(lib, name)(
-        *ptrs, out_ptr, S, T, H, Hk, D, bs, nb, mb, qs, scale, *mask, _ptr(workspace), nbytes,
+        *ptrs, out_ptr, S, T, H, Hk, q.shape[2], bs, nb, mb, qs, scale, *mask, _ptr(workspace), nbytes,
         _raw_stream(dev)))
     return out

@@ -1040,17 +1040,16 @@ unsigned long long fa_paged_prefill_workspace_bytes(int num_seqs, int total_toke
 }
 
 namespace {
-int paged_prefill(const void *q, const void *k_cache, const void *v_cache,
-                  const int *block_tables, const int *context_lens, const int *cu_seqlens,
-                  void *out, int num_seqs, int total_tokens, int num_heads, int num_kv_heads,
-                  int head_size, int block_size, int num_blocks, int max_num_blocks_per_seq,
-                  long long q_stride, float scale, const Visible &see, void *workspace,
-                  unsigned long long workspace_bytes, fa_stream_t stream) {
+// Checks shared by the chunk calls over the paged cache.
+int check_chunks(const void *q, const void *k_cache, const void *v_cache, const int *block_tables,
+                 const int *context_lens, const int *cu_seqlens, const void *out, int num_seqs,
+                 int total_tokens, int num_heads, int num_kv_heads, int head_size, int block_size,
+                 int num_blocks, int max_num_blocks_per_seq, long long q_stride, float scale) {
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !cu_seqlens || !out)
     return FA_ERR_INVALID_ARG;
   if (num_blocks <= 0 || max_num_blocks_per_seq <= 0) return FA_ERR_INVALID_ARG;
   if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
-  int rc = check_packed_sizes(num_seqs, total_tokens, num_heads, num_kv_heads);
+  const int rc = check_packed_sizes(num_seqs, total_tokens, num_heads, num_kv_heads);
   if (rc != FA_OK) return rc;
   if (head_size != fattn::kDecodeHeadSize || block_size != fattn::kDecodeBlockSize)
     return FA_ERR_UNSUPPORTED;
@@ -1058,26 +1057,48 @@ int paged_prefill(const void *q, const void *k_cache, const void *v_cache,
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
       !aligned_to(block_tables, 4) || !aligned_to(context_lens, 4) || !aligned_to(cu_seqlens, 4))
     return FA_ERR_ALIGNMENT;
-  if ((rc = check_token_stride(q_stride, num_heads, head_size, 2)) != FA_OK) return rc;
+  return check_token_stride(q_stride, num_heads, head_size, 2);
+}
+
+int check_workspace(const void *workspace, unsigned long long bytes, size_t need) {
+  if (need == 0) return FA_OK;
+  if (!workspace || bytes < need) return FA_ERR_INVALID_ARG;
+  return aligned16(workspace) ? FA_OK : FA_ERR_ALIGNMENT;
+}
+
+// The tensor maps of a chunk call.
+int encode_chunk_maps(CUtensorMap *tq, CUtensorMap *tk, CUtensorMap *tv, const void *q,
+                      const void *k_cache, const void *v_cache, int T, int H, int Hk,
+                      int num_blocks, long long q_stride) {
+  const int group = H / Hk;
+  const int rc = encode_rows_map(tq, q, T, H, fattn::kDecodeHeadSize, q_stride, false, group,
+                                 fattn::packed_tile_tokens(group),
+                                 CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+  return rc != FA_OK ? rc : encode_paged_kv_maps(tk, tv, k_cache, v_cache, Hk, num_blocks, true);
+}
+
+int paged_prefill(const void *q, const void *k_cache, const void *v_cache,
+                  const int *block_tables, const int *context_lens, const int *cu_seqlens,
+                  void *out, int num_seqs, int total_tokens, int num_heads, int num_kv_heads,
+                  int head_size, int block_size, int num_blocks, int max_num_blocks_per_seq,
+                  long long q_stride, float scale, const Visible &see, void *workspace,
+                  unsigned long long workspace_bytes, fa_stream_t stream) {
+  int rc = check_chunks(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out, num_seqs,
+                        total_tokens, num_heads, num_kv_heads, head_size, block_size, num_blocks,
+                        max_num_blocks_per_seq, q_stride, scale);
+  if (rc != FA_OK) return rc;
   if (num_seqs == 0 || total_tokens == 0) return FA_OK;
-  const size_t need = fattn::paged_prefill_workspace_bytes(total_tokens, num_seqs, num_heads,
-                                                           num_kv_heads, max_num_blocks_per_seq,
-                                                           see.window, see.sinks);
-  if (need > 0) {
-    if (!workspace || workspace_bytes < need) return FA_ERR_INVALID_ARG;
-    if (!aligned16(workspace)) return FA_ERR_ALIGNMENT;
-  }
+  rc = check_workspace(workspace, workspace_bytes,
+                       fattn::paged_prefill_workspace_bytes(total_tokens, num_seqs, num_heads,
+                                                            num_kv_heads, max_num_blocks_per_seq,
+                                                            see.window, see.sinks));
+  if (rc != FA_OK) return rc;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int *sched = nullptr, *status = nullptr, fault_cta = -1;
   if ((rc = acquire_sched(s, 1, &sched, &status, &fault_cta)) != FA_OK) return rc;
-  const int group = num_heads / num_kv_heads;
   CUtensorMap tq, tk, tv;
-  if ((rc = encode_rows_map(&tq, q, total_tokens, num_heads, head_size, q_stride, false, group,
-                            fattn::packed_tile_tokens(group),
-                            CU_TENSOR_MAP_DATA_TYPE_BFLOAT16)) != FA_OK)
-    return rc;
-  if ((rc = encode_paged_kv_maps(&tk, &tv, k_cache, v_cache, num_kv_heads, num_blocks,
-                                 true)) != FA_OK)
+  if ((rc = encode_chunk_maps(&tq, &tk, &tv, q, k_cache, v_cache, total_tokens, num_heads,
+                              num_kv_heads, num_blocks, q_stride)) != FA_OK)
     return rc;
   fattn::PackedProblem p{};
   p.o = out, p.cu_seqlens = cu_seqlens, p.context_lens = context_lens;
@@ -1129,6 +1150,58 @@ int fa_paged_prefill_window(const void *q, const void *k_cache, const void *v_ca
                        total_tokens, num_heads, num_kv_heads, head_size, block_size, num_blocks,
                        max_num_blocks_per_seq, q_stride, scale, see, workspace, workspace_bytes,
                        stream);
+}
+
+unsigned long long fa_paged_prefill_shared_workspace_bytes(int num_seqs, int total_tokens,
+                                                           int num_groups, int num_heads,
+                                                           int num_kv_heads,
+                                                           int max_num_blocks_per_seq) {
+  if (num_seqs <= 0 || total_tokens <= 0 || max_num_blocks_per_seq <= 0) return 0;
+  if (num_groups < 0 || num_groups > fattn::kSharedMaxGroups) return 0;
+  if (check_packed_sizes(num_seqs, total_tokens, num_heads, num_kv_heads) != FA_OK) return 0;
+  return static_cast<unsigned long long>(fattn::shared_layout(total_tokens, num_seqs, num_groups,
+                                                              num_heads, num_kv_heads,
+                                                              max_num_blocks_per_seq)
+                                             .bytes);
+}
+
+int fa_paged_prefill_shared(const void *q, const void *k_cache, const void *v_cache,
+                            const int *block_tables, const int *context_lens,
+                            const int *cu_seqlens, const int *cu_groups, const int *prefix_lens,
+                            void *out, int num_seqs, int total_tokens, int num_groups,
+                            int num_heads, int num_kv_heads, int head_size, int block_size,
+                            int num_blocks, int max_num_blocks_per_seq, long long q_stride,
+                            float scale, void *workspace, unsigned long long workspace_bytes,
+                            fa_stream_t stream) {
+  if (num_groups < 0 || (num_groups > 0 && (!cu_groups || !prefix_lens))) return FA_ERR_INVALID_ARG;
+  int rc = check_chunks(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out, num_seqs,
+                        total_tokens, num_heads, num_kv_heads, head_size, block_size, num_blocks,
+                        max_num_blocks_per_seq, q_stride, scale);
+  if (rc != FA_OK) return rc;
+  if (num_groups > fattn::kSharedMaxGroups) return FA_ERR_UNSUPPORTED;
+  if (!aligned_to(cu_groups, 4) || !aligned_to(prefix_lens, 4)) return FA_ERR_ALIGNMENT;
+  if (num_seqs == 0 || total_tokens == 0) return FA_OK;
+  rc = check_workspace(workspace, workspace_bytes,
+                       fattn::shared_layout(total_tokens, num_seqs, num_groups, num_heads,
+                                            num_kv_heads, max_num_blocks_per_seq)
+                           .bytes);
+  if (rc != FA_OK) return rc;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int *sched = nullptr, *status = nullptr, fault_cta = -1;
+  if ((rc = acquire_sched(s, 1, &sched, &status, &fault_cta)) != FA_OK) return rc;
+  CUtensorMap tq, tk, tv;
+  if ((rc = encode_chunk_maps(&tq, &tk, &tv, q, k_cache, v_cache, total_tokens, num_heads,
+                              num_kv_heads, num_blocks, q_stride)) != FA_OK)
+    return rc;
+  fattn::PackedProblem p{};
+  p.o = out, p.cu_seqlens = cu_seqlens, p.context_lens = context_lens;
+  p.block_tables = block_tables;
+  p.S = num_seqs, p.T = total_tokens, p.H = num_heads, p.Hk = num_kv_heads;
+  p.max_blocks = max_num_blocks_per_seq, p.num_blocks = num_blocks, p.scale = scale;
+  p.causal = 1;
+  return cuda_status(fattn::launch_paged_shared(tq, tk, tv, p, cu_groups, prefix_lens, num_groups,
+                                                static_cast<char *>(workspace), sched, status,
+                                                fault_cta, s));
 }
 
 int fa_device_status(void) {

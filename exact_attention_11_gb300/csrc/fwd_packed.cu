@@ -60,6 +60,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -167,8 +168,9 @@ static_assert(8 * kNumBars + sizeof(Misc) <= kBarArea, "barrier area");
 constexpr int kDevBadSmemBase = -2;
 
 // What a query sees: all keys of its sequence up to its own (or, packed, all of
-// them); or of those a window and the sequence's first tokens.
-enum : int { kAll = 0, kWindow = 1 };
+// them); or of those a window and the sequence's first tokens; or all of them where
+// groups of sequences share the blocks of a prefix (paged).
+enum : int { kAll = 0, kWindow = 1, kShared = 2 };
 
 struct Args {
   uint16_t *o;
@@ -188,8 +190,23 @@ struct Args {
 struct WindowArgs : Args {
   int window, sinks;            // up to 2^30 each
 };
+// A prefix is walked once for all rows of its group: it and what each sequence has of
+// its own are items of their own, numbered by shared_plan_kernel, and their partial rows
+// lie in ws_o one behind the other, those of the prefix from partition n_split on.
+struct SharedArgs : Args {
+  const int *cu_groups, *prefix_lens;
+  int P, pre_split;             // groups; most partitions of a prefix
+  int *head;                    // number of entries of `first` and `rec`
+  int *first;                   // [entries + 1]: their first items, heaviest first
+  int4 *rec;                    // [entries][2]: begin, n, kv_len, pos;
+                                // table row, first table column, partitions, first ws_o partition
+                                // (or -1: rows are written directly)
+  int4 *seq;                    // [S][2]: begin, n, kv_len, pos (of the sequence's own keys);
+                                // partitions, those of the prefix (0: none), -, -
+};
 template <int FORM>
-using FormArgs = std::conditional_t<FORM == kWindow, WindowArgs, Args>;
+using FormArgs = std::conditional_t<FORM == kWindow, WindowArgs,
+                                    std::conditional_t<FORM == kShared, SharedArgs, Args>>;
 
 // Key tiles that `n` tokens, the last of which sees key `last` last, visit.
 __device__ __forceinline__ int tiles_for(int n, int last, int kv_len) {
@@ -265,14 +282,16 @@ __device__ __forceinline__ Work work_of(const FormArgs<FORM> &a, const Seq &q) {
 // blocks, of one key/value head.  Each block of the sequence cuts its own key tiles into
 // that many.  (Roundings are spelled out: the merge kernel has to reach the same
 // number.)
-__device__ __forceinline__ int parts_of(const Args &a, const Seq &q, int tiles, int64_t work) {
-  constexpr float kFixed = 2.5f, kRow = 0.02f, kLeast = 4.f;
-  if (a.n_split == 1) return 1;
+constexpr float kPartFixed = 2.5f, kPartRow = 0.02f;
+__device__ __forceinline__ int parts_of(const Args &a, const Seq &q, int tiles, int64_t work,
+                                        int most) {
+  constexpr float kFixed = kPartFixed, kRow = kPartRow, kLeast = 4.f;
+  if (most == 1) return 1;
   const float w = __fmul_rn(__ll2float_rn(work * a.Hk), 1.f / (152.f * 0.7f));
   const float c = __fmaf_rn(kRow, static_cast<float>(min(q.n, 2 * a.tpb) * a.G), kFixed);
   const float size = fmaxf(__fsqrt_rn(__fmul_rn(w, c)), kLeast);
   const float n = __fdiv_rn(static_cast<float>(tiles), size);
-  return n < 1.5f ? 1 : min(__float2int_ru(n), a.n_split);
+  return n < 1.5f ? 1 : min(__float2int_ru(n), most);
 }
 __device__ __forceinline__ int part_size(int total, int parts) {
   return max(1, (total + parts - 1) / parts);
@@ -306,7 +325,7 @@ __device__ __forceinline__ void number_items(const FormArgs<FORM> &a, Misc *m) {
   for (int i = lane; i < a.S; i += 32) {
     const Seq q = seq(i);
     const int tiles = work_of<FORM>(a, q).tiles;
-    const int parts = PAGED ? parts_of(a, q, tiles, work) : 1;
+    const int parts = PAGED ? parts_of(a, q, tiles, work, a.n_split) : 1;
     const int size = PAGED ? part_size(tiles, parts) : tiles;
     m->key[i] = min(size, (1 << 23) - 1) * 128 + i;
     m->n_parts[i] = static_cast<int16_t>(parts);
@@ -340,11 +359,42 @@ __device__ __forceinline__ void number_items(const FormArgs<FORM> &a, Misc *m) {
   __syncwarp();
 }
 
+// kShared: the numbered entries in global memory, by their sizes.
+__device__ __forceinline__ bool decode_shared(const SharedArgs &a, int w, Item &it, Gap &gap) {
+  const int at = warp_search(*a.head, w, [&](int i) { return a.first[i]; });
+  const int4 q = a.rec[2 * at], r = a.rec[2 * at + 1];
+  int blk = (w - a.first[at]) / a.Hk;
+  it.kvh = w - a.first[at] - blk * a.Hk;
+  const int x = blk / r.z, part = blk - x * r.z, tok0 = x * 2 * a.tpb;
+  it.live = 1;
+  it.row0 = q.x + tok0;
+  it.pos0 = q.w + tok0;
+  it.kv_len = q.z;
+  it.kv0 = r.x;
+  gap = {0, r.y};
+  int total[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    it.n_tok[t] = clampi(q.y - tok0 - t * a.tpb, 0, a.tpb);
+    total[t] = tiles_for(it.n_tok[t], it.pos0 + t * a.tpb + it.n_tok[t] - 1, q.z);
+  }
+  const int size = part_size(max(total[0], total[1]), r.z);
+  it.split = r.w >= 0;
+  it.part = max(r.w, 0) + part;
+  it.kt0 = part * size;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) it.n[t] = clampi(total[t] - it.kt0, 0, size);
+  it.clear[0] = q.z % BN != 0 ? q.z / BN - it.kt0 : -1;
+  it.clear[1] = it.n[0] <= it.clear[0] ? it.clear[0] : -1;
+  return part == 0 || it.n[0] > 0 || it.n[1] > 0;
+}
+
 // Item w of n_items (whole warp); false if it has no work.  m: the numbered
 // sequences, or null.
 template <bool PAGED, int FORM>
 __device__ __forceinline__ bool decode_item(const FormArgs<FORM> &a, const Misc *m, int n_items,
                                             int w, Item &it, Gap &gap) {
+  if constexpr (FORM == kShared) return decode_shared(a, w, it, gap);
   const int tb = 2 * a.tpb, u = n_items - 1 - w;
   int s, blk, parts = 1;
   Seq q;
@@ -531,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // may be scheduled from here on; it waits for this grid in turn.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (PAGED && threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const bool cached = a.S <= kCachedSeqs;
+  const bool cached = FORM != kShared && a.S <= kCachedSeqs;
   if (cached)
     for (int i = threadIdx.x; i <= a.S; i += kThreads)
       misc->seq[i] = make_int2(seq_begin(a, i), PAGED && i < a.S ? a.context_lens[i] : 0);
@@ -552,7 +602,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         number_items<PAGED, FORM>(a, misc);
       }
       const Misc *numbered = cached ? misc : nullptr;
-      const int n_items = cached ? misc->first[a.S] : a.n_vblocks * a.Hk;
+      int n_items = cached ? misc->first[a.S] : a.n_vblocks * a.Hk;
+      if constexpr (FORM == kShared) n_items = a.first[*a.head];
       int e = 0, nq = 0;        // tiles and Q tiles copied so far
       bool ok = true;
       int w = blockIdx.x;       // the first item is the CTA's own; the rest are claimed
@@ -576,7 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (FORM == kWindow)
           if (b * kBlk >= a.sinks && b * kBlk + kBlk - 1 <= it.pos0 - a.window)
             return a.num_blocks;
-        return a.block_tables[static_cast<int64_t>(it.kv0) * a.max_blocks + b];
+        return a.block_tables[static_cast<int64_t>(it.kv0) * a.max_blocks + b +
+                              (FORM == kShared ? gap.skip : 0)];
       };
       auto find = [&]() {
         for (;;) {
@@ -1071,28 +1123,36 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
   // it are another kernel's writes sure to be visible.  (Bounds read ahead of it took 1 us off
   // 16 drafts over up to 4096, 33.2 against 34.3.)
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // The call's work, as number_items adds it up, and the sequence's partitions, by one
-  // warp (every block asks L2 for the same few lines).
   const int lane = threadIdx.x & 31;
-  __shared__ Seq shared_seq;
-  __shared__ int shared_cut;
-  if (threadIdx.x < 32) {
-    int64_t work = 0;
-    for (int i = lane; i < a.S; i += 32) {
-      const Work w = work_of<FORM>(a, global_seq<true>(a, i));
-      work += static_cast<int64_t>(w.tiles) * w.blocks;
+  Seq q;
+  int cut, pre = 0;                                      // partitions; those of the prefix
+  if constexpr (FORM == kShared) {
+    const int4 x = a.seq[2 * blockIdx.x], y = a.seq[2 * blockIdx.x + 1];
+    q = {x.x, x.y, x.z, x.w};
+    cut = y.x, pre = y.y;
+  } else {
+    // The call's work, as number_items adds it up, and the sequence's partitions, by one
+    // warp (every block asks L2 for the same few lines).
+    __shared__ Seq shared_seq;
+    __shared__ int shared_cut;
+    if (threadIdx.x < 32) {
+      int64_t work = 0;
+      for (int i = lane; i < a.S; i += 32) {
+        const Work w = work_of<FORM>(a, global_seq<true>(a, i));
+        work += static_cast<int64_t>(w.tiles) * w.blocks;
+      }
+      work = warp_sum(work);
+      const Seq q = global_seq<true>(a, blockIdx.x);
+      if (lane == 0) {
+        shared_seq = q;
+        shared_cut = parts_of(a, q, work_of<FORM>(a, q).tiles, work, a.n_split);
+      }
     }
-    work = warp_sum(work);
-    const Seq q = global_seq<true>(a, blockIdx.x);
-    if (lane == 0) {
-      shared_seq = q;
-      shared_cut = parts_of(a, q, work_of<FORM>(a, q).tiles, work);
-    }
+    __syncthreads();
+    q = shared_seq;
+    cut = shared_cut;
   }
-  __syncthreads();
-  const Seq q = shared_seq;
-  const int cut = shared_cut;
-  if (cut == 1) return;                                  // written directly
+  if (cut == 1 && pre == 0) return;                      // written directly
   const int64_t stride = static_cast<int64_t>(a.T) * a.H;
   for (int x = blockIdx.y * 8 + (threadIdx.x >> 5); x < q.n * a.H; x += gridDim.y * 8) {
     const int i = x / a.H;                               // token of the sequence
@@ -1101,7 +1161,12 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
     const int block = i / (2 * a.tpb), last = min((block + 1) * 2 * a.tpb, q.n) - 1;
     const int skip = gap_of<FORM>(a, q.pos + block * 2 * a.tpb).skip;
     const int size = part_size(tiles_for(1, q.pos + last, q.kv_len) - skip, cut);
-    const int parts = (tiles_for(1, q.pos + i, q.kv_len) - skip + size - 1) / size;
+    const int own = (tiles_for(1, q.pos + i, q.kv_len) - skip + size - 1) / size;
+    const int parts = own + pre;
+    // Partition p's place: the prefix's lie behind the most that a context has.
+    auto place = [&](int p) -> int64_t {
+      return FORM == kShared && p >= own ? a.n_split + p - own : p;
+    };
     // 32 partitions at a time, lane p holding partition p's (max, sum): their rows'
     // loads do not wait for one another.
     float m = -INFINITY, l = 0.f;
@@ -1109,7 +1174,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
     for (int p0 = 0; p0 < parts; p0 += 32) {
       const int n = min(32, parts - p0);
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < n) ml = a.ws_ml[(p0 + lane) * stride + row];
+      if (lane < n) ml = a.ws_ml[place(p0 + lane) * stride + row];
       float mx = ml.x;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, off));
@@ -1128,7 +1193,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
       const float *src = a.ws_o + (p0 * stride + row) * D + lane * 4;
 #pragma unroll 16
       for (int p = 0; p < n; ++p) {
-        const float4 v = *reinterpret_cast<const float4 *>(src + p * stride * D);
+        if (FORM == kShared) src = a.ws_o + (place(p0 + p) * stride + row) * D + lane * 4;
+        const float4 v = *reinterpret_cast<const float4 *>(src + (FORM == kShared ? 0 : p * stride * D));
         const float w = __shfl_sync(~0u, f, p);
         o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y);
         o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
@@ -1139,6 +1205,171 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
     w.x = pack_bf16x2(o.x * inv, o.y * inv);
     w.y = pack_bf16x2(o.z * inv, o.w * inv);
     *reinterpret_cast<uint2 *>(a.o + row * D + lane * 4) = w;
+  }
+}
+
+// Numbers the items of a call with shared prefixes (one block).  A sequence shares its
+// group's prefix if all of that lies before its new tokens; sequences that do are
+// walked behind it only, and the prefix, read through the table of the first of them,
+// is walked by all rows of the group together.  Prefixes that save less than they cost
+// (partial rows, the start of their items) are not shared.
+constexpr int kMaxGroups = kSharedMaxGroups, kClasses = 32;
+__global__ void __launch_bounds__(1024) shared_plan_kernel(const SharedArgs a) {
+  if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ int g_first[kMaxGroups + 1], g_prefix[kMaxGroups], g_lead[kMaxGroups];
+  __shared__ int g_blocks[kMaxGroups];
+  __shared__ unsigned long long classes[kClasses], work_sum;
+  const int tid = threadIdx.x, tb = 2 * a.tpb;
+  for (int g = tid; g <= a.P; g += 1024) {
+    g_first[g] = a.P > 0 ? clampi(a.cu_groups[g], 0, a.S) : 0;
+    if (g == a.P) break;
+    g_prefix[g] = clampi(a.prefix_lens[g], 0, a.max_blocks * kBlk) / kBlk * kBlk;
+    g_lead[g] = a.S;
+    g_blocks[g] = 0;
+  }
+  if (tid < kClasses) classes[tid] = 0;
+  if (tid == 0) work_sum = 0;
+  __syncthreads();
+  // The group of sequence s, or -1 (the last that begins at or before it, if s is in it).
+  auto group_of = [&](int s) {
+    int lo = 0, n = a.P;
+    while (n > 0) {
+      const int half = n / 2;
+      if (g_first[lo + half] <= s) lo += half + 1, n -= half + 1;
+      else n = half;
+    }
+    return lo > 0 && s < g_first[lo] ? lo - 1 : -1;
+  };
+  // Its group, if it shares the prefix, else -1; q: the whole sequence.
+  auto sharing = [&](int s, Seq &q) {
+    q = global_seq<true>(a, s);
+    const int g = group_of(s);
+    return g >= 0 && q.n > 0 && g_prefix[g] > 0 && q.pos >= g_prefix[g] ? g : -1;
+  };
+  for (int s = tid; s < a.S; s += 1024) {
+    Seq q;
+    const int g = sharing(s, q);
+    if (g < 0) continue;
+    atomicMin(&g_lead[g], s);
+    atomicAdd(&g_blocks[g], work_of<kShared>(a, q).blocks);
+  }
+  __syncthreads();
+  // The rows of a group's prefix; all see all of it.
+  auto group_seq = [&](int g) {
+    Seq q;
+    q.begin = seq_begin(a, g_first[g]);
+    q.n = max(seq_begin(a, g_first[g + 1]) - q.begin, 0);
+    q.kv_len = g_prefix[g];
+    q.pos = kSeesAll;
+    return q;
+  };
+  int64_t work = 0;
+  for (int g = tid; g < a.P; g += 1024) {
+    const Seq q = group_seq(g);
+    const Work w = work_of<kShared>(a, q);
+    const float saved = static_cast<float>(g_blocks[g] - w.blocks) * w.tiles;
+    const float cost = kPartFixed * w.blocks + 2.f * kPartRow * q.n * a.G;
+    if (g_lead[g] == a.S || !(saved > cost))
+      g_prefix[g] = 0;
+    else
+      work += static_cast<int64_t>(w.tiles) * w.blocks;
+  }
+  __syncthreads();
+  // What sequence s (or, from S on, group s - S) walks: its rows, keys, table.
+  auto entry = [&](int s, int &row, int &col, bool &shares) {
+    if (s >= a.S) {
+      const int g = s - a.S;
+      shares = true;
+      row = min(g_lead[g], a.S - 1);
+      col = 0;
+      Seq q = group_seq(g);
+      if (g_prefix[g] == 0) q.n = 0;
+      return q;
+    }
+    Seq q;
+    const int g = sharing(s, q);
+    shares = g >= 0;
+    row = s;
+    col = 0;
+    if (shares) {
+      col = g_prefix[g] / kBlk;
+      q.kv_len -= g_prefix[g];
+      q.pos -= g_prefix[g];
+    }
+    return q;
+  };
+  for (int s = tid; s < a.S; s += 1024) {
+    int row, col;
+    bool shares;
+    const Work w = work_of<kShared>(a, entry(s, row, col, shares));
+    work += static_cast<int64_t>(w.tiles) * w.blocks;
+  }
+  work = warp_sum(work);
+  if ((tid & 31) == 0) atomicAdd(&work_sum, static_cast<unsigned long long>(work));
+  __syncthreads();
+  work = static_cast<int64_t>(work_sum);
+  // Items by size, largest first, in classes of 1 .. 15 key tiles, then of half powers of
+  // two; a class's counter holds its entries (high word) and items.
+  auto parts_for = [&](int s, const Seq &q, const Work &w) {
+    return parts_of(a, q, w.tiles, work, s >= a.S ? a.pre_split : a.n_split);
+  };
+  auto class_of = [&](int size) {
+    if (size < 16) return size;
+    const int log = 31 - __clz(size);
+    return min(16 + 2 * (log - 4) + ((size >> (log - 1)) & 1), kClasses - 1);
+  };
+  auto count_of = [&](int blocks, int parts) {
+    return (1ull << 32) + static_cast<unsigned long long>(blocks * parts * a.Hk);
+  };
+  for (int s = tid; s < a.S + a.P; s += 1024) {
+    int row, col;
+    bool shares;
+    const Seq q = entry(s, row, col, shares);
+    const Work w = work_of<kShared>(a, q);
+    if (w.blocks == 0) continue;
+    const int parts = parts_for(s, q, w);
+    atomicAdd(&classes[class_of(part_size(w.tiles, parts))], count_of(w.blocks, parts));
+  }
+  __syncthreads();
+  if (tid == 0) {
+    unsigned long long at = 0;
+    for (int c = kClasses - 1; c >= 0; --c) {
+      const unsigned long long n = classes[c];
+      classes[c] = at;
+      at += n;
+    }
+    const int entries = static_cast<int>(at >> 32);
+    *a.head = entries;
+    a.first[entries] = static_cast<int>(at);
+  }
+  __syncthreads();
+  for (int s = tid; s < a.S + a.P; s += 1024) {
+    int row, col;
+    bool shares;
+    const Seq q = entry(s, row, col, shares);
+    const Work w = work_of<kShared>(a, q);
+    const int parts = w.blocks == 0 ? 1 : parts_for(s, q, w);
+    if (s < a.S) {
+      int pre = 0;
+      if (shares) {
+        // Every block of the prefix cuts its tiles alike.
+        const Seq p = group_seq(group_of(s));
+        const Work pw = work_of<kShared>(a, p);
+        const int size = part_size(pw.tiles, parts_for(a.S, p, pw));
+        pre = (pw.tiles + size - 1) / size;
+      }
+      a.seq[2 * s] = make_int4(q.begin, q.n, q.kv_len, q.pos);
+      a.seq[2 * s + 1] = make_int4(parts, pre, 0, 0);
+    }
+    if (w.blocks == 0) continue;
+    const unsigned long long at =
+        atomicAdd(&classes[class_of(part_size(w.tiles, parts))], count_of(w.blocks, parts));
+    const int i = static_cast<int>(at >> 32);
+    a.first[i] = static_cast<int>(at);
+    a.rec[2 * i] = make_int4(q.begin, q.n, q.kv_len, q.pos);
+    a.rec[2 * i + 1] = make_int4(row, col, parts,
+                                 s >= a.S ? a.n_split : shares || parts > 1 ? 0 : -1);
   }
 }
 
@@ -1159,7 +1390,9 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   e = cudaFuncSetAttribute(fwd_packed_kernel<D, F16, PAGED, FORM>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
   if (e != cudaSuccess) return e;
-  const int64_t n_items = static_cast<int64_t>(a.n_vblocks) * a.n_split * a.Hk;   // a bound
+  int64_t n_items = static_cast<int64_t>(a.n_vblocks) * a.n_split * a.Hk;   // a bound
+  if constexpr (FORM == kShared)
+    n_items += (static_cast<int64_t>(a.T) / (2 * a.tpb) + a.P) * a.pre_split * a.Hk;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(n_items < sms ? n_items : sms));
   cfg.blockDim = dim3(kThreads);
@@ -1171,9 +1404,10 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, fwd_packed_kernel<D, F16, PAGED, FORM>, tq, tk, tv, a);
-  if (e != cudaSuccess || !PAGED || a.n_split == 1) return e;
-  // Eight blocks an SM in all, spread over the sequences (at most kCachedSeqs).
-  cfg.gridDim = dim3(static_cast<unsigned>(a.S), static_cast<unsigned>(8 * sms / a.S));
+  if (e != cudaSuccess || !PAGED || (FORM != kShared && a.n_split == 1)) return e;
+  // Eight blocks an SM in all, spread over the sequences (at most kCachedSeqs; kShared:
+  // any number).
+  cfg.gridDim = dim3(static_cast<unsigned>(a.S), static_cast<unsigned>(std::max(8 * sms / a.S, 1)));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_merge_kernel<FORM>, a);
@@ -1271,6 +1505,62 @@ cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
   }
   if (p.window == 0) return launch<128, false, true, kAll>(tq, tk, tv, a, stream);
   return launch<128, false, true, kWindow>(tq, tk, tv, window_args(a, p), stream);
+}
+
+// Workspace of a call with shared prefixes: partial rows (at least one of a row's own
+// context and one of its prefix, up to 256 MB in all), then the plan.
+SharedLayout shared_layout(int T, int S, int P, int H, int Hk, int max_blocks) {
+  SharedLayout l{};
+  const double tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;
+  const double least = std::fmax(4.0, std::sqrt(tiles * Hk / 152 * 2.5 / 0.7));
+  const double room = 256e6 / 2 / (sizeof(float) * (kDecodeHeadSize + 2.0) * T * H);
+  const double n = std::fmin(std::fmin(tiles / least + 1, room), 32767);
+  l.split = n < 1 ? 1 : static_cast<int>(n);
+  l.pre_split = P > 0 ? l.split : 0;
+  const size_t rows = static_cast<size_t>(l.split + l.pre_split) * T * H;
+  auto take = [&](size_t bytes) {
+    const size_t at = l.bytes;
+    l.bytes += (bytes + 15) / 16 * 16;
+    return at;
+  };
+  const size_t entries = static_cast<size_t>(S) + P;
+  l.rows = take(rows * kDecodeHeadSize * sizeof(float));
+  l.sums = take(rows * sizeof(float2));
+  l.rec = take(entries * 2 * sizeof(int4));
+  l.seq = take(static_cast<size_t>(S) * 2 * sizeof(int4));
+  l.first = take((entries + 1) * sizeof(int));
+  l.head = take(sizeof(int));
+  return l;
+}
+
+cudaError_t launch_paged_shared(const CUtensorMap &tq, const CUtensorMap &tk,
+                                const CUtensorMap &tv, const PackedProblem &p,
+                                const int *cu_groups, const int *prefix_lens, int P,
+                                char *workspace, int *sched, int *dev_status, int fault_cta,
+                                cudaStream_t stream) {
+  const SharedLayout l = shared_layout(p.T, p.S, P, p.H, p.Hk, p.max_blocks);
+  SharedArgs a;
+  static_cast<Args &>(a) = args_of(p, sched, dev_status, fault_cta);
+  a.n_split = l.split, a.pre_split = l.pre_split;
+  a.ws_o = reinterpret_cast<float *>(workspace + l.rows);
+  a.ws_ml = reinterpret_cast<float2 *>(workspace + l.sums);
+  a.rec = reinterpret_cast<int4 *>(workspace + l.rec);
+  a.seq = reinterpret_cast<int4 *>(workspace + l.seq);
+  a.first = reinterpret_cast<int *>(workspace + l.first);
+  a.head = reinterpret_cast<int *>(workspace + l.head);
+  a.cu_groups = cu_groups, a.prefix_lens = prefix_lens, a.P = P;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_plan_kernel, a);
+  if (e != cudaSuccess) return e;
+  return launch<128, false, true, kShared>(tq, tk, tv, a, stream);
 }
 
 }  // namespace fattn

@@ -240,6 +240,20 @@ cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
                                  int *sched, int *dev_status, int fault_cta,
                                  cudaStream_t stream);
 
+// Paged, with groups of sequences that share a prefix: P groups, cu_groups [P + 1] over
+// the sequences, prefix_lens [P].  The workspace's parts are bytes from its start.
+constexpr int kSharedMaxGroups = 1024;
+struct SharedLayout {
+  int split, pre_split;       // most partitions of a context, of a prefix
+  size_t rows, sums, rec, seq, first, head, bytes;
+};
+SharedLayout shared_layout(int T, int S, int P, int H, int Hk, int max_blocks);
+cudaError_t launch_paged_shared(const CUtensorMap &tq, const CUtensorMap &tk,
+                                const CUtensorMap &tv, const PackedProblem &p,
+                                const int *cu_groups, const int *prefix_lens, int P,
+                                char *workspace, int *sched, int *dev_status, int fault_cta,
+                                cudaStream_t stream);
+
 // Gradients of the packed forward (bwd_packed.cu).  Workspace, in floats from
 // its start: the dQ accumulator [H][n_blocks * 128][d], those of dK and dV
 // [Hk][..][d] (where several items add to them), [-LSE2 | -D] per head and block,

@@ -677,6 +677,47 @@ int fa_paged_prefill_window(const void *q, const void *k_cache, const void *v_ca
                             unsigned long long workspace_bytes, fa_stream_t stream);
 
 /*
+ * fa_paged_prefill_shared -- fa_paged_prefill for sequences that share the cache blocks
+ * of a long prefix (a system prompt, a document, the stem of sampled continuations):
+ * the prefix is read once for all rows of its group, not once per sequence, and what
+ * each sequence has behind it on its own; the two are joined row by row.
+ *
+ *   cu_groups     int32 [num_groups + 1] on the device, non-decreasing, in [0, num_seqs]:
+ *                 group g has sequences cu_groups[g] .. cu_groups[g+1] - 1 (of any
+ *                 number; sequences of no group share nothing).
+ *   prefix_lens   int32 [num_groups] on the device: the group's first tokens that are
+ *                 the same, rounded down to whole cache blocks.
+ *   num_groups    0 (then both may be NULL) to 1024 (more: FA_ERR_UNSUPPORTED).
+ *   block_tables, context_lens   as for fa_paged_prefill, prefix included.  The first
+ *                 prefix_lens[g] / block_size table entries of the group's sequences name
+ *                 the same blocks, or blocks with the same contents: the call reads them
+ *                 through the table of one of the sequences (and does not check that they
+ *                 agree).
+ *   workspace     device memory of at least fa_paged_prefill_shared_workspace_bytes bytes
+ *                 (never 0), 16-byte aligned, scratch during the call; calls that may run
+ *                 at the same time need separate ones.
+ * The output is that of fa_paged_prefill for the same tables, up to the order of fp32
+ * sums.  A sequence whose prefix does not lie before all its new tokens (it is shorter,
+ * say, or a padded row's context is 0) takes no part in the sharing and is walked whole,
+ * as every sequence is whose group's prefix would save less than it costs: that is found
+ * on the device, so that a captured call serves changing lengths.  Contexts and prefixes
+ * are cut into partitions for any number of sequences.  Results are the same from call to
+ * call, bit for bit.  Every other argument and error as for fa_paged_prefill.
+ */
+unsigned long long fa_paged_prefill_shared_workspace_bytes(int num_seqs, int total_tokens,
+                                                           int num_groups, int num_heads,
+                                                           int num_kv_heads,
+                                                           int max_num_blocks_per_seq);
+int fa_paged_prefill_shared(const void *q, const void *k_cache, const void *v_cache,
+                            const int *block_tables, const int *context_lens,
+                            const int *cu_seqlens, const int *cu_groups, const int *prefix_lens,
+                            void *out, int num_seqs, int total_tokens, int num_groups,
+                            int num_heads, int num_kv_heads, int head_size, int block_size,
+                            int num_blocks, int max_num_blocks_per_seq, long long q_stride,
+                            float scale, void *workspace, unsigned long long workspace_bytes,
+                            fa_stream_t stream);
+
+/*
  * fa_debug_inject_fault -- test hook for the device-side failure path.
  *
  * mode 1 arms the current device: the next tensor-core forward launched on
