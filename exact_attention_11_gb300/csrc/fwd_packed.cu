@@ -139,12 +139,17 @@ struct Item {
   int clear[2];      // the step in which tile A's (B's) softmax clears V's last rows, or < 0
 };
 
-// kWindow: a block visits a list of key tiles: those of the sequence's first tokens,
-// then those from the first key that its first token sees on.  Entry x of the list is
-// tile x, or x + skip from entry `at` on; a tile of both comes once.
+// kWindow: a block visits a list of cells of 16 keys: those of the sequence's first
+// tokens, then those from the first key that its first token sees on; eight cells are a
+// key tile.  Cell x of the list is the sequence's cell x, or x + skip from `at` on.
+// Positions and lengths in an item count along the list: skip cells less than in the
+// sequence (every real row lies behind the gap).
+// kShared: skip is the first table column of the item's keys.
+constexpr int kCell = 16;
+static_assert(kCell == kBlk, "a cell of the paged list is a cache block");
 struct Gap {
   int at, skip;
-  __device__ int tile(int x) const { return x >= at ? x + skip : x; }
+  __device__ int cell(int x) const { return x >= at ? x + skip : x; }
 };
 
 constexpr int kCachedSeqs = 112;
@@ -152,7 +157,6 @@ struct Misc {
   uint32_t tmem_base;
   int abort;
   Item item[2];
-  Gap gap[2];                   // kWindow: of the items
   int2 seq[kCachedSeqs + 1];    // (first row, context length)
   // By weight of their items, lightest first: the sequences, their partitions, and
   // the items of those before ([S]: of all).
@@ -190,6 +194,16 @@ struct Args {
 struct WindowArgs : Args {
   int window, sinks;            // up to 2^30 each
 };
+// The map of k or v (packed, kWindow: and one with boxes of 64 x 16 x 1).
+struct CellMaps {
+  CUtensorMap tiles, cells;
+};
+template <bool PAGED, int FORM>
+using KvMap = std::conditional_t<!PAGED && FORM == kWindow, CellMaps, CUtensorMap>;
+__host__ __device__ __forceinline__ const CUtensorMap &tile_map(const CUtensorMap &m) { return m; }
+__host__ __device__ __forceinline__ const CUtensorMap &cell_map(const CUtensorMap &m) { return m; }
+__host__ __device__ __forceinline__ const CUtensorMap &tile_map(const CellMaps &m) { return m.tiles; }
+__host__ __device__ __forceinline__ const CUtensorMap &cell_map(const CellMaps &m) { return m.cells; }
 // A prefix is walked once for all rows of its group: it and what each sequence has of
 // its own are items of their own, numbered by shared_plan_kernel, and their partial rows
 // lie in ws_o one behind the other, those of the prefix from partition n_split on.
@@ -250,8 +264,8 @@ __device__ __forceinline__ Seq global_seq(const Args &a, int s) {
 template <int FORM>
 __device__ __forceinline__ Gap gap_of(const FormArgs<FORM> &a, int pos) {
   if constexpr (FORM == kWindow) {
-    const int first = max(pos - a.window + 1, 0) / BN;
-    const int at = min((a.sinks + BN - 1) / BN, first);
+    const int first = max(pos - a.window + 1, 0) / kCell;
+    const int at = min((a.sinks + kCell - 1) / kCell, first);
     return {at, first - at};
   }
   return {0, 0};
@@ -263,10 +277,10 @@ struct Work {
 };
 template <int FORM>
 __device__ __forceinline__ Work work_of(const FormArgs<FORM> &a, const Seq &q) {
-  Work w = {tiles_for(q.n, q.pos + q.n - 1, q.kv_len), (q.n + 2 * a.tpb - 1) / (2 * a.tpb)};
-  if (FORM == kWindow)
-    w.tiles = max(w.tiles - gap_of<FORM>(a, q.pos + max(w.blocks - 1, 0) * 2 * a.tpb).skip, 0);
-  return w;
+  const int blocks = (q.n + 2 * a.tpb - 1) / (2 * a.tpb);
+  const int gap =
+      FORM == kWindow ? gap_of<FORM>(a, q.pos + max(blocks - 1, 0) * 2 * a.tpb).skip * kCell : 0;
+  return {tiles_for(q.n, q.pos + q.n - 1 - gap, q.kv_len - gap), blocks};
 }
 
 // Partitions.  With W key tiles of work per SM cut into partitions of p, a
@@ -425,14 +439,15 @@ __device__ __forceinline__ bool decode_item(const FormArgs<FORM> &a, const Misc 
   it.live = 1;
   it.row0 = q.begin + tok0;
   it.pos0 = q.pos + tok0;
-  it.kv_len = q.kv_len;
   it.kv0 = PAGED ? s : q.begin;
   gap = gap_of<FORM>(a, it.pos0);
+  if (FORM == kWindow) it.pos0 -= gap.skip * kCell, q.kv_len -= gap.skip * kCell;
+  it.kv_len = q.kv_len;
   int total[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     it.n_tok[t] = clampi(q.n - tok0 - t * a.tpb, 0, a.tpb);
-    total[t] = tiles_for(it.n_tok[t], it.pos0 + t * a.tpb + it.n_tok[t] - 1, q.kv_len) - gap.skip;
+    total[t] = tiles_for(it.n_tok[t], it.pos0 + t * a.tpb + it.n_tok[t] - 1, q.kv_len);
   }
   const int size = part_size(max(total[0], total[1]), parts);
   it.split = parts > 1;
@@ -440,8 +455,8 @@ __device__ __forceinline__ bool decode_item(const FormArgs<FORM> &a, const Misc 
 #pragma unroll
   for (int t = 0; t < 2; ++t) it.n[t] = clampi(total[t] - it.kt0, 0, size);
   // Where both tiles visit the sequence's ragged last key tile A clears its V, whose
-  // P V goes first.  (It lies behind the gap: no earlier than the window's first tile.)
-  it.clear[0] = q.kv_len % BN != 0 ? q.kv_len / BN - gap.skip - it.kt0 : -1;
+  // P V goes first.
+  it.clear[0] = q.kv_len % BN != 0 ? q.kv_len / BN - it.kt0 : -1;
   it.clear[1] = it.n[0] <= it.clear[0] ? it.clear[0] : -1;
   return it.part == 0 || it.n[0] > 0 || it.n[1] > 0;
 }
@@ -517,8 +532,8 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t ph) {
 template <int D, bool F16, bool PAGED, int FORM>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_packed_kernel(const __grid_constant__ CUtensorMap tm_q,
-                      const __grid_constant__ CUtensorMap tm_k,
-                      const __grid_constant__ CUtensorMap tm_v, const FormArgs<FORM> a) {
+                      const __grid_constant__ KvMap<PAGED, FORM> tm_k,
+                      const __grid_constant__ KvMap<PAGED, FORM> tm_v, const FormArgs<FORM> a) {
   using C = Cfg<D, PAGED>;
   static_assert(!PAGED || (D == 128 && !F16), "the paged cache is bf16, d = 128");
   constexpr int R = C::kSlots;
@@ -595,8 +610,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // issues the packed copies; lanes 0 .. 7 issue a paged tile's copies.
       if (lane == 0) {
         tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
+        tma_prefetch_desc(&tile_map(tm_k));
+        tma_prefetch_desc(&tile_map(tm_v));
       }
       if (cached) {
         number_items<PAGED, FORM>(a, misc);
@@ -616,19 +631,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       Item nxt;
       Gap nxt_gap;
       int nxt_id = 0;           // paged: block id of the item's block `lane`
-      auto ids_of = [&](const Item &it, const Gap &gap, int x) -> int {
-        // Lane i: block i of the four key tiles from entry x on; past the context, or
-        // where no token of the item sees it, a block that the cache does not have
-        // (reads as zeros).
-        const int b = FORM == kWindow
-                          ? gap.tile(x + lane / kTileBlocks) * kTileBlocks + lane % kTileBlocks
-                          : x * kTileBlocks + lane;
+      auto ids_of = [&](const Item &it, const Gap &gap, int tile) -> int {
+        // Lane i: block i of the four key tiles from `tile` on; past the
+        // context, a block that the cache does not have (reads as zeros).
+        const int b = tile * kTileBlocks + lane;
         if (b >= (it.kv_len + kBlk - 1) / kBlk) return a.num_blocks;
-        if constexpr (FORM == kWindow)
-          if (b * kBlk >= a.sinks && b * kBlk + kBlk - 1 <= it.pos0 - a.window)
-            return a.num_blocks;
-        return a.block_tables[static_cast<int64_t>(it.kv0) * a.max_blocks + b +
-                              (FORM == kShared ? gap.skip : 0)];
+        const int at = FORM == kWindow ? gap.cell(b) : FORM == kShared ? gap.skip + b : b;
+        return a.block_tables[static_cast<int64_t>(it.kv0) * a.max_blocks + at];
+      };
+      // Packed: the copies of a key or value tile.  Where the list's gap lies inside it
+      // (kWindow), cell by cell; else one box of 128 rows for every 64 values.
+      auto load_rows = [&](const auto &map, const Item &it, const Gap &gap, int tile, uint32_t dst,
+                           uint32_t full) {
+        const int c0 = tile * (BN / kCell);
+        if (FORM == kWindow && gap.skip > 0 && c0 < gap.at && c0 + BN / kCell > gap.at) {
+          const int c = lane % (BN / kCell), b = lane / (BN / kCell);
+          if (b < C::kBoxes)
+            tma_load_3d(dst + b * C::kBoxBytes + c * kCell * 128, &cell_map(map), b * 64,
+                        it.kv0 + gap.cell(c0 + c) * kCell, it.kvh, full);
+        } else if (lane == 0) {
+          const int row = it.kv0 + (FORM == kWindow ? gap.cell(c0) * kCell : tile * BN);
+          for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_3d(dst + b * C::kBoxBytes, &tile_map(map), b * 64, row, it.kvh, full);
+        }
       };
       auto find = [&]() {
         for (;;) {
@@ -661,7 +686,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait(bar(kBarItemEmpty + slot), ((k >> 1) & 1) ^ 1, abort_flag);
           if (ok) {
             misc->item[slot] = it;
-            if (FORM == kWindow) misc->gap[slot] = gap;
             mbar_arrive(bar(kBarItemFull + slot));
           }
         }
@@ -693,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const int n_max = max(it.n[0], it.n[1]);
         for (int j = 0; j < n_max; ++j) {
-          const int tile = FORM == kWindow ? gap.tile(it.kt0 + j) : it.kt0 + j;
+          const int tile = it.kt0 + j;
           // The next item is claimed as late as its loads allow (an item held by a
           // CTA that is busy is lost to the others: 2 sequences of 4096, 16 heads,
           // 113 us when it was claimed at the start, 94 so), decoded behind the last copy.
@@ -702,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (PAGED) {
             if ((j & 3) == 0) {
               if (j > 0) ids = ids_next;
-              if (j + 4 < n_max) ids_next = ids_of(it, gap, it.kt0 + j + 4);
+              if (j + 4 < n_max) ids_next = ids_of(it, gap, tile + 4);
             }
             pb = __shfl_sync(~0u, ids, (j & 3) * kTileBlocks + (lane & 7));
           }
@@ -711,11 +735,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t k_bar = bar(kBarFull + e % R);
           if (PAGED) {
             if (lane < kTileBlocks)
-              tma_load_5d(k_dst + lane * 4096, &tm_k, 0, 0, 0, it.kvh, pb, k_bar);
-          } else if (lane == 0) {
-            for (int b = 0; b < C::kBoxes; ++b)
-              tma_load_3d(k_dst + b * C::kBoxBytes, &tm_k, b * 64, it.kv0 + tile * BN, it.kvh,
-                          k_bar);
+              tma_load_5d(k_dst + lane * 4096, &tile_map(tm_k), 0, 0, 0, it.kvh, pb, k_bar);
+          } else {
+            load_rows(tm_k, it, gap, tile, k_dst, k_bar);
           }
           ++e;
           if (j == 0 && !(ok = load_q(0) && load_q(1))) break;
@@ -724,11 +746,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t v_bar = bar(kBarFull + e % R);
           if (PAGED) {
             if (lane < kTileBlocks)
-              tma_load_4d(v_dst + lane * 4096, &tm_v, 0, 0, it.kvh, pb, v_bar);
-          } else if (lane == 0) {
-            for (int b = 0; b < C::kBoxes; ++b)
-              tma_load_3d(v_dst + b * C::kBoxBytes, &tm_v, b * 64, it.kv0 + tile * BN, it.kvh,
-                          v_bar);
+              tma_load_4d(v_dst + lane * 4096, &tile_map(tm_v), 0, 0, it.kvh, pb, v_bar);
+          } else {
+            load_rows(tm_v, it, gap, tile, v_dst, v_bar);
           }
           ++e;
         }
@@ -882,8 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!it.live) break;
       const int n_mine = it.n[t];
       // Keys below lim are visible to this row (the first is key 0 of the partition).
-      const int lim = min(it.kv_len, it.pos0 + t * a.tpb + row_in_tile() / a.G + 1) -
-                      (FORM == kWindow ? 0 : it.kt0 * BN);
+      const int lim = min(it.kv_len, it.pos0 + t * a.tpb + row_in_tile() / a.G + 1) - it.kt0 * BN;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n_mine; ++j, phases ^= 1) {
         if (j == it.clear[t]) {
@@ -915,11 +934,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < 4; ++c) tmem_wait_ld(sv[c]);
 #define S_(c) sv[(c) >> 5][(c) & 31]
         if constexpr (FORM == kWindow) {
-          // lim counts from key 0; keys from lim - window on, or below `sinks`, are
-          // visible.  (A row that holds a query sees its own position: lim is that + 1.)
-          const volatile Gap &gap = misc->gap[k & 1];
-          const int x = it.kt0 + j, base = (x + (x >= gap.at ? gap.skip : 0)) * BN;
-          const int lim_j = lim - base, low_j = lim_j - a.window, first_j = a.sinks - base;
+          // Keys from lim - window on, or among the first `sinks`, are visible.  (A row
+          // that holds a query sees its own position: lim is that + 1.)
+          const int lim_j = lim - j * BN, low_j = lim_j - a.window;
+          const int first_j = a.sinks - (it.kt0 + j) * BN;
           if (__any_sync(~0u, lim_j < BN || low_j > max(first_j, 0))) {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -1159,9 +1177,10 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
     const int64_t row = static_cast<int64_t>(q.begin) * a.H + x;
     // The block's last token sets the partitions' size, the row's own those it is in.
     const int block = i / (2 * a.tpb), last = min((block + 1) * 2 * a.tpb, q.n) - 1;
-    const int skip = gap_of<FORM>(a, q.pos + block * 2 * a.tpb).skip;
-    const int size = part_size(tiles_for(1, q.pos + last, q.kv_len) - skip, cut);
-    const int own = (tiles_for(1, q.pos + i, q.kv_len) - skip + size - 1) / size;
+    const int gap =
+        FORM == kWindow ? gap_of<FORM>(a, q.pos + block * 2 * a.tpb).skip * kCell : 0;
+    const int size = part_size(tiles_for(1, q.pos + last - gap, q.kv_len - gap), cut);
+    const int own = (tiles_for(1, q.pos + i - gap, q.kv_len - gap) + size - 1) / size;
     const int parts = own + pre;
     // Partition p's place: the prefix's lie behind the most that a context has.
     auto place = [&](int p) -> int64_t {
@@ -1381,8 +1400,8 @@ cudaError_t sm_count(int *n) {
 }
 
 template <int D, bool F16, bool PAGED, int FORM>
-cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                   const FormArgs<FORM> &a, cudaStream_t stream) {
+cudaError_t launch(const CUtensorMap &tq, const KvMap<PAGED, FORM> &tk,
+                   const KvMap<PAGED, FORM> &tv, const FormArgs<FORM> &a, cudaStream_t stream) {
   using C = Cfg<D, PAGED>;
   int sms = 0;
   cudaError_t e = sm_count(&sms);
@@ -1414,9 +1433,9 @@ cudaError_t launch(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorM
 }
 
 template <int FORM>
-cudaError_t launch_packed_form(const CUtensorMap &tq, const CUtensorMap &tk,
-                               const CUtensorMap &tv, const FormArgs<FORM> &a, int d, bool f16,
-                               cudaStream_t stream) {
+cudaError_t launch_packed_form(const CUtensorMap &tq, const KvMap<false, FORM> &tk,
+                               const KvMap<false, FORM> &tv, const FormArgs<FORM> &a, int d,
+                               bool f16, cudaStream_t stream) {
   if (d == 64)
     return f16 ? launch<64, true, false, FORM>(tq, tk, tv, a, stream)
                : launch<64, false, false, FORM>(tq, tk, tv, a, stream);
@@ -1462,7 +1481,8 @@ cudaError_t launch_fwd_packed(const CUtensorMap &tq, const CUtensorMap &tk, cons
                               int *dev_status, int fault_cta, cudaStream_t stream) {
   const Args a = args_of(p, sched, dev_status, fault_cta);
   if (p.window == 0) return launch_packed_form<kAll>(tq, tk, tv, a, d, f16, stream);
-  return launch_packed_form<kWindow>(tq, tk, tv, window_args(a, p), d, f16, stream);
+  return launch_packed_form<kWindow>(tq, CellMaps{tk, *p.k_cells}, CellMaps{tv, *p.v_cells},
+                                     window_args(a, p), d, f16, stream);
 }
 
 // The most partitions of a context, from what the host knows (the longest one's
@@ -1476,10 +1496,11 @@ int paged_max_parts(int T, int S, int H, int Hk, int max_blocks, int window, int
   double tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;
   // With a window, a block's list of key tiles is that long at most.
   if (window > 0)
-    tiles = std::fmin(tiles, (window + 2.0 * packed_tile_tokens(H / Hk)) / BN + 2 +
-                                 (sinks + BN - 1) / BN);
+    tiles = std::fmin(tiles, std::ceil((window + 2.0 * packed_tile_tokens(H / Hk) + sinks +
+                                        2 * kCell) / BN));
   const double least = std::fmax(4.0, std::sqrt(tiles * Hk / 152 * 2.5 / 0.7));
   const double room = 256e6 / (sizeof(float) * (kDecodeHeadSize + 2.0) * T * H);
+  if (tiles < 1.5 * least) return 1;   // parts_of never cuts so few
   const double n = std::fmin(std::fmin(tiles / least + 1, room), 32767);
   return n < 1 ? 1 : static_cast<int>(n);
 }

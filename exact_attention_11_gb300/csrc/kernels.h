@@ -224,6 +224,8 @@ struct PackedProblem {
   // A query at position p sees keys j <= p with j > p - window or j < sinks (both up to
   // 2^30); window 0: all keys up to its own (packed and not causal: all).
   int window, sinks;
+  // Packed with a window: tk and tv with boxes of 64 x 16 x 1.
+  const CUtensorMap *k_cells, *v_cells;
 };
 int packed_tile_tokens(int group);              // tokens of a 128-row query tile
 int packed_blocks(int T, int S, int group);     // bound on the two-tile blocks of a call
