@@ -274,3 +274,28 @@ def test_refusals():
             fa.paged_prefill_window(*x, window, sinks)
     with pytest.raises(ValueError):
         fa.forward_packed_window(q.float(), k.float(), v.float(), cu, 4)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, F16), (128, BF16)])
+def test_outputs_aligned_to_16_bytes_only(d, dtype):
+    q, k, v, cu = draw([300, 41], 4, 2, d, dtype, seed=3)
+    a, _ = fa.forward_packed_window(q, k, v, cu, 70, 2)
+    room = torch.full((a.numel() + 24,), 7.0, dtype=dtype, device=DEV)
+    for off in (8, 16):
+        out = room[off:off + a.numel()].view(a.shape)
+        fa.forward_packed_window(q, k, v, cu, 70, 2, out=out)
+        assert torch.equal(a, out)
+        assert (room[:off] == 7).all() and (room[off + a.numel():] == 7).all()
+        room.fill_(7.0)
+
+
+def test_paged_buffers_aligned_to_16_bytes_only():
+    x = draw_paged([1, 30, 4, 1], [3000, 5000, 800, 40], 8, 2, seed=11)
+    a = fa.paged_prefill_window(*x, 2500, 4)
+    n = fa.fa_paged_prefill_window_workspace_bytes(4, 36, 8, 2, x[3].shape[1], 2500, 4)
+    assert n > 0
+    room = torch.zeros(a.numel() + 8, dtype=BF16, device=DEV)
+    ws = torch.empty(n + 16, dtype=torch.uint8, device=DEV)
+    out = room[8:].view(a.shape)
+    fa.paged_prefill_window(*x, 2500, 4, out=out, workspace=ws[16:])
+    assert torch.equal(a, out)
