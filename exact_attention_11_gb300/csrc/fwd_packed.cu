@@ -64,6 +64,7 @@
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 #include <type_traits>
 
 #include "kernels.h"
@@ -210,6 +211,7 @@ __host__ __device__ __forceinline__ const CUtensorMap &cell_map(const CellMaps &
 struct SharedArgs : Args {
   const int *cu_groups, *prefix_lens;
   int P, pre_split;             // groups; most partitions of a prefix
+  int ctas;                     // CTAs that have their first item in `start`
   int *head;                    // number of entries of `first` and `rec`
   int *first;                   // [entries + 1]: their first items, heaviest first
   int4 *rec;                    // [entries][2]: begin, n, kv_len, pos;
@@ -217,6 +219,7 @@ struct SharedArgs : Args {
                                 // (or -1: rows are written directly)
   int4 *seq;                    // [S][2]: begin, n, kv_len, pos (of the sequence's own keys);
                                 // partitions, those of the prefix (0: none), -, -
+  int4 *start;                  // [ctas][4]: Item and the first table column
 };
 template <int FORM>
 using FormArgs = std::conditional_t<FORM == kWindow, WindowArgs,
@@ -373,12 +376,11 @@ __device__ __forceinline__ void number_items(const FormArgs<FORM> &a, Misc *m) {
   __syncwarp();
 }
 
-// kShared: the numbered entries in global memory, by their sizes.
-__device__ __forceinline__ bool decode_shared(const SharedArgs &a, int w, Item &it, Gap &gap) {
-  const int at = warp_search(*a.head, w, [&](int i) { return a.first[i]; });
-  const int4 q = a.rec[2 * at], r = a.rec[2 * at + 1];
-  int blk = (w - a.first[at]) / a.Hk;
-  it.kvh = w - a.first[at] - blk * a.Hk;
+// kShared: item i of an entry, whose words are q and r.
+__device__ __forceinline__ bool decode_entry(const SharedArgs &a, const int4 &q, const int4 &r,
+                                             int i, Item &it, Gap &gap) {
+  const int blk = i / a.Hk;
+  it.kvh = i - blk * a.Hk;
   const int x = blk / r.z, part = blk - x * r.z, tok0 = x * 2 * a.tpb;
   it.live = 1;
   it.row0 = q.x + tok0;
@@ -401,6 +403,12 @@ __device__ __forceinline__ bool decode_shared(const SharedArgs &a, int w, Item &
   it.clear[0] = q.z % BN != 0 ? q.z / BN - it.kt0 : -1;
   it.clear[1] = it.n[0] <= it.clear[0] ? it.clear[0] : -1;
   return part == 0 || it.n[0] > 0 || it.n[1] > 0;
+}
+
+// Item w of the numbered entries, in global memory.
+__device__ __forceinline__ bool decode_shared(const SharedArgs &a, int w, Item &it, Gap &gap) {
+  const int at = warp_search(*a.head, w, [&](int i) { return a.first[i]; });
+  return decode_entry(a, a.rec[2 * at], a.rec[2 * at + 1], w - a.first[at], it, gap);
 }
 
 // Item w of n_items (whole warp); false if it has no work.  m: the numbered
@@ -689,7 +697,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return __shfl_sync(~0u, good, 0);
       };
-      find();
+      if constexpr (FORM == kShared) {
+        // The CTA's own item comes decoded (found like the others, it takes 0.6 us longer).
+        nxt.live = 0;
+        if (w < n_items) {
+          static_assert(sizeof(Item) == 60, "four words of 16 bytes with the table column");
+          int4 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = a.start[4 * w + i];
+          memcpy(&nxt, x, sizeof nxt);
+          nxt_gap = {0, x[3].w};
+          nxt_id = ids_of(nxt, nxt_gap, nxt.kt0);
+        }
+      } else {
+        find();
+      }
       for (int k = 0; ok; ++k) {
         const Item it = nxt;
         const Gap gap = nxt_gap;
@@ -1127,8 +1149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       if (!PAGED && a.lse != nullptr && my_out >= 0)
-        a.lse[static_cast<int64_t>(my_out % a.H) * a.T + my_out / a.H] =
-            (m + __log2f(l)) * 0.6931471805599453f;
+        a.lse[static_cast<int64_t>(head) * a.T + row] = (m + __log2f(l)) * 0.6931471805599453f;
     }
   }
 
@@ -1255,15 +1276,23 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
 // walked behind it only, and the prefix, read through the table of the first of them,
 // is walked by all rows of the group together.  Prefixes that save less than they cost
 // (partial rows, the start of their items) are not shared.
-constexpr int kMaxGroups = kSharedMaxGroups, kClasses = 32;
-__global__ void __launch_bounds__(1024) shared_plan_kernel(const SharedArgs a) {
+constexpr int kMaxGroups = kSharedMaxGroups, kClasses = 32, kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedArgs a) {
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   __shared__ int g_first[kMaxGroups + 1], g_prefix[kMaxGroups], g_lead[kMaxGroups];
   __shared__ int g_blocks[kMaxGroups];
+  __shared__ int begins[kPlanThreads + 1];                 // of the first sequences
+  __shared__ int firsts[kPlanThreads];                     // of the first entries
   __shared__ unsigned long long classes[kClasses], work_sum;
-  const int tid = threadIdx.x, tb = 2 * a.tpb;
-  for (int g = tid; g <= a.P; g += 1024) {
+  __shared__ int n_entries;
+  const int tid = threadIdx.x;
+  // The thread's first sequence stays in registers; with that, and the groups, global
+  // memory is read once, up to 1024 sequences.
+  Seq mine = {};
+  if (tid < a.S) mine = global_seq<true>(a, tid);
+  if (tid < a.S) begins[tid] = mine.begin, begins[tid + 1] = seq_begin(a, tid + 1);
+  for (int g = tid; g <= a.P; g += kPlanThreads) {
     g_first[g] = a.P > 0 ? clampi(a.cu_groups[g], 0, a.S) : 0;
     if (g == a.P) break;
     g_prefix[g] = clampi(a.prefix_lens[g], 0, a.max_blocks * kBlk) / kBlk * kBlk;
@@ -1273,6 +1302,8 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const SharedArgs a) {
   if (tid < kClasses) classes[tid] = 0;
   if (tid == 0) work_sum = 0;
   __syncthreads();
+  auto whole = [&](int s) { return s == tid ? mine : global_seq<true>(a, s); };
+  auto begin_of = [&](int s) { return s <= kPlanThreads ? begins[s] : seq_begin(a, s); };
   // The group of sequence s, or -1 (the last that begins at or before it, if s is in it).
   auto group_of = [&](int s) {
     int lo = 0, n = a.P;
@@ -1283,14 +1314,13 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const SharedArgs a) {
     }
     return lo > 0 && s < g_first[lo] ? lo - 1 : -1;
   };
-  // Its group, if it shares the prefix, else -1; q: the whole sequence.
-  auto sharing = [&](int s, Seq &q) {
-    q = global_seq<true>(a, s);
+  // Its group, if the whole sequence q shares the prefix, else -1.
+  auto sharing = [&](int s, const Seq &q) {
     const int g = group_of(s);
     return g >= 0 && q.n > 0 && g_prefix[g] > 0 && q.pos >= g_prefix[g] ? g : -1;
   };
-  for (int s = tid; s < a.S; s += 1024) {
-    Seq q;
+  for (int s = tid; s < a.S; s += kPlanThreads) {
+    const Seq q = whole(s);
     const int g = sharing(s, q);
     if (g < 0) continue;
     atomicMin(&g_lead[g], s);
@@ -1300,14 +1330,14 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const SharedArgs a) {
   // The rows of a group's prefix; all see all of it.
   auto group_seq = [&](int g) {
     Seq q;
-    q.begin = seq_begin(a, g_first[g]);
-    q.n = max(seq_begin(a, g_first[g + 1]) - q.begin, 0);
+    q.begin = begin_of(g_first[g]);
+    q.n = max(begin_of(g_first[g + 1]) - q.begin, 0);
     q.kv_len = g_prefix[g];
     q.pos = kSeesAll;
     return q;
   };
   int64_t work = 0;
-  for (int g = tid; g < a.P; g += 1024) {
+  for (int g = tid; g < a.P; g += kPlanThreads) {
     const Seq q = group_seq(g);
     const Work w = work_of<kShared>(a, q);
     const float saved = static_cast<float>(g_blocks[g] - w.blocks) * w.tiles;
@@ -1318,33 +1348,40 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const SharedArgs a) {
       work += static_cast<int64_t>(w.tiles) * w.blocks;
   }
   __syncthreads();
-  // What sequence s (or, from S on, group s - S) walks: its rows, keys, table.
-  auto entry = [&](int s, int &row, int &col, bool &shares) {
-    if (s >= a.S) {
-      const int g = s - a.S;
-      shares = true;
-      row = min(g_lead[g], a.S - 1);
-      col = 0;
-      Seq q = group_seq(g);
-      if (g_prefix[g] == 0) q.n = 0;
-      return q;
-    }
+  // What entry s walks -- sequence s, or, from S on, group s - S: its rows and keys, where
+  // they are found, and whether its rows are partial.
+  struct Entry {
     Seq q;
-    const int g = sharing(s, q);
-    shares = g >= 0;
-    row = s;
-    col = 0;
-    if (shares) {
-      col = g_prefix[g] / kBlk;
-      q.kv_len -= g_prefix[g];
-      q.pos -= g_prefix[g];
-    }
-    return q;
-  };
-  for (int s = tid; s < a.S; s += 1024) {
+    Work w;
     int row, col;
     bool shares;
-    const Work w = work_of<kShared>(a, entry(s, row, col, shares));
+  };
+  auto entry = [&](int s) {
+    Entry x;
+    if (s >= a.S) {
+      const int g = s - a.S;
+      x.shares = true;
+      x.row = min(g_lead[g], a.S - 1);
+      x.col = 0;
+      x.q = group_seq(g);
+      if (g_prefix[g] == 0) x.q.n = 0;
+    } else {
+      x.q = whole(s);
+      const int g = sharing(s, x.q);
+      x.shares = g >= 0;
+      x.row = s;
+      x.col = x.shares ? g_prefix[g] / kBlk : 0;
+      x.q.kv_len -= x.col * kBlk;
+      x.q.pos -= x.col * kBlk;
+    }
+    x.w = work_of<kShared>(a, x.q);
+    return x;
+  };
+  Entry own = {};
+  if (tid < a.S + a.P) own = entry(tid);
+  auto entry_of = [&](int s) { return s == tid ? own : entry(s); };
+  for (int s = tid; s < a.S; s += kPlanThreads) {
+    const Work w = entry_of(s).w;
     work += static_cast<int64_t>(w.tiles) * w.blocks;
   }
   work = warp_sum(work);
@@ -1354,64 +1391,82 @@ __global__ void __launch_bounds__(1024) shared_plan_kernel(const SharedArgs a) {
   // Items by size, largest first, in classes of 1 .. 15 key tiles, then of half powers of
   // two; a class's counter holds its entries (high word) and items.
   auto parts_for = [&](int s, const Seq &q, const Work &w) {
-    return parts_of(a, q, w.tiles, work, s >= a.S ? a.pre_split : a.n_split);
+    return w.blocks == 0 ? 1 : parts_of(a, q, w.tiles, work, s >= a.S ? a.pre_split : a.n_split);
   };
   auto class_of = [&](int size) {
-    if (size < 16) return size;
     const int log = 31 - __clz(size);
-    return min(16 + 2 * (log - 4) + ((size >> (log - 1)) & 1), kClasses - 1);
+    return kClasses - 1 -
+           (size < 16 ? size : min(16 + 2 * (log - 4) + ((size >> (log - 1)) & 1), kClasses - 1));
   };
   auto count_of = [&](int blocks, int parts) {
     return (1ull << 32) + static_cast<unsigned long long>(blocks * parts * a.Hk);
   };
-  for (int s = tid; s < a.S + a.P; s += 1024) {
-    int row, col;
-    bool shares;
-    const Seq q = entry(s, row, col, shares);
-    const Work w = work_of<kShared>(a, q);
-    if (w.blocks == 0) continue;
-    const int parts = parts_for(s, q, w);
-    atomicAdd(&classes[class_of(part_size(w.tiles, parts))], count_of(w.blocks, parts));
+  for (int s = tid; s < a.S + a.P; s += kPlanThreads) {
+    const Entry x = entry_of(s);
+    if (x.w.blocks == 0) continue;
+    const int parts = parts_for(s, x.q, x.w);
+    atomicAdd(&classes[class_of(part_size(x.w.tiles, parts))], count_of(x.w.blocks, parts));
   }
   __syncthreads();
-  if (tid == 0) {
-    unsigned long long at = 0;
-    for (int c = kClasses - 1; c >= 0; --c) {
-      const unsigned long long n = classes[c];
-      classes[c] = at;
-      at += n;
+  if (tid < kClasses) {
+    const unsigned long long n = classes[tid];
+    unsigned long long sum = n;
+#pragma unroll
+    for (int off = 1; off < kClasses; off <<= 1) {
+      const unsigned long long below = __shfl_up_sync(~0u, sum, off);
+      if (tid >= off) sum += below;
     }
-    const int entries = static_cast<int>(at >> 32);
-    *a.head = entries;
-    a.first[entries] = static_cast<int>(at);
+    classes[tid] = sum - n;
+    if (tid == kClasses - 1) {
+      n_entries = static_cast<int>(sum >> 32);
+      *a.head = n_entries;
+      a.first[n_entries] = static_cast<int>(sum);
+    }
   }
   __syncthreads();
-  for (int s = tid; s < a.S + a.P; s += 1024) {
-    int row, col;
-    bool shares;
-    const Seq q = entry(s, row, col, shares);
-    const Work w = work_of<kShared>(a, q);
-    const int parts = w.blocks == 0 ? 1 : parts_for(s, q, w);
+  for (int s = tid; s < a.S + a.P; s += kPlanThreads) {
+    const Entry x = entry_of(s);
+    const int parts = parts_for(s, x.q, x.w);
     if (s < a.S) {
       int pre = 0;
-      if (shares) {
+      if (x.shares) {
         // Every block of the prefix cuts its tiles alike.
         const Seq p = group_seq(group_of(s));
         const Work pw = work_of<kShared>(a, p);
         const int size = part_size(pw.tiles, parts_for(a.S, p, pw));
         pre = (pw.tiles + size - 1) / size;
       }
-      a.seq[2 * s] = make_int4(q.begin, q.n, q.kv_len, q.pos);
+      a.seq[2 * s] = make_int4(x.q.begin, x.q.n, x.q.kv_len, x.q.pos);
       a.seq[2 * s + 1] = make_int4(parts, pre, 0, 0);
     }
-    if (w.blocks == 0) continue;
+    if (x.w.blocks == 0) continue;
     const unsigned long long at =
-        atomicAdd(&classes[class_of(part_size(w.tiles, parts))], count_of(w.blocks, parts));
+        atomicAdd(&classes[class_of(part_size(x.w.tiles, parts))], count_of(x.w.blocks, parts));
     const int i = static_cast<int>(at >> 32);
     a.first[i] = static_cast<int>(at);
-    a.rec[2 * i] = make_int4(q.begin, q.n, q.kv_len, q.pos);
-    a.rec[2 * i + 1] = make_int4(row, col, parts,
-                                 s >= a.S ? a.n_split : shares || parts > 1 ? 0 : -1);
+    if (i < kPlanThreads) firsts[i] = static_cast<int>(at);
+    a.rec[2 * i] = make_int4(x.q.begin, x.q.n, x.q.kv_len, x.q.pos);
+    a.rec[2 * i + 1] = make_int4(x.row, x.col, parts,
+                                 s >= a.S ? a.n_split : x.shares || parts > 1 ? 0 : -1);
+  }
+  __syncthreads();
+  // The first item of each CTA, decoded.  (Every entry has an item: they are among the
+  // first entries.)
+  for (int w = tid; w < a.ctas && w < a.first[n_entries]; w += kPlanThreads) {
+    int lo = 0, n = min(n_entries, kPlanThreads);
+    while (n > 1) {
+      const int half = n / 2;
+      if (firsts[lo + half] <= w) lo += half, n -= half;
+      else n = half;
+    }
+    Item it = {};
+    Gap gap;
+    decode_entry(a, a.rec[2 * lo], a.rec[2 * lo + 1], w - firsts[lo], it, gap);
+    int4 x[4];
+    memcpy(x, &it, sizeof it);
+    x[3].w = gap.skip;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a.start[4 * w + i] = x[i];
   }
 }
 
@@ -1433,8 +1488,10 @@ cudaError_t launch(const CUtensorMap &tq, const KvMap<PAGED, FORM> &tk,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
   if (e != cudaSuccess) return e;
   int64_t n_items = static_cast<int64_t>(a.n_vblocks) * a.n_split * a.Hk;   // a bound
-  if constexpr (FORM == kShared)
+  if constexpr (FORM == kShared) {
+    sms = a.ctas;
     n_items += (static_cast<int64_t>(a.T) / (2 * a.tpb) + a.P) * a.pre_split * a.Hk;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(n_items < sms ? n_items : sms));
   cfg.blockDim = dim3(kThreads);
@@ -1574,6 +1631,7 @@ SharedLayout shared_layout(int T, int S, int P, int H, int Hk, int max_blocks) {
   l.seq = take(static_cast<size_t>(S) * 2 * sizeof(int4));
   l.first = take((entries + 1) * sizeof(int));
   l.head = take(sizeof(int));
+  l.start = take(static_cast<size_t>(kSharedMaxCtas) * sizeof(int4) * 4);
   return l;
 }
 
@@ -1592,7 +1650,11 @@ cudaError_t launch_paged_shared(const CUtensorMap &tq, const CUtensorMap &tk,
   a.seq = reinterpret_cast<int4 *>(workspace + l.seq);
   a.first = reinterpret_cast<int *>(workspace + l.first);
   a.head = reinterpret_cast<int *>(workspace + l.head);
+  a.start = reinterpret_cast<int4 *>(workspace + l.start);
   a.cu_groups = cu_groups, a.prefix_lens = prefix_lens, a.P = P;
+  cudaError_t e = sm_count(&a.ctas);
+  if (e != cudaSuccess) return e;
+  a.ctas = std::min(a.ctas, kSharedMaxCtas);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(1024);
@@ -1602,7 +1664,7 @@ cudaError_t launch_paged_shared(const CUtensorMap &tq, const CUtensorMap &tk,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_plan_kernel, a);
+  e = cudaLaunchKernelEx(&cfg, shared_plan_kernel, a);
   if (e != cudaSuccess) return e;
   return launch<128, false, true, kShared>(tq, tk, tv, a, stream);
 }

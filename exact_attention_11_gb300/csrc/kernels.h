@@ -244,10 +244,10 @@ cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
 
 // Paged, with groups of sequences that share a prefix: P groups, cu_groups [P + 1] over
 // the sequences, prefix_lens [P].  The workspace's parts are bytes from its start.
-constexpr int kSharedMaxGroups = 1024;
+constexpr int kSharedMaxGroups = 1024, kSharedMaxCtas = 256;   // (an sm_103a GPU has 152 SMs)
 struct SharedLayout {
   int split, pre_split;       // most partitions of a context, of a prefix
-  size_t rows, sums, rec, seq, first, head, bytes;
+  size_t rows, sums, rec, seq, first, head, start, bytes;
 };
 SharedLayout shared_layout(int T, int S, int P, int H, int Hk, int max_blocks);
 cudaError_t launch_paged_shared(const CUtensorMap &tq, const CUtensorMap &tk,
