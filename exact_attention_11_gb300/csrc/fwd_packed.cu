@@ -978,7 +978,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int w = 0; w < 4; ++w) {
               const uint32_t bits = low_bits(lim_j - 32 * w) & (~low_bits(low_j - 32 * w) |
                                                                 low_bits(first_j - 32 * w));
-              if (__all_sync(~0u, bits == ~0u)) continue;
 #pragma unroll
               for (int c = 0; c < 32; ++c)
                 if (((bits >> c) & 1u) == 0u) sv[w][c] = __float_as_uint(-INFINITY);
