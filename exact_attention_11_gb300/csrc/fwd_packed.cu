@@ -1116,9 +1116,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t *c16 = &ov[q >> 1][(q & 1) * 16];
           uint32_t v[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            v[e] = pack2<F16>(__uint_as_float(c16[2 * e]) * inv_l,
-                              __uint_as_float(c16[2 * e + 1]) * inv_l);
+          for (int e = 0; e < 8; ++e) {
+            const float2 x = f2_split(fmul2(
+                f2(__uint_as_float(c16[2 * e]), __uint_as_float(c16[2 * e + 1])), f2(inv_l, inv_l)));
+            v[e] = pack2<F16>(x.x, x.y);
+          }
           // A row that sees no key is zero whatever its accumulator holds.  Packed, a
           // query sees itself at least: a sum of 0 means scores that are all -inf, NaN
           // (as inv_l makes it; without the select the compiler's registers cost 1%).
