@@ -8,7 +8,9 @@ kernels of ``libfattn.so``.  ``forward``, ``backward`` and ``paged_decode`` are 
 conveniences that allocate the outputs and pass the tensors' device pointers; so
 are ``qk_norm_rope``, ``qk_norm_rope_cache``, ``qk_norm_rope_backward`` (norm and
 rotation of queries and keys), ``forward_packed``, ``backward_packed`` (prompts of
-different lengths) and ``paged_prefill`` (chunks of new tokens over a paged cache).
+different lengths), ``paged_prefill`` (chunks of new tokens over a paged cache), their
+forms with a sliding window (``forward_packed_window``, ``backward_packed_window``,
+``paged_prefill_window``) and ``paged_prefill_shared`` (sequences that share a prefix).
 
 There is no fallback: if ``libfattn.so`` is missing, cannot be loaded, or the
 device is not an sm_103 GPU, the calls raise.
@@ -1072,6 +1074,6 @@ def _paged_prefill(name, q, k_cache, v_cache, block_tables, context_lens, cu_seq
         if nbytes:
             workspace = _torch().empty(nbytes, dtype=_torch().uint8, device=q.device)
     _check(name, getattr(lib, name)(
-        *ptrs, out_ptr, S, T, H, Hk, q.shape[2], bs, nb, mb, qs, scale, *mask, _ptr(workspace), nbytes,
-        _raw_stream(dev)))
+        *ptrs, out_ptr, S, T, H, Hk, q.shape[2], bs, nb, mb, qs, scale, *mask, _ptr(workspace),
+        nbytes, _raw_stream(dev)))
     return out

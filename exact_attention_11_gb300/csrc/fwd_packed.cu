@@ -7,6 +7,9 @@
 //   paged    a chunk of new queries per sequence, q [T, H, d], against the
 //            paged cache that holds the sequence's whole context (the chunk's
 //            own keys included): query i of n sees keys 0 .. ctx - n + i.
+// Each has a form with a sliding window and first tokens that stay visible (kWindow:
+// position p sees keys j <= p with j > p - window or j < sinks), and the paged one a form
+// for groups of sequences that share a prefix's cache blocks (kShared).
 //
 // What is computed per row: O = softmax(scale q K^T) V over the visible keys,
 // key tile by key tile with the running maximum and sum of eqs. (2)-(4) of
@@ -45,6 +48,15 @@
 //    short ones would finish alone: a block's context is then cut into equal
 //    partitions (parts_of); each writes its unnormalised fp32 rows and (max, sum),
 //    and paged_merge_kernel joins them (eq. (4)).
+//  * kWindow: a block of queries visits the keys from the first that its first query sees
+//    on, and before them the cells of 16 keys that hold first tokens, which share the
+//    first key tile with the window's start (8 prompts up to 8192, window 1024, 4 first
+//    tokens: 260 us; with a key tile of their own 272).  Inside an item positions count
+//    along that list, so only the copies' addresses and the mask's lower bound differ.
+//  * kShared: a group's prefix is walked by the rows of all its sequences as if they were
+//    one sequence's, and what each has behind it on its own; both write partial rows, which
+//    the merge joins.  The items of up to 112 sequences and groups are numbered by every
+//    CTA for itself, of more by a kernel of one block ahead.
 //
 // What bounds it: for long prompts the tensor pipe and the softmax chain (S out of
 // TMEM, exponentials, P back) of a two-tile step, 1.4 us where the MMAs alone take
@@ -54,7 +66,15 @@
 // to 4096 tokens, 32 / 8 heads, d = 128, causal, 182 us (1497 TFLOP/s); one of 16384,
 // 8 / 1 heads, fp16, 330 us (1665); 32 prompts up to 200, 16 heads, d = 64, 17 us;
 // chunks of 4 x 1024 tokens over 8192, 345 us (1494 TFLOP/s), up to 1024 over up to
-// 16384, 94 us; 64 single tokens over 4096, 180 us (6.0 TB/s).
+// 16384, 93 us; 64 single tokens over 4096, 180 us (6.0 TB/s).  Windows: 8 prompts up to
+// 8192, 32 / 8 heads, d = 128, window 1024: 260 us (1230 TFLOP/s; a block's nine key tiles
+// take 1.5 us each, its start and end 3); one of 16384, 8 / 1 heads, fp16, window 4000,
+// 150 us (1605); 64 single tokens, window 4096, 182 us (5.9 TB/s); chunks up to 2048 over
+// up to 32768, window 4096, 179 us (1370 TFLOP/s).  Shared prefixes, single tokens, 32 / 8
+// heads: 64 sequences behind 8192 tokens, up to 512 of their own, 41 us (2.4 TB/s: start,
+// the chains of an SM's four or five short items, merge; 314 without sharing); 256 behind
+// 32768, up to 2048 of their own, 283 us (4.3 TB/s; first the prefix, bound by the tensor
+// cores, 65 us, then the rest at 5.8 TB/s; 4579 without).
 // Rounding: P to the element type before P V, O once at the end; scores, maxima, sums,
 // partial rows and their merge are fp32.
 #include <cuda.h>
@@ -63,6 +83,7 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 #include <cstring>
 #include <type_traits>
@@ -212,6 +233,7 @@ struct SharedArgs : Args {
   const int *cu_groups, *prefix_lens;
   int P, pre_split;             // groups; most partitions of a prefix
   int ctas;                     // CTAs that have their first item in `start`
+  int planned;                  // 0: few sequences, which the CTAs number themselves
   int *head;                    // number of entries of `first` and `rec`
   int *first;                   // [entries + 1]: their first items, heaviest first
   int4 *rec;                    // [entries][2]: begin, n, kv_len, pos;
@@ -416,7 +438,6 @@ __device__ __forceinline__ bool decode_shared(const SharedArgs &a, int w, Item &
 template <bool PAGED, int FORM>
 __device__ __forceinline__ bool decode_item(const FormArgs<FORM> &a, const Misc *m, int n_items,
                                             int w, Item &it, Gap &gap) {
-  if constexpr (FORM == kShared) return decode_shared(a, w, it, gap);
   const int tb = 2 * a.tpb, u = n_items - 1 - w;
   int s, blk, parts = 1;
   Seq q;
@@ -550,6 +571,233 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t ph) {
   }
 }
 
+// What a call with shared prefixes walks.  A sequence shares its group's prefix if all of
+// that lies before its new tokens; sequences that do are walked behind it only, and the
+// prefix, read through the table of the first of them, is walked by all rows of the group
+// together.  Prefixes that save less than they cost (partial rows, the start of their
+// items) are not shared.
+struct PlanEntry {              // entry s: sequence s, or, from S on, group s - S
+  Seq q;                        // its rows and keys
+  Work w;
+  int row, col;                 // table row, first table column
+  int parts, slot;              // partitions, the first one's place in ws_o, or -1
+  int group;                    // that whose prefix the sequence shares, or -1
+};
+// By all THREADS threads of a block.  The thread's first sequence stays in registers; with
+// that, and the groups, global memory is read once, up to THREADS sequences.
+template <int THREADS, int GROUPS>
+struct Planner {
+  struct Scratch {
+    int g_first[GROUPS + 1], g_prefix[GROUPS], g_lead[GROUPS], g_blocks[GROUPS];
+    int begins[THREADS + 1];    // of the first sequences
+    unsigned long long work;
+  };
+  const SharedArgs &a;
+  Scratch &m;
+  const int tid;
+  Seq mine;
+  PlanEntry own;
+  int64_t work;
+
+  __device__ Planner(const SharedArgs &args, Scratch &scratch)
+      : a(args), m(scratch), tid(threadIdx.x), mine{}, own{}, work(0) {
+    if (tid < a.S) {
+      mine = global_seq<true>(a, tid);
+      m.begins[tid] = mine.begin;
+      m.begins[tid + 1] = seq_begin(a, tid + 1);
+    }
+    for (int g = tid; g <= a.P; g += THREADS) {
+      m.g_first[g] = a.P > 0 ? clampi(a.cu_groups[g], 0, a.S) : 0;
+      if (g == a.P) break;
+      m.g_prefix[g] = clampi(a.prefix_lens[g], 0, a.max_blocks * kBlk) / kBlk * kBlk;
+      m.g_lead[g] = a.S;
+      m.g_blocks[g] = 0;
+    }
+    if (tid == 0) m.work = 0;
+    __syncthreads();
+    for (int s = tid; s < a.S; s += THREADS) {
+      const Seq q = whole(s);
+      const int g = sharing(s, q);
+      if (g < 0) continue;
+      atomicMin(&m.g_lead[g], s);
+      atomicAdd(&m.g_blocks[g], work_of<kShared>(a, q).blocks);
+    }
+    __syncthreads();
+    int64_t sum = 0;
+    for (int g = tid; g < a.P; g += THREADS) {
+      const Seq q = group_seq(g);
+      const Work w = work_of<kShared>(a, q);
+      const float saved = static_cast<float>(m.g_blocks[g] - w.blocks) * w.tiles;
+      const float cost = kPartFixed * w.blocks + 2.f * kPartRow * q.n * a.G;
+      if (m.g_lead[g] == a.S || !(saved > cost))
+        m.g_prefix[g] = 0;
+      else
+        sum += static_cast<int64_t>(w.tiles) * w.blocks;
+    }
+    __syncthreads();
+    if (tid < a.S + a.P) own = entry(tid);
+    for (int s = tid; s < a.S; s += THREADS) {
+      const Work w = s == tid ? own.w : entry(s).w;
+      sum += static_cast<int64_t>(w.tiles) * w.blocks;
+    }
+    sum = warp_sum(sum);
+    if ((tid & 31) == 0) atomicAdd(&m.work, static_cast<unsigned long long>(sum));
+    __syncthreads();
+    work = static_cast<int64_t>(m.work);
+    if (tid < a.S + a.P) cut(tid, own);
+  }
+  __device__ Seq whole(int s) const { return s == tid ? mine : global_seq<true>(a, s); }
+  __device__ int begin_of(int s) const { return s <= THREADS ? m.begins[s] : seq_begin(a, s); }
+  // The group of the whole sequence q if it shares the prefix, else -1.  (A sequence is in
+  // the last group that begins at or before it, if in any.)
+  __device__ int sharing(int s, const Seq &q) const {
+    int lo = 0, n = a.P;
+    while (n > 0) {
+      const int half = n / 2;
+      if (m.g_first[lo + half] <= s) lo += half + 1, n -= half + 1;
+      else n = half;
+    }
+    if (lo == 0 || s >= m.g_first[lo]) return -1;
+    const int prefix = m.g_prefix[lo - 1];
+    return q.n > 0 && prefix > 0 && q.pos >= prefix ? lo - 1 : -1;
+  }
+  // The rows of a group's prefix; all see all of it.
+  __device__ Seq group_seq(int g) const {
+    Seq q;
+    q.begin = begin_of(m.g_first[g]);
+    q.n = max(begin_of(m.g_first[g + 1]) - q.begin, 0);
+    q.kv_len = m.g_prefix[g];
+    q.pos = kSeesAll;
+    return q;
+  }
+  // (Without its partitions.)
+  __device__ PlanEntry entry(int s) const {
+    PlanEntry x;
+    x.group = -1;
+    if (s >= a.S) {
+      const int g = s - a.S;
+      x.row = min(m.g_lead[g], a.S - 1);
+      x.col = 0;
+      x.q = group_seq(g);
+      if (m.g_prefix[g] == 0) x.q.n = 0;
+    } else {
+      x.q = whole(s);
+      x.group = sharing(s, x.q);
+      x.row = s;
+      x.col = x.group >= 0 ? m.g_prefix[x.group] / kBlk : 0;
+      x.q.kv_len -= x.col * kBlk;
+      x.q.pos -= x.col * kBlk;
+    }
+    x.w = work_of<kShared>(a, x.q);
+    return x;
+  }
+  __device__ void cut(int s, PlanEntry &x) const {
+    const bool prefix = s >= a.S;
+    x.parts = x.w.blocks == 0
+                  ? 1
+                  : parts_of(a, x.q, x.w.tiles, work, prefix ? a.pre_split : a.n_split);
+    x.slot = prefix ? a.n_split : x.group >= 0 || x.parts > 1 ? 0 : -1;
+  }
+  __device__ PlanEntry entry_of(int s) const {
+    if (s == tid) return own;
+    PlanEntry x = entry(s);
+    cut(s, x);
+    return x;
+  }
+  // What the merge has to know of sequence s.
+  __device__ void put_seq(int s, const PlanEntry &x) const {
+    int pre = 0;
+    if (x.group >= 0) {
+      // Every block of the prefix cuts its tiles alike.
+      const PlanEntry p = entry_of(a.S + x.group);
+      const int size = part_size(p.w.tiles, p.parts);
+      pre = (p.w.tiles + size - 1) / size;
+    }
+    a.seq[2 * s] = make_int4(x.q.begin, x.q.n, x.q.kv_len, x.q.pos);
+    a.seq[2 * s + 1] = make_int4(x.parts, pre, 0, 0);
+  }
+};
+
+// The numbered entries of a call with few sequences, in shared memory in place of
+// Misc's: every CTA finds the same ones for itself (64 requests behind 8192 tokens:
+// 40.8 us, 44.0 with a kernel ahead that numbers them).
+struct PlanTable {
+  int entries, items;
+  int begins[kCachedSeqs + 1];  // first rows of the sequences
+  int first[kCachedSeqs + 1];   // first items, heaviest entry first
+  int kv_len[kCachedSeqs], col[kCachedSeqs];
+  int16_t parts[kCachedSeqs];   // negative: rows are written directly
+  uchar4 of[kCachedSeqs];       // first and last sequence of its rows (+ 1), table row, prefix?
+};
+constexpr int kPlanTableAt = 8 * kNumBars + offsetof(Misc, seq);
+static_assert(kPlanTableAt + sizeof(PlanTable) <= kBarArea && kPlanTableAt % 8 == 0, "barrier area");
+
+// By the whole block; scratch: the ring's memory, ahead of its first copies.
+__device__ __forceinline__ void plan_items(const SharedArgs &a, PlanTable *m, uint8_t *scratch) {
+  using Plan = Planner<kThreads, kCachedSeqs>;
+  struct Work {
+    Plan::Scratch plan;
+    int key[kCachedSeqs], count[kCachedSeqs];
+  };
+  Work &x = *reinterpret_cast<Work *>(scratch);
+  Plan plan(a, x.plan);
+  const int tid = threadIdx.x, n = a.S + a.P;
+  const PlanEntry &e = plan.own;
+  // Key: key tiles of an item, then the index; entries without rows come last.
+  int key = -1;
+  if (tid < n) {
+    if (e.w.blocks > 0)
+      key = min(part_size(e.w.tiles, e.parts), (1 << 23) - 1) * 128 + tid;
+    x.key[tid] = key;
+    if (blockIdx.x == 0 && tid < a.S) plan.put_seq(tid, e);
+  }
+  if (tid <= a.S) m->begins[tid] = x.plan.begins[tid];
+  __syncthreads();
+  int rank = 0;
+  if (tid < n) {
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) rank += x.key[j] > key ? 1 : 0;
+    if (key >= 0) {
+      x.count[rank] = e.w.blocks * e.parts * a.Hk;
+      const int g = tid - a.S;
+      m->kv_len[rank] = e.q.kv_len;
+      m->col[rank] = e.col;
+      m->parts[rank] = static_cast<int16_t>(e.slot < 0 ? -e.parts : e.parts);
+      m->of[rank] = g >= 0 ? make_uchar4(x.plan.g_first[g], x.plan.g_first[g + 1], e.row, 1)
+                           : make_uchar4(tid, tid + 1, e.row, 0);
+    }
+  }
+  const int entries = __syncthreads_count(key >= 0);
+  if (tid < 32) {
+    int carry = 0;
+    for (int base = 0; base < entries; base += 32) {
+      const int c = base + tid < entries ? x.count[base + tid] : 0;
+      int sum = c;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int below = __shfl_up_sync(~0u, sum, off);
+        if (tid >= off) sum += below;
+      }
+      if (base + tid < entries) m->first[base + tid] = carry + sum - c;
+      carry += __shfl_sync(~0u, sum, 31);
+    }
+    if (tid == 0) m->entries = entries, m->items = carry;
+  }
+  fence_proxy_async_smem();     // the ring's copies come after what was written there
+}
+
+__device__ __forceinline__ bool decode_planned(const SharedArgs &a, const PlanTable *m, int w,
+                                               Item &it, Gap &gap) {
+  const int at = warp_search(m->entries, w, [&](int i) { return m->first[i]; });
+  const uchar4 of = m->of[at];
+  const int begin = m->begins[of.x], n = max(m->begins[of.y] - begin, 0), kv_len = m->kv_len[at];
+  const int parts = m->parts[at];
+  return decode_entry(a, make_int4(begin, n, kv_len, of.w ? kSeesAll : kv_len - n),
+                      make_int4(of.z, m->col[at], abs(parts),
+                                of.w ? a.n_split : parts < 0 ? -1 : 0),
+                      w - m->first[at], it, gap);
+}
+
 template <int D, bool F16, bool PAGED, int FORM>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_packed_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -617,6 +865,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // may be scheduled from here on; it waits for this grid in turn.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (PAGED && threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  PlanTable *table = reinterpret_cast<PlanTable *>(smem + C::kBar + kPlanTableAt);
+  if constexpr (FORM == kShared)
+    if (a.planned == 0) plan_items(a, table, smem + C::kRing);
   const bool cached = FORM != kShared && a.S <= kCachedSeqs;
   if (cached)
     for (int i = threadIdx.x; i <= a.S; i += kThreads)
@@ -639,7 +890,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const Misc *numbered = cached ? misc : nullptr;
       int n_items = cached ? misc->first[a.S] : a.n_vblocks * a.Hk;
-      if constexpr (FORM == kShared) n_items = a.first[*a.head];
+      if constexpr (FORM == kShared) n_items = a.planned ? a.first[*a.head] : table->items;
       int e = 0, nq = 0;        // tiles and Q tiles copied so far
       bool ok = true;
       int w = blockIdx.x;       // the first item is the CTA's own; the rest are claimed
@@ -682,7 +933,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             nxt.live = 0;
             return;
           }
-          if (decode_item<PAGED, FORM>(a, numbered, n_items, w, nxt, nxt_gap)) break;
+          bool some;
+          if constexpr (FORM == kShared)
+            some = a.planned ? decode_shared(a, w, nxt, nxt_gap)
+                             : decode_planned(a, table, w, nxt, nxt_gap);
+          else
+            some = decode_item<PAGED, FORM>(a, numbered, n_items, w, nxt, nxt_gap);
+          if (some) break;
           claim();
           w = claimed();
         }
@@ -697,21 +954,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return __shfl_sync(~0u, good, 0);
       };
+      bool found = false;
       if constexpr (FORM == kShared) {
-        // The CTA's own item comes decoded (found like the others, it takes 0.6 us longer).
-        nxt.live = 0;
-        if (w < n_items) {
-          static_assert(sizeof(Item) == 60, "four words of 16 bytes with the table column");
-          int4 x[4];
+        if (a.planned) {
+          // The CTA's own item comes decoded (found like the others, it takes 0.6 us longer).
+          found = true;
+          nxt.live = 0;
+          if (w < n_items) {
+            static_assert(sizeof(Item) == 60, "four words of 16 bytes with the table column");
+            int4 x[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = a.start[4 * w + i];
-          memcpy(&nxt, x, sizeof nxt);
-          nxt_gap = {0, x[3].w};
-          nxt_id = ids_of(nxt, nxt_gap, nxt.kt0);
+            for (int i = 0; i < 4; ++i) x[i] = a.start[4 * w + i];
+            memcpy(&nxt, x, sizeof nxt);
+            nxt_gap = {0, x[3].w};
+            nxt_id = ids_of(nxt, nxt_gap, nxt.kt0);
+          }
         }
-      } else {
-        find();
       }
+      if (!found) find();
       for (int k = 0; ok; ++k) {
         const Item it = nxt;
         const Gap gap = nxt_gap;
@@ -1272,141 +1532,32 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
   }
 }
 
-// Numbers the items of a call with shared prefixes (one block).  A sequence shares its
-// group's prefix if all of that lies before its new tokens; sequences that do are
-// walked behind it only, and the prefix, read through the table of the first of them,
-// is walked by all rows of the group together.  Prefixes that save less than they cost
-// (partial rows, the start of their items) are not shared.
-constexpr int kMaxGroups = kSharedMaxGroups, kClasses = 32, kPlanThreads = 1024;
+// Numbers the items of a call with shared prefixes of many sequences (one block).
+constexpr int kPlanThreads = 1024, kClasses = 32;
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedArgs a) {
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ int g_first[kMaxGroups + 1], g_prefix[kMaxGroups], g_lead[kMaxGroups];
-  __shared__ int g_blocks[kMaxGroups];
-  __shared__ int begins[kPlanThreads + 1];                 // of the first sequences
+  using Plan = Planner<kPlanThreads, kSharedMaxGroups>;
+  __shared__ Plan::Scratch scratch;
   __shared__ int firsts[kPlanThreads];                     // of the first entries
-  __shared__ unsigned long long classes[kClasses], work_sum;
+  __shared__ unsigned long long classes[kClasses];
   __shared__ int n_entries;
   const int tid = threadIdx.x;
-  // The thread's first sequence stays in registers; with that, and the groups, global
-  // memory is read once, up to 1024 sequences.
-  Seq mine = {};
-  if (tid < a.S) mine = global_seq<true>(a, tid);
-  if (tid < a.S) begins[tid] = mine.begin, begins[tid + 1] = seq_begin(a, tid + 1);
-  for (int g = tid; g <= a.P; g += kPlanThreads) {
-    g_first[g] = a.P > 0 ? clampi(a.cu_groups[g], 0, a.S) : 0;
-    if (g == a.P) break;
-    g_prefix[g] = clampi(a.prefix_lens[g], 0, a.max_blocks * kBlk) / kBlk * kBlk;
-    g_lead[g] = a.S;
-    g_blocks[g] = 0;
-  }
   if (tid < kClasses) classes[tid] = 0;
-  if (tid == 0) work_sum = 0;
-  __syncthreads();
-  auto whole = [&](int s) { return s == tid ? mine : global_seq<true>(a, s); };
-  auto begin_of = [&](int s) { return s <= kPlanThreads ? begins[s] : seq_begin(a, s); };
-  // The group of sequence s, or -1 (the last that begins at or before it, if s is in it).
-  auto group_of = [&](int s) {
-    int lo = 0, n = a.P;
-    while (n > 0) {
-      const int half = n / 2;
-      if (g_first[lo + half] <= s) lo += half + 1, n -= half + 1;
-      else n = half;
-    }
-    return lo > 0 && s < g_first[lo] ? lo - 1 : -1;
-  };
-  // Its group, if the whole sequence q shares the prefix, else -1.
-  auto sharing = [&](int s, const Seq &q) {
-    const int g = group_of(s);
-    return g >= 0 && q.n > 0 && g_prefix[g] > 0 && q.pos >= g_prefix[g] ? g : -1;
-  };
-  for (int s = tid; s < a.S; s += kPlanThreads) {
-    const Seq q = whole(s);
-    const int g = sharing(s, q);
-    if (g < 0) continue;
-    atomicMin(&g_lead[g], s);
-    atomicAdd(&g_blocks[g], work_of<kShared>(a, q).blocks);
-  }
-  __syncthreads();
-  // The rows of a group's prefix; all see all of it.
-  auto group_seq = [&](int g) {
-    Seq q;
-    q.begin = begin_of(g_first[g]);
-    q.n = max(begin_of(g_first[g + 1]) - q.begin, 0);
-    q.kv_len = g_prefix[g];
-    q.pos = kSeesAll;
-    return q;
-  };
-  int64_t work = 0;
-  for (int g = tid; g < a.P; g += kPlanThreads) {
-    const Seq q = group_seq(g);
-    const Work w = work_of<kShared>(a, q);
-    const float saved = static_cast<float>(g_blocks[g] - w.blocks) * w.tiles;
-    const float cost = kPartFixed * w.blocks + 2.f * kPartRow * q.n * a.G;
-    if (g_lead[g] == a.S || !(saved > cost))
-      g_prefix[g] = 0;
-    else
-      work += static_cast<int64_t>(w.tiles) * w.blocks;
-  }
-  __syncthreads();
-  // What entry s walks -- sequence s, or, from S on, group s - S: its rows and keys, where
-  // they are found, and whether its rows are partial.
-  struct Entry {
-    Seq q;
-    Work w;
-    int row, col;
-    bool shares;
-  };
-  auto entry = [&](int s) {
-    Entry x;
-    if (s >= a.S) {
-      const int g = s - a.S;
-      x.shares = true;
-      x.row = min(g_lead[g], a.S - 1);
-      x.col = 0;
-      x.q = group_seq(g);
-      if (g_prefix[g] == 0) x.q.n = 0;
-    } else {
-      x.q = whole(s);
-      const int g = sharing(s, x.q);
-      x.shares = g >= 0;
-      x.row = s;
-      x.col = x.shares ? g_prefix[g] / kBlk : 0;
-      x.q.kv_len -= x.col * kBlk;
-      x.q.pos -= x.col * kBlk;
-    }
-    x.w = work_of<kShared>(a, x.q);
-    return x;
-  };
-  Entry own = {};
-  if (tid < a.S + a.P) own = entry(tid);
-  auto entry_of = [&](int s) { return s == tid ? own : entry(s); };
-  for (int s = tid; s < a.S; s += kPlanThreads) {
-    const Work w = entry_of(s).w;
-    work += static_cast<int64_t>(w.tiles) * w.blocks;
-  }
-  work = warp_sum(work);
-  if ((tid & 31) == 0) atomicAdd(&work_sum, static_cast<unsigned long long>(work));
-  __syncthreads();
-  work = static_cast<int64_t>(work_sum);
+  Plan plan(a, scratch);
   // Items by size, largest first, in classes of 1 .. 15 key tiles, then of half powers of
   // two; a class's counter holds its entries (high word) and items.
-  auto parts_for = [&](int s, const Seq &q, const Work &w) {
-    return w.blocks == 0 ? 1 : parts_of(a, q, w.tiles, work, s >= a.S ? a.pre_split : a.n_split);
-  };
   auto class_of = [&](int size) {
     const int log = 31 - __clz(size);
     return kClasses - 1 -
            (size < 16 ? size : min(16 + 2 * (log - 4) + ((size >> (log - 1)) & 1), kClasses - 1));
   };
-  auto count_of = [&](int blocks, int parts) {
-    return (1ull << 32) + static_cast<unsigned long long>(blocks * parts * a.Hk);
+  auto count_of = [&](const PlanEntry &x) {
+    return (1ull << 32) + static_cast<unsigned long long>(x.w.blocks * x.parts * a.Hk);
   };
   for (int s = tid; s < a.S + a.P; s += kPlanThreads) {
-    const Entry x = entry_of(s);
-    if (x.w.blocks == 0) continue;
-    const int parts = parts_for(s, x.q, x.w);
-    atomicAdd(&classes[class_of(part_size(x.w.tiles, parts))], count_of(x.w.blocks, parts));
+    const PlanEntry x = plan.entry_of(s);
+    if (x.w.blocks > 0) atomicAdd(&classes[class_of(part_size(x.w.tiles, x.parts))], count_of(x));
   }
   __syncthreads();
   if (tid < kClasses) {
@@ -1426,29 +1577,16 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
   }
   __syncthreads();
   for (int s = tid; s < a.S + a.P; s += kPlanThreads) {
-    const Entry x = entry_of(s);
-    const int parts = parts_for(s, x.q, x.w);
-    if (s < a.S) {
-      int pre = 0;
-      if (x.shares) {
-        // Every block of the prefix cuts its tiles alike.
-        const Seq p = group_seq(group_of(s));
-        const Work pw = work_of<kShared>(a, p);
-        const int size = part_size(pw.tiles, parts_for(a.S, p, pw));
-        pre = (pw.tiles + size - 1) / size;
-      }
-      a.seq[2 * s] = make_int4(x.q.begin, x.q.n, x.q.kv_len, x.q.pos);
-      a.seq[2 * s + 1] = make_int4(parts, pre, 0, 0);
-    }
+    const PlanEntry x = plan.entry_of(s);
+    if (s < a.S) plan.put_seq(s, x);
     if (x.w.blocks == 0) continue;
     const unsigned long long at =
-        atomicAdd(&classes[class_of(part_size(x.w.tiles, parts))], count_of(x.w.blocks, parts));
+        atomicAdd(&classes[class_of(part_size(x.w.tiles, x.parts))], count_of(x));
     const int i = static_cast<int>(at >> 32);
     a.first[i] = static_cast<int>(at);
     if (i < kPlanThreads) firsts[i] = static_cast<int>(at);
     a.rec[2 * i] = make_int4(x.q.begin, x.q.n, x.q.kv_len, x.q.pos);
-    a.rec[2 * i + 1] = make_int4(x.row, x.col, parts,
-                                 s >= a.S ? a.n_split : x.shares || parts > 1 ? 0 : -1);
+    a.rec[2 * i + 1] = make_int4(x.row, x.col, x.parts, x.slot);
   }
   __syncthreads();
   // The first item of each CTA, decoded.  (Every entry has an item: they are among the
@@ -1656,9 +1794,11 @@ cudaError_t launch_paged_shared(const CUtensorMap &tq, const CUtensorMap &tk,
   cudaError_t e = sm_count(&a.ctas);
   if (e != cudaSuccess) return e;
   a.ctas = std::min(a.ctas, kSharedMaxCtas);
+  a.planned = p.S + P > kCachedSeqs;
+  if (!a.planned) return launch<128, false, true, kShared>(tq, tk, tv, a, stream);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);
-  cfg.blockDim = dim3(1024);
+  cfg.blockDim = dim3(kPlanThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

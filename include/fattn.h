@@ -1,7 +1,7 @@
 /*
  * fattn.h -- C ABI of libfattn: exact scaled-dot-product attention on one
- * NVIDIA GB300 (sm_103a), dense, packed and over a paged cache, and the norm
- * and rotation of its queries and keys.
+ * NVIDIA GB300 (sm_103a), dense, packed and over a paged cache, with sliding
+ * windows and shared prefixes, and the norm and rotation of its queries and keys.
  *
  * Every call takes plain device pointers and sizes, enqueues its kernels on
  * `stream` and returns without synchronising.  Nothing here depends on any
@@ -722,16 +722,17 @@ int fa_paged_prefill_shared(const void *q, const void *k_cache, const void *v_ca
  *
  * mode 1 arms the current device: the next tensor-core forward launched on
  * it (fa_forward, fa_forward_f16, fa_forward_masked, fa_forward_fp8,
- * fa_forward_packed, fa_forward_packed_f16 or fa_paged_prefill, for head
- * dimension 64 or 128) makes its first CTA's TMA producer stop at
- * that CTA's first item, as if a copy had been lost.  The MMA warp's bounded wait for the
- * missing key tile then runs out (after about 2 s), the CTA unwinds (in-flight
- * copies and MMAs drained, tensor memory freed) and fa_device_status()
- * returns FA_ERR_TIMEOUT.  That launch's output is incomplete; the CUDA
- * context and the library stay usable.  mode 2 does the same to the next
- * fa_backward or fa_backward_packed: its main kernel's first CTA loses the K and V copies of its
- * first work item.  mode 0 disarms.  Returns FA_OK, or FA_ERR_INVALID_ARG
- * for another mode, or FA_ERR_NO_DEVICE.
+ * fa_forward_packed, fa_forward_packed_f16, fa_paged_prefill, their _window
+ * forms or fa_paged_prefill_shared, for head dimension 64 or 128) makes its
+ * first CTA's TMA producer stop at that CTA's first item, as if a copy had been
+ * lost.  The MMA warp's bounded wait for the missing key tile then runs out
+ * (after about 2 s), the CTA unwinds (in-flight copies and MMAs drained, tensor
+ * memory freed) and fa_device_status() returns FA_ERR_TIMEOUT.  That launch's
+ * output is incomplete; the CUDA context and the library stay usable.  mode 2
+ * does the same to the next fa_backward, fa_backward_packed or
+ * fa_backward_packed_window: its main kernel's first CTA loses the K and V
+ * copies of its first work item.  mode 0 disarms.  Returns FA_OK, or
+ * FA_ERR_INVALID_ARG for another mode, or FA_ERR_NO_DEVICE.
  */
 int fa_debug_inject_fault(int mode);
 
