@@ -57,12 +57,15 @@ struct SideArgs {
   // A window: the main kernel's query blocks per entry of the table, and their count.
   int2 *range;
   int *count;
-  int entries, split, window, sinks;
+  int entries, split, whole, window, sinks;
 };
 
 // A window: key block jb is seen by the query blocks from its own to `reach` further;
-// if it holds first tokens, by all later ones too, which are items of their own (entries
-// of kFar query blocks or more): one item of the whole sequence would end the call alone.
+// if it holds first tokens, by all later ones too.  In sequences of more than `whole`
+// blocks, an SM's share of the call's steps, those are items of their own (entries of
+// kFar query blocks or more): one item of the whole sequence would end the call alone
+// (one document of 16384, 8 heads, window 512: 185 us, 354 in one item; but four of 8192,
+// whose items fit in: 631, 622 so).  Far parts of four blocks: 190, 633 us.
 constexpr int kFar = 8;
 __host__ __device__ __forceinline__ int reach(int window) {
   return (BQ - 2 + window) / BQ;
@@ -74,11 +77,13 @@ __host__ __device__ __forceinline__ int far_steps(int window) {
 // Entries for the far query blocks of key block jb, of a sequence of `blocks`.
 __device__ __forceinline__ int far_entries(const SideArgs &a, int jb, int blocks) {
   const int step = far_steps(a.window);
-  return jb * BQ < a.split ? (max(blocks - 1 - jb - reach(a.window), 0) + step - 1) / step : 0;
+  if (jb * BQ >= a.split || blocks <= a.whole) return 0;
+  return (max(blocks - 1 - jb - reach(a.window), 0) + step - 1) / step;
 }
 __device__ __forceinline__ int far_entries(const SideArgs &a, int blocks) {
   int n = 0;
-  for (int jb = 0; jb < blocks && jb * BQ < a.split; ++jb) n += far_entries(a, jb, blocks);
+  if (blocks > a.whole)
+    for (int jb = 0; jb < blocks && jb * BQ < a.split; ++jb) n += far_entries(a, jb, blocks);
   return n;
 }
 
@@ -161,7 +166,7 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
         used = total(sum + 8);
         if (blk == 0) *a.count = min(used + total(sum + 24), a.entries);
         if (live) {
-          put_range(at, local * BQ < a.sinks && a.split == 0 ? blocks - 1 : last);
+          put_range(at, local * BQ < a.sinks && (a.split == 0 || blocks <= a.whole) ? blocks - 1 : last);
           int to = used + total(sum + 16);
           for (int jb = 0; jb < local; ++jb) to += far_entries(a, jb, blocks);
           const int step = far_steps(a.window), n_far = far_entries(a, local, blocks);
@@ -358,6 +363,8 @@ cudaError_t launch_bwd_packed(const PackedGradMaps &m, const PackedGrad &p, floa
     a.count = reinterpret_cast<int *>(ws + l.count);
     a.entries = static_cast<int>(l.entries), a.split = l.split;
     a.window = p.window, a.sinks = p.sinks;
+    a.whole = static_cast<int>(std::min(
+        static_cast<long long>(p.T) / BQ * (reach(p.window) + 1) * p.H / 152, 1ll << 30));
     return p.d == 128 ? launch_d<128, true>(m, p, a, sched, dev_status, fault_cta, stream)
                       : launch_d<64, true>(m, p, a, sched, dev_status, fault_cta, stream);
   }
