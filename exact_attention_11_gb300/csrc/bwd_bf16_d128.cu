@@ -51,6 +51,9 @@
 // would make the causal kernel's heaviest items too long to balance; they add
 // their dK, dV to fp32 accumulators with TMA reduces, or, with one query head
 // per key/value head, store them as the dense kernel does.
+// kWindow (fa_backward_packed_window): an item comes with the query blocks that it
+// visits; a query sees a key if it is at most window - 1 behind or among the first
+// `sinks` (bwd_tile.cuh's masks by bits, in the blocks that either border crosses).
 #include <cuda_runtime.h>
 
 #include <cmath>

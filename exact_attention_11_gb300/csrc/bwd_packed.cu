@@ -22,6 +22,12 @@
 // kernels 5.4 and 6.7 TB/s); 16 documents of 2168 tokens, d = 64: 8 + 31 + 6, 45 us, of
 // which the main kernel's start and tail are half.  An item per query head and not per
 // group: with two to sixteen steps of a group an item, 50 - 59 us and 213 - 215.
+// With a window (fa_backward_packed_window) a key block's item visits the query blocks
+// that see it only, which the table gives with it; what bounds it and how it rounds stay:
+// 4 documents of 10560 tokens in all, window 1024, 4 first tokens: 36 + 211 + 27 us, 281
+// for the call (660 TFLOP/s of visible pairs; the main kernel's 2.7 us a step of 128 x 128
+// pairs, nine steps an item, of which the window leaves 0.89, and 1.5 us between items);
+// 16 of 2168 tokens, d = 64, window 256: 8 + 28 + 6, 37 us.
 // Rounding: P and dS to bf16 before their products, as the dense kernels; sums and
 // accumulators fp32; each gradient once.
 #include <cuda_runtime.h>

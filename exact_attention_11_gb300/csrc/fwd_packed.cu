@@ -9,7 +9,7 @@
 //            own keys included): query i of n sees keys 0 .. ctx - n + i.
 // Each has a form with a sliding window and first tokens that stay visible (kWindow:
 // position p sees keys j <= p with j > p - window or j < sinks), and the paged one a form
-// for groups of sequences that share a prefix's cache blocks (kShared).
+// for groups of sequences that share a prefix's cache blocks (kShared, kSharedFew).
 //
 // What is computed per row: O = softmax(scale q K^T) V over the visible keys,
 // key tile by key tile with the running maximum and sum of eqs. (2)-(4) of
@@ -53,7 +53,7 @@
 //    first key tile with the window's start (8 prompts up to 8192, window 1024, 4 first
 //    tokens: 260 us; with a key tile of their own 272).  Inside an item positions count
 //    along that list, so only the copies' addresses and the mask's lower bound differ.
-//  * kShared: a group's prefix is walked by the rows of all its sequences as if they were
+//  * kShared, kSharedFew: a group's prefix is walked by the rows of all its sequences as if they were
 //    one sequence's, and what each has behind it on its own; both write partial rows, which
 //    the merge joins.  The items of up to 112 sequences and groups are numbered by every
 //    CTA for itself, of more by a kernel of one block ahead.
@@ -64,16 +64,16 @@
 // tokens over long contexts the 16 copies of a paged key tile and HBM; for short
 // prompts the start (5 us) and the chain of an SM's few items.  Measured: 8 prompts up
 // to 4096 tokens, 32 / 8 heads, d = 128, causal, 182 us (1497 TFLOP/s); one of 16384,
-// 8 / 1 heads, fp16, 330 us (1665); 32 prompts up to 200, 16 heads, d = 64, 17 us;
+// 8 / 1 heads, fp16, 330 us (1665); 32 prompts up to 200, 16 heads, d = 64, 16 us;
 // chunks of 4 x 1024 tokens over 8192, 345 us (1494 TFLOP/s), up to 1024 over up to
 // 16384, 93 us; 64 single tokens over 4096, 180 us (6.0 TB/s).  Windows: 8 prompts up to
 // 8192, 32 / 8 heads, d = 128, window 1024: 260 us (1230 TFLOP/s; a block's nine key tiles
 // take 1.5 us each, its start and end 3); one of 16384, 8 / 1 heads, fp16, window 4000,
 // 150 us (1605); 64 single tokens, window 4096, 182 us (5.9 TB/s); chunks up to 2048 over
 // up to 32768, window 4096, 179 us (1370 TFLOP/s).  Shared prefixes, single tokens, 32 / 8
-// heads: 64 sequences behind 8192 tokens, up to 512 of their own, 41 us (2.4 TB/s: start,
+// heads: 64 sequences behind 8192 tokens, up to 512 of their own, 40 us (2.5 TB/s: start,
 // the chains of an SM's four or five short items, merge; 314 without sharing); 256 behind
-// 32768, up to 2048 of their own, 283 us (4.3 TB/s; first the prefix, bound by the tensor
+// 32768, up to 2048 of their own, 282 us (4.3 TB/s; first the prefix, bound by the tensor
 // cores, 65 us, then the rest at 5.8 TB/s; 4579 without).
 // Rounding: P to the element type before P V, O once at the end; scores, maxima, sums,
 // partial rows and their merge are fp32.
@@ -166,7 +166,7 @@ struct Item {
 // key tile.  Cell x of the list is the sequence's cell x, or x + skip from `at` on.
 // Positions and lengths in an item count along the list: skip cells less than in the
 // sequence (every real row lies behind the gap).
-// kShared: skip is the first table column of the item's keys.
+// With shared prefixes, skip is the first table column of the item's keys.
 constexpr int kCell = 16;
 static_assert(kCell == kBlk, "a cell of the paged list is a cache block");
 struct Gap {
@@ -195,8 +195,12 @@ constexpr int kDevBadSmemBase = -2;
 
 // What a query sees: all keys of its sequence up to its own (or, packed, all of
 // them); or of those a window and the sequence's first tokens; or all of them where
-// groups of sequences share the blocks of a prefix (paged).
-enum : int { kAll = 0, kWindow = 1, kShared = 2 };
+// groups of sequences share the blocks of a prefix (paged), numbered ahead or, of few
+// sequences, by every CTA.  (Both in one kernel cost 1.5% of 256 sequences behind 32768 tokens.)
+enum : int { kAll = 0, kWindow = 1, kShared = 2, kSharedFew = 3 };
+__host__ __device__ constexpr bool is_shared(int form) {
+  return form == kShared || form == kSharedFew;
+}
 
 struct Args {
   uint16_t *o;
@@ -233,7 +237,6 @@ struct SharedArgs : Args {
   const int *cu_groups, *prefix_lens;
   int P, pre_split;             // groups; most partitions of a prefix
   int ctas;                     // CTAs that have their first item in `start`
-  int planned;                  // 0: few sequences, which the CTAs number themselves
   int *head;                    // number of entries of `first` and `rec`
   int *first;                   // [entries + 1]: their first items, heaviest first
   int4 *rec;                    // [entries][2]: begin, n, kv_len, pos;
@@ -245,7 +248,7 @@ struct SharedArgs : Args {
 };
 template <int FORM>
 using FormArgs = std::conditional_t<FORM == kWindow, WindowArgs,
-                                    std::conditional_t<FORM == kShared, SharedArgs, Args>>;
+                                    std::conditional_t<is_shared(FORM), SharedArgs, Args>>;
 
 // Key tiles that `n` tokens, the last of which sees key `last` last, visit.
 __device__ __forceinline__ int tiles_for(int n, int last, int kv_len) {
@@ -720,7 +723,7 @@ struct Planner {
 
 // The numbered entries of a call with few sequences, in shared memory in place of
 // Misc's: every CTA finds the same ones for itself (64 requests behind 8192 tokens:
-// 40.8 us, 44.0 with a kernel ahead that numbers them).
+// 39.9 us, 44.8 with a kernel ahead that numbers them).
 struct PlanTable {
   int entries, items;
   int begins[kCachedSeqs + 1];  // first rows of the sequences
@@ -866,9 +869,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (PAGED && threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   PlanTable *table = reinterpret_cast<PlanTable *>(smem + C::kBar + kPlanTableAt);
-  if constexpr (FORM == kShared)
-    if (a.planned == 0) plan_items(a, table, smem + C::kRing);
-  const bool cached = FORM != kShared && a.S <= kCachedSeqs;
+  if constexpr (FORM == kSharedFew) plan_items(a, table, smem + C::kRing);
+  const bool cached = !is_shared(FORM) && a.S <= kCachedSeqs;
   if (cached)
     for (int i = threadIdx.x; i <= a.S; i += kThreads)
       misc->seq[i] = make_int2(seq_begin(a, i), PAGED && i < a.S ? a.context_lens[i] : 0);
@@ -890,7 +892,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const Misc *numbered = cached ? misc : nullptr;
       int n_items = cached ? misc->first[a.S] : a.n_vblocks * a.Hk;
-      if constexpr (FORM == kShared) n_items = a.planned ? a.first[*a.head] : table->items;
+      if constexpr (FORM == kShared) n_items = a.first[*a.head];
+      if constexpr (FORM == kSharedFew) n_items = table->items;
       int e = 0, nq = 0;        // tiles and Q tiles copied so far
       bool ok = true;
       int w = blockIdx.x;       // the first item is the CTA's own; the rest are claimed
@@ -908,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // context, a block that the cache does not have (reads as zeros).
         const int b = tile * kTileBlocks + lane;
         if (b >= (it.kv_len + kBlk - 1) / kBlk) return a.num_blocks;
-        const int at = FORM == kWindow ? gap.cell(b) : FORM == kShared ? gap.skip + b : b;
+        const int at = FORM == kWindow ? gap.cell(b) : is_shared(FORM) ? gap.skip + b : b;
         return a.block_tables[static_cast<int64_t>(it.kv0) * a.max_blocks + at];
       };
       // Packed: the copies of a key or value tile.  Where the list's gap lies inside it
@@ -935,8 +938,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           bool some;
           if constexpr (FORM == kShared)
-            some = a.planned ? decode_shared(a, w, nxt, nxt_gap)
-                             : decode_planned(a, table, w, nxt, nxt_gap);
+            some = decode_shared(a, w, nxt, nxt_gap);
+          else if constexpr (FORM == kSharedFew)
+            some = decode_planned(a, table, w, nxt, nxt_gap);
           else
             some = decode_item<PAGED, FORM>(a, numbered, n_items, w, nxt, nxt_gap);
           if (some) break;
@@ -954,24 +958,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return __shfl_sync(~0u, good, 0);
       };
-      bool found = false;
       if constexpr (FORM == kShared) {
-        if (a.planned) {
-          // The CTA's own item comes decoded (found like the others, it takes 0.6 us longer).
-          found = true;
-          nxt.live = 0;
-          if (w < n_items) {
-            static_assert(sizeof(Item) == 60, "four words of 16 bytes with the table column");
-            int4 x[4];
+        // The CTA's own item comes decoded (found like the others, it takes 0.6 us longer).
+        nxt.live = 0;
+        if (w < n_items) {
+          static_assert(sizeof(Item) == 60, "four words of 16 bytes with the table column");
+          int4 x[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = a.start[4 * w + i];
-            memcpy(&nxt, x, sizeof nxt);
-            nxt_gap = {0, x[3].w};
-            nxt_id = ids_of(nxt, nxt_gap, nxt.kt0);
-          }
+          for (int i = 0; i < 4; ++i) x[i] = a.start[4 * w + i];
+          memcpy(&nxt, x, sizeof nxt);
+          nxt_gap = {0, x[3].w};
+          nxt_id = ids_of(nxt, nxt_gap, nxt.kt0);
         }
+      } else {
+        find();
       }
-      if (!found) find();
       for (int k = 0; ok; ++k) {
         const Item it = nxt;
         const Gap gap = nxt_gap;
@@ -1627,7 +1628,7 @@ cudaError_t launch(const CUtensorMap &tq, const KvMap<PAGED, FORM> &tk,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, C::kAlloc);
   if (e != cudaSuccess) return e;
   int64_t n_items = static_cast<int64_t>(a.n_vblocks) * a.n_split * a.Hk;   // a bound
-  if constexpr (FORM == kShared) {
+  if constexpr (is_shared(FORM)) {
     sms = a.ctas;
     n_items += (static_cast<int64_t>(a.T) / (2 * a.tpb) + a.P) * a.pre_split * a.Hk;
   }
@@ -1642,13 +1643,13 @@ cudaError_t launch(const CUtensorMap &tq, const KvMap<PAGED, FORM> &tk,
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, fwd_packed_kernel<D, F16, PAGED, FORM>, tq, tk, tv, a);
-  if (e != cudaSuccess || !PAGED || (FORM != kShared && a.n_split == 1)) return e;
-  // Eight blocks an SM in all, spread over the sequences (at most kCachedSeqs; kShared:
-  // any number).
+  if (e != cudaSuccess || !PAGED || (!is_shared(FORM) && a.n_split == 1)) return e;
+  // Eight blocks an SM in all, spread over the sequences (at most kCachedSeqs; with
+  // shared prefixes any number).
   cfg.gridDim = dim3(static_cast<unsigned>(a.S), static_cast<unsigned>(std::max(8 * sms / a.S, 1)));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<FORM>, a);
+  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<FORM == kSharedFew ? kShared : FORM>, a);
 }
 
 template <int FORM>
@@ -1794,8 +1795,7 @@ cudaError_t launch_paged_shared(const CUtensorMap &tq, const CUtensorMap &tk,
   cudaError_t e = sm_count(&a.ctas);
   if (e != cudaSuccess) return e;
   a.ctas = std::min(a.ctas, kSharedMaxCtas);
-  a.planned = p.S + P > kCachedSeqs;
-  if (!a.planned) return launch<128, false, true, kShared>(tq, tk, tv, a, stream);
+  if (p.S + P <= kCachedSeqs) return launch<128, false, true, kSharedFew>(tq, tk, tv, a, stream);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(kPlanThreads);
