@@ -887,12 +887,12 @@ int forward_packed(const void *q, const void *k, const void *v, void *o, float *
   p.o = o, p.lse = lse, p.cu_seqlens = cu_seqlens;
   p.S = S, p.T = T, p.H = H, p.Hk = Hk, p.scale = scale;
   p.causal = see.causal, p.window = see.window, p.sinks = see.sinks;
-  CUtensorMap cells[2];
-  if (see.window > 0) {
-    if ((rc = encode_rows_map(&cells[0], k, T, Hk, d, k_stride, true, 16, 1, dt)) != FA_OK) return rc;
-    if ((rc = encode_rows_map(&cells[1], v, T, Hk, d, v_stride, true, 16, 1, dt)) != FA_OK) return rc;
-    p.k_cells = &cells[0], p.v_cells = &cells[1];
+  CUtensorMap k_cells = tk, v_cells = tv;
+  if (see.sinks > 0) {   // (without first tokens a tile has no gap)
+    if ((rc = encode_rows_map(&k_cells, k, T, Hk, d, k_stride, true, 16, 1, dt)) != FA_OK) return rc;
+    if ((rc = encode_rows_map(&v_cells, v, T, Hk, d, v_stride, true, 16, 1, dt)) != FA_OK) return rc;
   }
+  p.k_cells = &k_cells, p.v_cells = &v_cells;
   return cuda_status(
       fattn::launch_fwd_packed(tq, tk, tv, p, d, f16, sched, status, fault_cta, s));
 }

@@ -604,11 +604,8 @@ struct Planner {
 
   __device__ Planner(const SharedArgs &args, Scratch &scratch)
       : a(args), m(scratch), tid(threadIdx.x), mine{}, own{}, work(0) {
-    if (tid < a.S) {
-      mine = global_seq<true>(a, tid);
-      m.begins[tid] = mine.begin;
-      m.begins[tid + 1] = seq_begin(a, tid + 1);
-    }
+    if (tid < a.S) mine = global_seq<true>(a, tid);
+    for (int s = tid; s <= min(a.S, THREADS); s += THREADS) m.begins[s] = seq_begin(a, s);
     for (int g = tid; g <= a.P; g += THREADS) {
       m.g_first[g] = a.P > 0 ? clampi(a.cu_groups[g], 0, a.S) : 0;
       if (g == a.P) break;

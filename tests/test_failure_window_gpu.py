@@ -24,8 +24,9 @@ def test_paged_prefill():
     check(1, lambda: (fa.paged_prefill_window(*x, 2000, 4),), (0,))
 
 
-def test_shared_prefix():
-    x = draw_shared([(1500, [(1, 9 + i) for i in range(30)])], 8, 2, seed=3)
+@pytest.mark.parametrize("S", [30, 150])
+def test_shared_prefix(S):
+    x = draw_shared([(1500, [(1, 9 + i) for i in range(S)])], 8, 2, seed=3)
     check(1, lambda: (fa.paged_prefill_shared(*x),), (0,))
 
 

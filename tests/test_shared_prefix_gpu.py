@@ -106,14 +106,17 @@ def test_prefix_lengths_that_do_not_fit(claim):
         check(*x[:6], fa.paged_prefill(*x[:6]))
 
 
-@pytest.mark.parametrize("S", [112, 113, 300, 1100])
+@pytest.mark.parametrize("S", [111, 112, 113, 300, 1100])
 def test_many_sequences(S):
+    """Up to 112 sequences and groups are numbered by the CTAs, more by a kernel ahead."""
     g = torch.Generator().manual_seed(S)
     own = torch.randint(1, 60, (S,), generator=g).tolist()
     run([(640, [(1, c) for c in own])], 4, 2, seed=S)
 
 
 def test_many_groups():
+    run([(160 + 16 * (i % 5), [(1, 3 + i % 40), (2, 20)][:1 + i % 2]) for i in range(45)], 4, 2,
+        seed=5)
     run([(160 + 16 * (i % 5), [(1, 3 + i % 40), (1, 20)]) for i in range(600)], 2, 1, seed=3)
     with pytest.raises(fa.FattnError):
         x = draw([(16, [])] * 1025, 2, 1, 4, loose=[(1, 5)])
@@ -153,6 +156,11 @@ def test_repeats_streams_and_captures():
     a = fa.paged_prefill_shared(*x)
     for _ in range(3):
         assert torch.equal(a, fa.paged_prefill_shared(*x))
+    many = draw([(900, [(1, 10 + i) for i in range(90)]), (400, [(2, 5 + i) for i in range(90)])],
+                8, 2, seed=12)
+    want = fa.paged_prefill_shared(*many)
+    for _ in range(3):
+        assert torch.equal(want, fa.paged_prefill_shared(*many))
     streams = [torch.cuda.Stream() for _ in range(2)]
     outs = []
     torch.cuda.synchronize()
