@@ -255,9 +255,11 @@ __device__ __forceinline__ int tiles_for(int n, int last, int kv_len) {
   return n > 0 ? (max(0, min(kv_len, last + 1)) + BN - 1) / BN : 0;
 }
 
-// The lowest n bits, none for n <= 0 and all for n >= 32.
-__device__ __forceinline__ uint32_t low_bits(int n) {
-  return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
+// All but the lowest n bits: all for n <= 0, none for n >= 32 (PTX clamps the shift).
+__device__ __forceinline__ uint32_t high_bits(int n) {
+  uint32_t r;
+  asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(~0u), "r"(max(n, 0)));
+  return r;
 }
 
 // A query that sees every key of its sequence.
@@ -1234,8 +1236,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (__any_sync(~0u, lim_j < BN || low_j > max(first_j, 0))) {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const uint32_t bits = low_bits(lim_j - 32 * w) & (~low_bits(low_j - 32 * w) |
-                                                                low_bits(first_j - 32 * w));
+              const uint32_t bits = ~high_bits(lim_j - 32 * w) &
+                                    (high_bits(low_j - 32 * w) | ~high_bits(first_j - 32 * w));
 #pragma unroll
               for (int c = 0; c < 32; ++c)
                 if (((bits >> c) & 1u) == 0u) sv[w][c] = __float_as_uint(-INFINITY);
