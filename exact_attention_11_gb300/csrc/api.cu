@@ -889,8 +889,9 @@ int forward_packed(const void *q, const void *k, const void *v, void *o, float *
   p.causal = see.causal, p.window = see.window, p.sinks = see.sinks;
   CUtensorMap k_cells = tk, v_cells = tv;
   if (see.sinks > 0) {   // (without first tokens a tile has no gap)
-    if ((rc = encode_rows_map(&k_cells, k, T, Hk, d, k_stride, true, 16, 1, dt)) != FA_OK) return rc;
-    if ((rc = encode_rows_map(&v_cells, v, T, Hk, d, v_stride, true, 16, 1, dt)) != FA_OK) return rc;
+    rc = encode_rows_map(&k_cells, k, T, Hk, d, k_stride, true, 16, 1, dt);
+    if (rc == FA_OK) rc = encode_rows_map(&v_cells, v, T, Hk, d, v_stride, true, 16, 1, dt);
+    if (rc != FA_OK) return rc;
   }
   p.k_cells = &k_cells, p.v_cells = &v_cells;
   return cuda_status(

@@ -154,7 +154,11 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
     };
     __shared__ int sum[WINDOW ? 32 : 8];
     add_up(before, sum);
-    if constexpr (WINDOW) add_up(used, sum + 8), add_up(far_before, sum + 16), add_up(far, sum + 24);
+    if constexpr (WINDOW) {
+      add_up(used, sum + 8);
+      add_up(far_before, sum + 16);
+      add_up(far, sum + 24);
+    }
     __syncthreads();
     if (threadIdx.x == 0) {
       auto total = [&](const int *x) {
@@ -172,7 +176,8 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
         used = total(sum + 8);
         if (blk == 0) *a.count = min(used + total(sum + 24), a.entries);
         if (live) {
-          put_range(at, local * BQ < a.sinks && (a.split == 0 || blocks <= a.whole) ? blocks - 1 : last);
+          const bool all = local * BQ < a.sinks && (a.split == 0 || blocks <= a.whole);
+          put_range(at, all ? blocks - 1 : last);
           int to = used + total(sum + 16);
           for (int jb = 0; jb < local; ++jb) to += far_entries(a, jb, blocks);
           const int step = far_steps(a.window), n_far = far_entries(a, local, blocks);
@@ -331,7 +336,8 @@ PackedGradLayout packed_grad_layout(int T, int S, int H, int Hk, int d, int wind
   if (window > 0 && window < T && S <= kSortedSeqs && sinks <= 8 * BQ) {
     l.split = sinks;
     const long long most = T / (BQ * (reach(window) + 1)) + 1;   // sequences with far parts
-    l.entries += (sinks + BQ - 1) / BQ * (T / (BQ * far_steps(window)) + 2 * std::min<long long>(S, most) + 1);
+    l.entries += (sinks + BQ - 1) / BQ *
+                 (T / (BQ * far_steps(window)) + 2 * std::min<long long>(S, most) + 1);
   }
   l.shared = H != Hk || l.split > 0;
   const size_t rows = static_cast<size_t>(l.n_blocks) * BQ;

@@ -53,10 +53,10 @@
 //    first key tile with the window's start (8 prompts up to 8192, window 1024, 4 first
 //    tokens: 260 us; with a key tile of their own 272).  Inside an item positions count
 //    along that list, so only the copies' addresses and the mask's lower bound differ.
-//  * kShared, kSharedFew: a group's prefix is walked by the rows of all its sequences as if they were
-//    one sequence's, and what each has behind it on its own; both write partial rows, which
-//    the merge joins.  The items of up to 112 sequences and groups are numbered by every
-//    CTA for itself, of more by a kernel of one block ahead.
+//  * kShared, kSharedFew: a group's prefix is walked by the rows of all its sequences as if
+//    they were one sequence's, and what each has behind it on its own; both write partial
+//    rows, which the merge joins.  The items of up to 112 sequences and groups are numbered
+//    by every CTA for itself, of more by a kernel of one block ahead.
 //
 // What bounds it: for long prompts the tensor pipe and the softmax chain (S out of
 // TMEM, exponentials, P back) of a two-tile step, 1.4 us where the MMAs alone take
@@ -226,10 +226,10 @@ struct CellMaps {
 };
 template <bool PAGED, int FORM>
 using KvMap = std::conditional_t<!PAGED && FORM == kWindow, CellMaps, CUtensorMap>;
-__host__ __device__ __forceinline__ const CUtensorMap &tile_map(const CUtensorMap &m) { return m; }
-__host__ __device__ __forceinline__ const CUtensorMap &cell_map(const CUtensorMap &m) { return m; }
-__host__ __device__ __forceinline__ const CUtensorMap &tile_map(const CellMaps &m) { return m.tiles; }
-__host__ __device__ __forceinline__ const CUtensorMap &cell_map(const CellMaps &m) { return m.cells; }
+__device__ __forceinline__ const CUtensorMap &tile_map(const CUtensorMap &m) { return m; }
+__device__ __forceinline__ const CUtensorMap &cell_map(const CUtensorMap &m) { return m; }
+__device__ __forceinline__ const CUtensorMap &tile_map(const CellMaps &m) { return m.tiles; }
+__device__ __forceinline__ const CUtensorMap &cell_map(const CellMaps &m) { return m.cells; }
 // A prefix is walked once for all rows of its group: it and what each sequence has of
 // its own are items of their own, numbered by shared_plan_kernel, and their partial rows
 // lie in ws_o one behind the other, those of the prefix from partition n_split on.
@@ -732,7 +732,8 @@ struct PlanTable {
   uchar4 of[kCachedSeqs];       // first and last sequence of its rows (+ 1), table row, prefix?
 };
 constexpr int kPlanTableAt = 8 * kNumBars + offsetof(Misc, seq);
-static_assert(kPlanTableAt + sizeof(PlanTable) <= kBarArea && kPlanTableAt % 8 == 0, "barrier area");
+static_assert(kPlanTableAt + sizeof(PlanTable) <= kBarArea && kPlanTableAt % 8 == 0,
+              "barrier area");
 
 // By the whole block; scratch: the ring's memory, ahead of its first copies.
 __device__ __forceinline__ void plan_items(const SharedArgs &a, PlanTable *m, uint8_t *scratch) {
@@ -1518,7 +1519,8 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
 #pragma unroll 16
       for (int p = 0; p < n; ++p) {
         if (FORM == kShared) src = a.ws_o + (place(p0 + p) * stride + row) * D + lane * 4;
-        const float4 v = *reinterpret_cast<const float4 *>(src + (FORM == kShared ? 0 : p * stride * D));
+        const int64_t off = FORM == kShared ? 0 : p * stride * D;
+        const float4 v = *reinterpret_cast<const float4 *>(src + off);
         const float w = __shfl_sync(~0u, f, p);
         o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y);
         o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
