@@ -71,9 +71,9 @@
 // take 1.5 us each, its start and end 3); one of 16384, 8 / 1 heads, fp16, window 4000,
 // 150 us (1605); 64 single tokens, window 4096, 182 us (5.9 TB/s); chunks up to 2048 over
 // up to 32768, window 4096, 179 us (1370 TFLOP/s).  Shared prefixes, single tokens, 32 / 8
-// heads: 64 sequences behind 8192 tokens, up to 512 of their own, 40 us (2.5 TB/s: start,
+// heads: 64 sequences behind 8192 tokens, up to 512 of their own, 38 us (2.6 TB/s: start,
 // the chains of an SM's four or five short items, merge; 314 without sharing); 256 behind
-// 32768, up to 2048 of their own, 282 us (4.3 TB/s; first the prefix, bound by the tensor
+// 32768, up to 2048 of their own, 280 us (4.3 TB/s; first the prefix, bound by the tensor
 // cores, 65 us, then the rest at 5.8 TB/s; 4579 without).
 // Rounding: P to the element type before P V, O once at the end; scores, maxima, sums,
 // partial rows and their merge are fp32.
@@ -1492,6 +1492,17 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
     auto place = [&](int p) -> int64_t {
       return FORM == kShared && p >= own ? a.n_split + p - own : p;
     };
+    auto part_row = [&](int p) {
+      return *reinterpret_cast<const float4 *>(a.ws_o + (place(p) * stride + row) * D + lane * 4);
+    };
+    // kShared: the first partitions' rows are loaded ahead of the (max, sum) that weigh
+    // them (64 requests behind 8192 tokens: 38.5 us, 40.6 without; but 16 drafts over up to
+    // 4096, cut without a prefix, 33.8 so and 33.0 without).
+    constexpr int kAhead = FORM == kShared ? 8 : 0;
+    float4 ahead[kAhead + 1];
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p)
+      if (p < parts) ahead[p] = part_row(p);
     // 32 partitions at a time, lane p holding partition p's (max, sum): their rows'
     // loads do not wait for one another.
     float m = -INFINITY, l = 0.f;
@@ -1515,16 +1526,20 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
       if (none) continue;
       o.x *= old, o.y *= old, o.z *= old, o.w *= old;
       m = mx;
-      const float *src = a.ws_o + (p0 * stride + row) * D + lane * 4;
-#pragma unroll 16
-      for (int p = 0; p < n; ++p) {
-        if (FORM == kShared) src = a.ws_o + (place(p0 + p) * stride + row) * D + lane * 4;
-        const int64_t off = FORM == kShared ? 0 : p * stride * D;
-        const float4 v = *reinterpret_cast<const float4 *>(src + off);
+      auto add = [&](int p, const float4 &v) {
         const float w = __shfl_sync(~0u, f, p);
         o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y);
         o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
-      }
+      };
+      if (p0 == 0)
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p)
+          if (p < n) add(p, ahead[p]);
+      const float *src = a.ws_o + (p0 * stride + row) * D + lane * 4;
+#pragma unroll 16
+      for (int p = p0 == 0 ? kAhead : 0; p < n; ++p)
+        add(p, FORM == kShared ? part_row(p0 + p)
+                               : *reinterpret_cast<const float4 *>(src + p * stride * D));
     }
     const float inv = parts == 0 ? 0.f : 1.f / l;        // a query that sees no key: zeros
     uint2 w;
