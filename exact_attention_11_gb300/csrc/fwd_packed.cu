@@ -70,7 +70,7 @@
 // 8192, 32 / 8 heads, d = 128, window 1024: 260 us (1230 TFLOP/s; a block's nine key tiles
 // take 1.5 us each, its start and end 3); one of 16384, 8 / 1 heads, fp16, window 4000,
 // 150 us (1605); 64 single tokens, window 4096, 182 us (5.9 TB/s); chunks up to 2048 over
-// up to 32768, window 4096, 179 us (1370 TFLOP/s).  Shared prefixes, single tokens, 32 / 8
+// up to 32768, window 4096, 171 us (1430 TFLOP/s).  Shared prefixes, single tokens, 32 / 8
 // heads: 64 sequences behind 8192 tokens, up to 512 of their own, 38 us (2.6 TB/s: start,
 // the chains of an SM's four or five short items, merge; 314 without sharing); 256 behind
 // 32768, up to 2048 of their own, 280 us (4.3 TB/s; first the prefix, bound by the tensor
@@ -325,7 +325,10 @@ __device__ __forceinline__ Work work_of(const FormArgs<FORM> &a, const Seq &q) {
 // took 1.3 for chunks of up to 1024 over up to 16384.)  `work`: key tiles of the call's
 // blocks, of one key/value head.  Each block of the sequence cuts its own key tiles into
 // that many.  (Roundings are spelled out: the merge kernel has to reach the same
-// number.)
+// number.)  kWindow: the few rows of a sequence of one block cost little to cut, and its
+// items come last, so where such sequences are less than an eighth of the work they take
+// eight times theirs for the call's (chunks of 6, 1536, 3 and 2048 over up to 32768, window
+// 4096: 171 us, 179 without; always their own work: 178 for 170 on 31 chunks up to 289).
 constexpr float kPartFixed = 2.5f, kPartRow = 0.02f;
 __device__ __forceinline__ int parts_of(const Args &a, const Seq &q, int tiles, int64_t work,
                                         int most) {
@@ -355,21 +358,25 @@ __device__ __forceinline__ void number_items(const FormArgs<FORM> &a, Misc *m) {
   auto seq = [&](int i) {
     return make_seq(a, PAGED, m->seq[i].x, m->seq[i + 1].x, m->seq[i].y);
   };
-  int64_t work = 0;
+  int64_t work = 0, work_short = 0;
   if (PAGED && a.n_split > 1) {
 #pragma unroll 1
     for (int i = lane; i < a.S; i += 32) {
       const Work w = work_of<FORM>(a, seq(i));
       work += static_cast<int64_t>(w.tiles) * w.blocks;
+      if (FORM == kWindow && w.blocks == 1) work_short += w.tiles;
     }
     work = warp_sum(work);
+    if (FORM == kWindow) work_short = min(work, 8 * warp_sum(work_short));
   }
   // Key: key tiles of an item, then the index, so that no two are equal.
 #pragma unroll 1
   for (int i = lane; i < a.S; i += 32) {
     const Seq q = seq(i);
-    const int tiles = work_of<FORM>(a, q).tiles;
-    const int parts = PAGED ? parts_of(a, q, tiles, work, a.n_split) : 1;
+    const Work x = work_of<FORM>(a, q);
+    const int tiles = x.tiles;
+    const int64_t of = FORM == kWindow && x.blocks == 1 ? work_short : work;
+    const int parts = PAGED ? parts_of(a, q, tiles, of, a.n_split) : 1;
     const int size = PAGED ? part_size(tiles, parts) : tiles;
     m->key[i] = min(size, (1 << 23) - 1) * 128 + i;
     m->n_parts[i] = static_cast<int16_t>(parts);
@@ -1460,16 +1467,22 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
     __shared__ Seq shared_seq;
     __shared__ int shared_cut;
     if (threadIdx.x < 32) {
-      int64_t work = 0;
+      const Seq q = global_seq<true>(a, blockIdx.x);
+      const Work own = work_of<FORM>(a, q);
+      int64_t work = 0, work_short = 0;
       for (int i = lane; i < a.S; i += 32) {
         const Work w = work_of<FORM>(a, global_seq<true>(a, i));
         work += static_cast<int64_t>(w.tiles) * w.blocks;
+        if (FORM == kWindow && w.blocks == 1) work_short += w.tiles;
       }
       work = warp_sum(work);
-      const Seq q = global_seq<true>(a, blockIdx.x);
+      if (FORM == kWindow) {
+        work_short = min(work, 8 * warp_sum(work_short));
+        if (own.blocks == 1) work = work_short;
+      }
       if (lane == 0) {
         shared_seq = q;
-        shared_cut = parts_of(a, q, work_of<FORM>(a, q).tiles, work, a.n_split);
+        shared_cut = parts_of(a, q, own.tiles, work, a.n_split);
       }
     }
     __syncthreads();

@@ -222,6 +222,15 @@ def test_paged_split_contexts(lens, ctx, window, sinks):
     run_paged(lens, ctx, 5, 1, window, sinks, seed=T + 1)
 
 
+@pytest.mark.parametrize("lens,ctx", [
+    ([1, 2000], [9000, 9000]),                        # few rows beside many, cut by their own share
+    ([64, 1, 65, 3, 0, 2500], [8200, 5, 7777, 8192, 400, 8193]),
+    ([700, 1], [700, 4096]),
+])
+def test_paged_single_tokens_beside_chunks(lens, ctx):
+    run_paged(lens, ctx, 8, 2, 4096, 20, seed=8)
+
+
 @pytest.mark.parametrize("S", [112, 113, 300])
 def test_paged_many_sequences(S):
     g = torch.Generator().manual_seed(S)
