@@ -54,6 +54,8 @@
 // kWindow (fa_backward_packed_window): an item comes with the query blocks that it
 // visits; a query sees a key if it is at most window - 1 behind or among the first
 // `sinks` (bwd_tile.cuh's masks by bits, in the blocks that either border crosses).
+// kWindowGroups: an item may have all query heads of its key/value head, one after another:
+// K and V are loaded once, dK and dV add up in TMEM and are stored.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -127,7 +129,7 @@ struct Misc {
   int abort;
   int item[2];
   int4 seq[2];          // PACKED: the item's entry of the block table
-  int2 range[2];        // kWindow: its first query block and their number
+  int4 range[2];        // WINDOW: first query block, their number, first head, heads
 };
 static_assert(kNumBars * 8 + sizeof(Misc) <= 512 && kNumBars % 2 == 0, "barrier area");
 
@@ -152,6 +154,7 @@ constexpr int kDevBadSmemBase = -2;
 struct BwdItem {
   int jb, bh, k0, i_first, n_steps, n_halves, N;
   int kvh, row0, blk0;   // PACKED: key/value head, first row, first padded block
+  int per;               // kWindowGroups: steps of a query head
   __device__ void decode(int w, int BH, int n_qb, int causal, int N_) {
     jb = w / BH;
     bh = kvh = w - jb * BH;
@@ -175,6 +178,14 @@ struct BwdItem {
     n_steps = n;
     n_halves = 2 * n;
   }
+  __device__ void set_range(const int4 &r, int G) {
+    i_first = r.x;
+    per = r.y;
+    bh = r.z;
+    kvh = bh / G;
+    n_steps = per * r.w;
+    n_halves = 2 * n_steps;
+  }
   __device__ void steps(int n_qb, int causal) {
     k0 = jb * BM;
     i_first = causal ? jb : 0;
@@ -184,10 +195,11 @@ struct BwdItem {
 };
 
 // What the kernel runs on: [B, H, N, d] tensors, packed sequences, or packed sequences
-// with a window.
-enum : int { kDense = 0, kPacked = 1, kWindow = 2 };
+// with a window, whose items have one query head, or some of them all heads of a group
+// (two kernels: in one, items of one head took 3 - 5% longer).
+enum : int { kDense = 0, kPacked = 1, kWindow = 2, kWindowGroups = 3 };
 template <int KIND>
-using Extra = std::conditional_t<KIND == kWindow, BwdWindow, BwdPacked>;
+using Extra = std::conditional_t<KIND >= kWindow, BwdWindow, BwdPacked>;
 
 template <int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -200,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       int BH, float scale, int causal, int *__restrict__ sched, int fault_cta,
                       int *__restrict__ dev_status, const __grid_constant__ CUtensorMap tm_dk,
                       const __grid_constant__ CUtensorMap tm_dv, const Extra<KIND> pk) {
-  constexpr bool PACKED = KIND != kDense, WINDOW = KIND == kWindow;
+  constexpr bool PACKED = KIND != kDense, WINDOW = KIND >= kWindow, GROUPS = KIND == kWindowGroups;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t s_base = smem_u32(smem);
   if ((s_base & 1023u) != 0) {
@@ -266,7 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const volatile int *e = reinterpret_cast<const volatile int *>(&misc->seq[slot]);
       it.decode_packed(w, make_int4(e[0], e[1], e[2], e[3]), BH, pk.group, causal);
       const volatile int *r = reinterpret_cast<const volatile int *>(&misc->range[slot]);
-      if (WINDOW) it.set_steps(r[0], r[1]);
+      if (GROUPS) it.set_range(make_int4(r[0], r[1], r[2], r[3]), pk.group);
+      else if (WINDOW) it.set_steps(r[0], r[1]);
     } else {
       it.decode(w, BH, n_qb, causal, N);
     }
@@ -285,8 +298,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&tm_do);
       int nq = 0, ndo = 0, nkv = 0;   // halves (and K/V pairs) issued so far
       bool ok = true;
-      int n_entries = 0;
-      if constexpr (WINDOW) n_entries = *pk.count;
+      // kWindowGroups: the first entry and item of those with all heads of a group, the first
+      // behind them; and the number of items.
+      int from = 0, to = 0, n_from = 0, n_to = 0, n_used = 0;
+      if constexpr (WINDOW && !GROUPS) n_used = pk.count[0] * BH;
+      if constexpr (GROUPS) {
+        const int4 count = *reinterpret_cast<const int4 *>(pk.count);
+        from = count.y;
+        to = from + count.z;
+        n_from = from * BH;
+        n_to = n_from + count.z * pk.kv_heads;
+        n_used = n_to + (count.x - to) * BH;
+      }
       auto claim = [&]() { return static_cast<int>(gridDim.x) + atomicAdd(sched, 1); };
       for (int k = 0; ok; ++k) {
         const int islot = k & 1;
@@ -294,15 +317,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The CTA's own first item, then claimed ones.
         int w = k == 0 ? static_cast<int>(blockIdx.x) : claim();
         int4 entry = make_int4(0, 0, 0, 0);
-        int2 range = make_int2(0, 0);
+        int4 range = make_int4(0, 0, 0, 0);
         if (PACKED) {
-          auto in_table = [&](int x) { return WINDOW && x / BH >= n_entries ? n_items : x; };
+          auto in_table = [&](int x) { return WINDOW && x >= n_used ? n_items : x; };
+          int at = 0;
+          auto entry_of = [&](int x) {
+            if (!GROUPS || x < n_from) at = x / BH;
+            else if (x < n_to) at = from + (x - n_from) / pk.kv_heads;
+            else at = to + (x - n_to) / BH;
+            return at;
+          };
           w = in_table(w);
           // Entries of length 0 end a sorted table, else are passed over.
-          while (w < n_items && (entry = pk.table[w / BH]).y == 0)
+          while (w < n_items && (entry = pk.table[entry_of(w)]).y == 0)
             w = pk.sorted ? n_items : in_table(claim());
           if constexpr (WINDOW)
-            if (w < n_items) range = pk.range[w / BH];
+            if (w < n_items) {
+              const int2 blocks = pk.range[at];
+              const bool all = GROUPS && at >= from && at < to;
+              const int head = all ? (w - n_from - (at - from) * pk.kv_heads) * pk.group
+                                   : at < from ? w - at * BH : w - n_to - (at - to) * BH;
+              range = make_int4(blocks.x, blocks.y, head, all ? pk.group : 1);
+            }
           // (Offsets that decrease leave entries unwritten: whatever they hold, the
           // item stays inside the tensors.)
           entry.x = min(max(entry.x, 0), pk.tokens - 1);
@@ -323,27 +359,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         BwdItem it;
         if (PACKED) {
           it.decode_packed(w, entry, BH, pk.group, causal);
-          if (WINDOW) it.set_steps(range.x, range.y);
+          if (GROUPS) it.set_range(range, pk.group);
+          else if (WINDOW) it.set_steps(range.x, range.y);
         } else
           it.decode(w, BH, n_qb, causal, N);
         const int h_base = nq;
+        int first_h = 0, head = it.bh;   // the head, and the half that it begins with
         // Q / dO half h of the item (with its [LSE2 | D] vectors on QFull).
         auto load_half = [&](int h) -> bool {
           const int g = h_base + h, slot = g % kSlots, use = g / kSlots;
-          const int qb = it.i_first + (h >> 1);
+          if (GROUPS && h - first_h == 2 * it.per) first_h = h, ++head;
+          const int qb = it.i_first + ((h - first_h) >> 1);
           const int qrow = qb * BQ + (h & 1) * BH_;
           if (!mbar_wait(bar(kBarQEmpty + slot), (use & 1) ^ 1, abort_flag)) return false;
           mbar_arrive_expect_tx(bar(kBarQFull + slot), kHalf + kVecBytes);
-          tma_load_3d(s_base + kOffQ + slot * kHalf, &tm_q, 0, it.row0 + qrow, it.bh, bar(kBarQFull + slot));
+          tma_load_3d(s_base + kOffQ + slot * kHalf, &tm_q, 0, it.row0 + qrow, head,
+                      bar(kBarQFull + slot));
           const float *vsrc =
-              vecs + (static_cast<int64_t>(it.bh) * n_qb + it.blk0 + qb) * (2 * BQ) + (h & 1) * BH_;
+              vecs + (static_cast<int64_t>(head) * n_qb + it.blk0 + qb) * (2 * BQ) + (h & 1) * BH_;
           bulk_load(s_base + kOffVec + slot * kVecBytes, vsrc, BH_ * 4, bar(kBarQFull + slot));
           bulk_load(s_base + kOffVec + slot * kVecBytes + BH_ * 4, vsrc + BQ, BH_ * 4,
                     bar(kBarQFull + slot));
           nq = g + 1;
           if (!mbar_wait(bar(kBarDOEmpty + slot), (use & 1) ^ 1, abort_flag)) return false;
           mbar_arrive_expect_tx(bar(kBarDOFull + slot), kHalf);
-          tma_load_3d(s_base + kOffDO + slot * kHalf, &tm_do, 0, it.row0 + qrow, it.bh,
+          tma_load_3d(s_base + kOffDO + slot * kHalf, &tm_do, 0, it.row0 + qrow, head,
                       bar(kBarDOFull + slot));
           ndo = g + 1;
           return true;
@@ -403,11 +443,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // sequence ends inside the half or before it, have been cleared.
       uint32_t fix_parity = 0;   // bit: ring slot
       int kv_fixes = 0;
+      int first_h = 0;           // kWindowGroups: the half that the last one's head begins with
       auto wait_half = [&](const BwdItem &it, int h, int g) -> bool {
         const int slot = g % kSlots;
         if (!mbar_wait(bar(kBarQFull + slot), (g / kSlots) & 1, abort_flag)) return false;
         if (!mbar_wait(bar(kBarDOFull + slot), (g / kSlots) & 1, abort_flag)) return false;
-        if (PACKED && (it.i_first * BQ + (h + 1) * BH_ > it.N)) {
+        if (GROUPS && h - first_h == 2 * it.per) first_h = h;
+        if (PACKED && (it.i_first * BQ + (h - first_h + 1) * BH_ > it.N)) {
           if (!mbar_wait(bar(kBarFix + slot), (fix_parity >> slot) & 1, abort_flag)) return false;
           fix_parity ^= 1u << slot;
         }
@@ -420,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int w;
         BwdItem it;
         if (!(ok = fetch_item(k, w, it, false)) || w >= n_items) break;
+        first_h = 0;
         if (!(ok = mbar_wait(bar(kBarKV), k & 1, abort_flag))) break;
         if (PACKED && it.k0 + BM > it.N) {
           if (!(ok = mbar_wait(bar(kBarKVFix), kv_fixes & 1, abort_flag))) break;
@@ -508,12 +551,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         int w;
         BwdItem it;
         if (!(ok = fetch_item(k, w, it, true)) || w >= n_items) break;
+        int first_h = 0;
         auto half = [&](int h) -> bool {
           const int slot = g % kSlots;
           const uint32_t ph = (g / kSlots) & 1;
           if (!wait_warp(bar(kBarQFull + slot), ph, abort_flag)) return false;
           if (!wait_warp(bar(kBarDOFull + slot), ph, abort_flag)) return false;
-          const int keep = it.N - it.i_first * BQ - h * BH_;   // rows of the sequence
+          // (rows of the sequence)
+          if (GROUPS && h - first_h == 2 * it.per) first_h = h;
+          const int keep = it.N - it.i_first * BQ - (h - first_h) * BH_;
           if (keep < BH_) {
             clear(kOffQ + slot * kHalf, BH_, max(keep, 0));
             clear(kOffDO + slot * kHalf, BH_, max(keep, 0));
@@ -568,6 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Step i of the item (global step steps + i): its dQ' rows (lanes =
       // queries), columns 32 t .. 32 t + 31 of d: TMEM -> registers ->
       // staging tile -> TMA reduce-add.
+      int first_i = 0;          // kWindowGroups: the step that head it.bh begins with
       auto readout = [&](int i) -> bool {
         const int s = steps + i, p = s & 1;
         if (!wait_warp(bar(kBarDQFull + p), (s >> 1) & 1, abort_flag)) return false;
@@ -594,14 +641,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           tma_reduce_add_3d(&tm_dq, stage_u32, 32 * t,
-                            (it.blk0 + it.i_first + i) * BQ + quarter * 32, it.bh);
+                            (it.blk0 + it.i_first + i - first_i) * BQ + quarter * 32, it.bh);
           bulk_commit();
         }
+        if (GROUPS && i + 1 - first_i == it.per) first_i = i + 1, ++it.bh;
         return true;
       };
       for (int i = 0; i < it.n_steps && ok; ++i) {
         const int h = 2 * i + t, st = steps + i, g = g0 + h, slot = g % kSlots;
-        const int q0 = (it.i_first + i) * BQ + t * BH_;   // first query of the sub-tile
+        // First query of the sub-tile.  (The step before is still to be read out.)
+        const int in_head = !GROUPS ? i : i - first_i == it.per ? 0 : i - first_i;
+        const int q0 = (it.i_first + in_head) * BQ + t * BH_;
         if (!(ok = wait_warp(bar(kBarSFull + t), st & 1, abort_flag))) break;
         // [LSE2 | D] of the sub-tile came with Q_t on QFull, which S_t needed.
         if (!(ok = wait_warp(bar(kBarQFull + slot), (g / kSlots) & 1, abort_flag))) break;
@@ -660,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kBarEpiDone));
       bool shared = PACKED && pk.group > 1;
+      if constexpr (GROUPS) shared = it.n_steps == it.per;
       if constexpr (WINDOW) shared = shared || it.k0 < pk.split;
       if (shared) {
         // Another query head of the group (kWindow: or another item of the block of
@@ -749,7 +800,7 @@ cudaError_t launch_main(const CUtensorMap &tq64, const CUtensorMap &tk, const CU
   if ((e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
     return e;
   long long n_items = KIND == kDense ? (N + BQ - 1) / BQ : pk.n_blocks;
-  if constexpr (KIND == kWindow) n_items = pk.entries;
+  if constexpr (KIND >= kWindow) n_items = pk.entries;
   n_items *= BH;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(n_items < n_sm ? n_items : n_sm));
@@ -796,8 +847,9 @@ cudaError_t launch_bwd_window_main_d64(const CUtensorMap &tq64, const CUtensorMa
                                         void *dv, int H, const BwdWindow &pk, float scale,
                                         int *sched, int *dev_status, int fault_cta,
                                         cudaStream_t stream) {
-  return launch_main<kWindow>(tq64, tk, tv, tdo64, tdq, vecs, dk, dv, H, 0, scale, 1, sched,
-                           fault_cta, dev_status, stream, tdk, tdv, pk);
+  auto launch = pk.grouping ? launch_main<kWindowGroups> : launch_main<kWindow>;
+  return launch(tq64, tk, tv, tdo64, tdq, vecs, dk, dv, H, 0, scale, 1, sched, fault_cta,
+                dev_status, stream, tdk, tdv, pk);
 }
 
 }  // namespace fattn

@@ -24,10 +24,12 @@
 // group: with two to sixteen steps of a group an item, 50 - 59 us and 213 - 215.
 // With a window (fa_backward_packed_window) a key block's item visits the query blocks
 // that see it only, which the table gives with it; what bounds it and how it rounds stay:
-// 4 documents of 10560 tokens in all, window 1024, 4 first tokens: 36 + 211 + 27 us, 281
-// for the call (660 TFLOP/s of visible pairs; the main kernel's 2.7 us a step of 128 x 128
-// pairs, nine steps an item, of which the window leaves 0.89, and 1.5 us between items);
-// 16 of 2168 tokens, d = 64, window 256: 8 + 28 + 6, 37 us.
+// 4 documents of 10560 tokens in all, window 1024, 4 first tokens: 258 us for the call (720
+// TFLOP/s of visible pairs; the main kernel takes 2.2 us a step of 128 x 128 pairs, of which
+// the window leaves 0.89); 16 of 2168 tokens, d = 64, window 256: 8 + 28 + 6, 37 us.
+// With a window items are alike and, in long calls, many: there most have all query heads of a
+// key/value head, load K and V once and store dK and dV, whose sums over heads stay in TMEM
+// (281 -> 258 us for the 4 documents; 3 of up to 4300, 32 / 8 heads, window 208: 203 -> 162).
 // Rounding: P and dS to bf16 before their products, as the dense kernels; sums and
 // accumulators fp32; each gradient once.
 #include <cuda_runtime.h>
@@ -47,7 +49,12 @@ constexpr int BQ = 128;
 // Up to this many sequences the table is sorted (each block compares its sequence
 // with all others); beyond, it goes by block number, unused blocks in between.
 constexpr int kSortedSeqs = 2048;
+constexpr int kSms = 152;     // of an sm_103a GPU
+constexpr int kStart = 3;     // an item's start and end, in steps
 constexpr float kLog2e = 1.4426950408889634f;
+// All keys up to a query's own (or all); a window; a window, and items that may have all heads
+// of a group.
+enum : int { kAll = 0, kWindow = 1, kGroups = 2 };
 
 struct SideArgs {
   const __nv_bfloat16 *o, *dout;
@@ -62,13 +69,15 @@ struct SideArgs {
   float scale;
   // A window: the main kernel's query blocks per entry of the table, and their count.
   int2 *range;
-  int *count;
+  int4 *count;
+  int *stored;
   int entries, split, whole, window, sinks;
 };
 
 // A window: key block jb is seen by the query blocks from its own to `reach` further;
 // if it holds first tokens, by all later ones too.  In sequences of more than `whole`
-// blocks, an SM's share of the call's steps, those are items of their own (entries of
+// blocks, an SM's share of the call's steps (beside items with all heads of a group, half of
+// it), those are items of their own (entries of
 // kFar query blocks or more): one item of the whole sequence would end the call alone
 // (one document of 16384, 8 heads, window 512: 185 us, 354 in one item; but four of 8192,
 // whose items fit in: 631, 622 so).  Far parts of four blocks: 190, 633 us.
@@ -99,8 +108,9 @@ __device__ __forceinline__ int first_block(const SideArgs &a, int s) {
 
 // One block of 256 threads per (padded block, head); heads H .. H + Hk - 1
 // stand for the key/value heads' accumulators.
-template <int D, bool WINDOW>
+template <int D, int KIND>
 __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
+  constexpr bool WINDOW = KIND != kAll, GROUPS = KIND == kGroups;
   // The main kernel may be scheduled once every block of this one has begun.
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int L = D / 8;                 // threads per row, eight values each
@@ -122,17 +132,25 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
   };
   const int blocks = (n + BQ - 1) / BQ;
   const int last = WINDOW ? min(local + reach(a.window), blocks - 1) : 0;
+  __shared__ int sum[GROUPS ? 48 : WINDOW ? 32 : 8];
+  __shared__ float sum_lost[GROUPS ? 8 : 1];
+  __shared__ int most[GROUPS ? 8 : 1];
   if (h == 0 && a.S > kSortedSeqs) {
     if (threadIdx.x == 0) {
       a.table[blk] = live ? make_int4(begin, n, blk - local, local) : make_int4(0, 0, 0, 0);
       put_range(blk, local * BQ < a.sinks ? blocks - 1 : last);
-      if (WINDOW && blk == 0) *a.count = a.n_blocks;
+      if (WINDOW && blk == 0) *a.count = make_int4(a.n_blocks, 0, 0, 0);
     }
-  } else if (h == 0) {
+  } else if (h == 0 || (GROUPS && h >= a.H)) {
     // The block's place in the table: behind the blocks of longer sequences (of
     // equal ones, those before it); an unused block, behind all used ones.
     int before = 0;
-    int used = 0, far_before = 0, far = 0;   // a window: entries of all sequences, far ones
+    // A window: entries of all sequences, far ones, and those of first tokens, which come
+    // first.
+    int used = 0, far_before = 0, far = 0, split_before = 0, split = 0;
+    const int n_split = (a.split + BQ - 1) / BQ;
+    float lost = 0.f;                        // steps that the last blocks have less than the others
+    int longest = 0;                         // blocks of a sequence
     for (int j = threadIdx.x; j < a.S; j += 256) {
       const int b = clampi(a.cu_seqlens[j], 0, a.T);
       const int len = clampi(a.cu_seqlens[j + 1], b, a.T) - b;
@@ -145,39 +163,83 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
       if (WINDOW) {
         const int f = far_entries(a, blocks);
         used += blocks, far += f, far_before += longer ? f : 0;
+        if (GROUPS) {
+          const int c = min(blocks, n_split);
+          split += c, split_before += longer ? c : 0;
+          const float r = static_cast<float>(reach(a.window)), b = static_cast<float>(blocks);
+          lost += b > r ? r * (r + 1.f) * 0.5f : b * (r + 1.f) - b * (b + 1.f) * 0.5f;
+          longest = max(longest, blocks);
+        }
       }
     }
-    auto add_up = [&](int x, int *sum) {
+    auto add_up = [&](auto x, auto *sum) {
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(~0u, x, off);
       if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = x;
     };
-    __shared__ int sum[WINDOW ? 32 : 8];
     add_up(before, sum);
     if constexpr (WINDOW) {
       add_up(used, sum + 8);
       add_up(far_before, sum + 16);
       add_up(far, sum + 24);
+      if (GROUPS) {
+        add_up(split_before, sum + 32);
+        add_up(split, sum + 40);
+        add_up(lost, sum_lost);
+        longest = __reduce_max_sync(~0u, longest);
+        if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = longest;
+      }
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-      auto total = [&](const int *x) {
-        int n = 0;
-        for (int u = 0; u < 8; ++u) n += x[u];
+      auto total = [&](const auto *x) {
+        auto n = x[0];
+        for (int u = 1; u < 8; ++u) n += x[u];
         return n;
       };
       before = total(sum);
+      int place = live ? before + local : before + blk;
+      if constexpr (GROUPS) {
+        split = total(sum + 40);
+        split_before = total(sum + 32);
+        if (live)
+          place = local < n_split ? split_before + local
+                                  : place + split - split_before - min(blocks, n_split);
+      }
       // (Offsets that decrease may lead anywhere: stay inside the table.)
-      const int at = clampi(live ? before + local : before + blk, 0, a.n_blocks - 1);
-      if (!WINDOW || live)
+      const int at = clampi(place, 0, a.n_blocks - 1);
+      if (h == 0 && (!WINDOW || live))
         a.table[at] = live ? make_int4(begin, n, blk - local, local) : make_int4(0, 0, 0, 0);
       if constexpr (WINDOW) {
         // The used entries come first, then the far ones.
         used = total(sum + 8);
-        if (blk == 0) *a.count = min(used + total(sum + 24), a.entries);
-        if (live) {
-          const bool all = local * BQ < a.sinks && (a.split == 0 || blocks <= a.whole);
-          put_range(at, all ? blocks - 1 : last);
+        const int far_all = total(sum + 24), all = clampi(used + far_all, 0, a.entries);
+        const int from = clampi(split, 0, all), rest = clampi(used, from, all) - from;
+        int grouped = 0;
+        if (GROUPS) {
+          // Items with all heads of a group load K and V once and need no sums of dK and dV
+          // in memory, but are few and long: if an SM's share of the call is one and a half
+          // of them or more (in steps; kStart: an item's start), they go first, and what
+          // comes last in items of one head takes the SMs most of one of them.
+          for (int u = 1; u < 8; ++u) most[0] = max(most[0], most[u]);
+          const float steps = static_cast<float>(reach(a.window)) + 1.f;
+          const float share =
+              (static_cast<float>(all) * (steps + kStart) - total(sum_lost)) * a.H / kSms;
+          const float item = fminf(steps, static_cast<float>(most[0])) * (a.H / a.Hk) + kStart;
+          const float last = 0.75f * kSms * item / ((item - kStart) + kStart * (a.H / a.Hk));
+          if (1.5f * item <= share)
+            grouped = clampi(rest + min(far_all, static_cast<int>(last) / a.Hk) -
+                                 static_cast<int>(last) / a.Hk, 0, rest);
+        }
+        // Its items have all heads of a group, which then store dK and dV.
+        if (GROUPS) {
+          sum[0] = live && at >= from && at < from + grouped && local >= n_split;
+          if (h == 0) a.stored[blk] = sum[0];
+        }
+        if (h == 0 && blk == 0) *a.count = make_int4(all, from, grouped, 0);
+        if (h == 0 && live) {
+          const bool to_end = local * BQ < a.sinks && (a.split == 0 || blocks <= a.whole);
+          put_range(at, to_end ? blocks - 1 : last);
           int to = used + total(sum + 16);
           for (int jb = 0; jb < local; ++jb) to += far_entries(a, jb, blocks);
           const int step = far_steps(a.window), n_far = far_entries(a, local, blocks);
@@ -191,6 +253,10 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
     }
   }
   if (!live) return;
+  if (GROUPS && h >= a.H) {
+    __syncthreads();
+    if (sum[0]) return;
+  }
   const int row_in = threadIdx.x / L, part = threadIdx.x % L;
   const int64_t rows = static_cast<int64_t>(a.n_blocks) * BQ;
   const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -248,8 +314,9 @@ __global__ void __launch_bounds__(256) packed_prep_kernel(const SideArgs a) {
 }
 
 // One block per token: its rows of every head, eight values a thread.
-template <int D, bool WINDOW>
+template <int D, int KIND>
 __global__ void __launch_bounds__(256) packed_out_kernel(const SideArgs a) {
+  constexpr bool WINDOW = KIND != kAll, GROUPS = KIND == kGroups;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int L = D / 8;
   const int tok = blockIdx.x;
@@ -261,6 +328,7 @@ __global__ void __launch_bounds__(256) packed_out_kernel(const SideArgs a) {
   const int64_t acc_row = static_cast<int64_t>(begin / BQ + s) * BQ + tok - begin;
   bool shared = a.dk_acc != nullptr;
   if (WINDOW && a.H == a.Hk) shared = shared && (tok - begin) / BQ * BQ < a.split;
+  if (GROUPS) shared = a.stored[begin / BQ + s + (tok - begin) / BQ] == 0;
   const int n = (a.H + (shared ? 2 * a.Hk : 0)) * L;
   for (int i = threadIdx.x; i < n; i += 256) {
     int h = i / L;
@@ -286,11 +354,11 @@ __global__ void __launch_bounds__(256) packed_out_kernel(const SideArgs a) {
   }
 }
 
-template <int D, bool WINDOW>
+template <int D, int KIND>
 cudaError_t launch_d(const PackedGradMaps &m, const PackedGrad &p, const SideArgs &a, int *sched,
                      int *dev_status, int fault_cta, cudaStream_t stream) {
   const int heads = p.H + (a.dk_acc != nullptr ? p.Hk : 0);
-  packed_prep_kernel<D, WINDOW><<<static_cast<unsigned>(a.n_blocks * heads), 256, 0, stream>>>(a);
+  packed_prep_kernel<D, KIND><<<static_cast<unsigned>(a.n_blocks * heads), 256, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   BwdWindow pk;
@@ -300,10 +368,11 @@ cudaError_t launch_d(const PackedGradMaps &m, const PackedGrad &p, const SideArg
   pk.n_blocks = a.n_blocks;
   pk.group = p.H / p.Hk;
   pk.kv_heads = p.Hk;
-  if (WINDOW) {
+  if (KIND != kAll) {
     pk.sorted = 0;   // (an entry of length 0 does not end it: the count does)
-    pk.range = a.range, pk.count = a.count, pk.entries = a.entries, pk.split = a.split;
-    pk.window = a.window, pk.sinks = a.sinks;
+    pk.range = a.range, pk.count = reinterpret_cast<const int *>(a.count);
+    pk.entries = a.entries, pk.split = a.split;
+    pk.window = a.window, pk.sinks = a.sinks, pk.grouping = KIND == kGroups;
     auto main_kernel = D == 128 ? launch_bwd_window_main_d128 : launch_bwd_window_main_d64;
     e = main_kernel(m.q, m.k, m.v, m.dout, m.dq_acc, m.dk_acc, m.dv_acc, a.vecs, p.dk, p.dv, p.H,
                     pk, p.scale, sched, dev_status, fault_cta, stream);
@@ -322,7 +391,7 @@ cudaError_t launch_d(const PackedGradMaps &m, const PackedGrad &p, const SideArg
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, packed_out_kernel<D, WINDOW>, a);
+  return cudaLaunchKernelEx(&cfg, packed_out_kernel<D, KIND>, a);
 }
 
 }  // namespace
@@ -347,8 +416,9 @@ PackedGradLayout packed_grad_layout(int T, int S, int H, int Hk, int d, int wind
   l.vecs = l.dv_acc + shared;
   l.table = l.vecs + static_cast<size_t>(l.n_blocks) * H * 2 * BQ;
   l.range = l.table + static_cast<size_t>(l.entries) * 4;
-  l.count = l.range + (window > 0 ? static_cast<size_t>(l.entries) * 2 : 0);
-  l.bytes = sizeof(float) * (l.count + (window > 0 ? 1 : 0));
+  l.count = l.range + (window > 0 ? (static_cast<size_t>(l.entries) * 2 + 3) / 4 * 4 : 0);
+  l.stored = l.count + (window > 0 ? 4 : 0);
+  l.bytes = sizeof(float) * (l.stored + (window > 0 ? l.n_blocks : 0));
   return l;
 }
 
@@ -372,16 +442,27 @@ cudaError_t launch_bwd_packed(const PackedGradMaps &m, const PackedGrad &p, floa
   a.scale = p.scale;
   if (p.window > 0) {
     a.range = reinterpret_cast<int2 *>(ws + l.range);
-    a.count = reinterpret_cast<int *>(ws + l.count);
+    a.count = reinterpret_cast<int4 *>(ws + l.count);
+    a.stored = reinterpret_cast<int *>(ws + l.stored);
     a.entries = static_cast<int>(l.entries), a.split = l.split;
     a.window = p.window, a.sinks = p.sinks;
-    a.whole = static_cast<int>(std::min(
-        static_cast<long long>(p.T) / BQ * (reach(p.window) + 1) * p.H / 152, 1ll << 30));
-    return p.d == 128 ? launch_d<128, true>(m, p, a, sched, dev_status, fault_cta, stream)
-                      : launch_d<64, true>(m, p, a, sched, dev_status, fault_cta, stream);
+    const long long blocks = p.T / BQ, steps = reach(p.window) + 1;
+    const long long share = blocks * steps * p.H / kSms;         // an SM's, in steps
+    // An SM's share is twice an item with all heads of a group, if all tokens are one
+    // sequence's (whose last blocks have less steps): packed_prep_kernel, which knows the
+    // lengths, decides.  (From one and a half here: calls that it then left to items of one
+    // head took 3 - 5% longer in the kernel for both.)
+    const long long cut = std::min(steps, blocks), group = p.H / p.Hk;
+    const long long most = (blocks * (steps + kStart) - cut * (cut - 1) / 2) * p.H / kSms;
+    const bool groups = group > 1 && p.S <= kSortedSeqs && (p.sinks == 0 || l.split > 0) &&
+                 2 * (group * std::min(steps, blocks + 1) + kStart) <= most;
+    a.whole = static_cast<int>(std::min(groups ? std::max(steps, share / 2) : share, 1ll << 30));
+    auto launch = p.d == 128 ? (groups ? launch_d<128, kGroups> : launch_d<128, kWindow>)
+                             : (groups ? launch_d<64, kGroups> : launch_d<64, kWindow>);
+    return launch(m, p, a, sched, dev_status, fault_cta, stream);
   }
-  return p.d == 128 ? launch_d<128, false>(m, p, a, sched, dev_status, fault_cta, stream)
-                    : launch_d<64, false>(m, p, a, sched, dev_status, fault_cta, stream);
+  return p.d == 128 ? launch_d<128, kAll>(m, p, a, sched, dev_status, fault_cta, stream)
+                    : launch_d<64, kAll>(m, p, a, sched, dev_status, fault_cta, stream);
 }
 
 }  // namespace fattn

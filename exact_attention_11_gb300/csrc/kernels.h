@@ -113,13 +113,17 @@ struct BwdPacked {
   const int4 *table;
   int n_blocks, group, kv_heads, tokens, sorted;
 };
-// With a window: `count` entries (of at most `entries`) are used, each with the query
-// blocks that its item visits (first, number) in `range`.  The key blocks that begin
-// below `split` are in several items, which add dK and dV to the accumulators.
+// With a window: `count` has the entries used (of at most `entries`), each with the query
+// blocks that its items visit (first, number) in `range`, and how many of them come first
+// whose items are their query heads, and then whose items are their key/value heads, each
+// with all its query heads; the items of the rest are their query heads again.  The key
+// blocks that begin below `split` are in several items, which add dK and dV to the
+// accumulators.
 struct BwdWindow : BwdPacked {
   const int2 *range;
   const int *count;
   int entries, split, window, sinks;
+  int grouping;                 // there may be entries with all heads of a group
 };
 cudaError_t launch_bwd_packed_main_d128(const CUtensorMap &tq64, const CUtensorMap &tk,
                                         const CUtensorMap &tv, const CUtensorMap &tdo64,
@@ -259,12 +263,13 @@ cudaError_t launch_paged_shared(const CUtensorMap &tq, const CUtensorMap &tk,
 // Gradients of the packed forward (bwd_packed.cu).  Workspace, in floats from
 // its start: the dQ accumulator [H][n_blocks * 128][d], those of dK and dV
 // [Hk][..][d] (where several items add to them), [-LSE2 | -D] per head and block,
-// the block table (`entries` of 4; with a window, of 2 more, then their count).
+// the block table (`entries` of 4; with a window, of 2 more, then the three counts, and for
+// each block whether its dK and dV are stored, not added up).
 struct PackedGradLayout {
   int n_blocks, split;        // split: see BwdWindow
   long long entries;
   bool shared;                // there are dK and dV accumulators
-  size_t dk_acc, dv_acc, vecs, table, range, count, bytes;
+  size_t dk_acc, dv_acc, vecs, table, range, count, stored, bytes;
 };
 PackedGradLayout packed_grad_layout(int T, int S, int H, int Hk, int d, int window = 0,
                                     int sinks = 0);

@@ -636,8 +636,8 @@ int fa_forward_packed_window_f16(const void *q, const void *k, const void *v, vo
  * fa_backward_packed, restricted to the pairs that the mask leaves.  o and lse are what
  * fa_forward_packed_window returned for the same inputs, window and sinks; the workspace
  * has at least fa_backward_packed_window_workspace_bytes bytes.  dK and dV of the blocks
- * of 128 keys that hold first tokens are summed in fp32 with atomic adds too (all others
- * as in fa_backward_packed), up to sinks = 1024.
+ * of 128 keys that hold first tokens are summed in fp32 with atomic adds too, up to
+ * sinks = 1024 (all others as in fa_backward_packed, or in one accumulator).
  */
 unsigned long long fa_backward_packed_window_workspace_bytes(int num_seqs, int total_tokens,
                                                              int num_heads, int num_kv_heads,

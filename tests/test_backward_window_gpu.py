@@ -99,6 +99,21 @@ def test_far_queries_of_the_first_tokens(d):
     run([3900, 1100], 1, 1, d, 1200, 1000, seed=3)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens,H,Hk,window,sinks", [
+    ([2500, 700, 1, 900], 32, 8, 40, 0),
+    ([2500, 700, 129, 0, 900], 32, 8, 200, 4),
+    ([1900, 1900, 5, 1900, 1900], 28, 4, 100, 300),
+    ([64] * 30 + [3300, 900], 32, 4, 33, 130),
+    ([4000], 16, 8, 257, 1),
+    ([1111] * 9, 40, 2, 64, 16),
+])
+def test_items_with_all_heads_of_a_group(lens, H, Hk, window, sinks, d):
+    """Enough key blocks that an item takes all query heads of a key/value head and
+    stores dK and dV itself, beside others that add them up."""
+    run(lens, H, Hk, d, window, sinks, seed=len(lens))
+
+
 def test_every_length_and_many_windows():
     for d in (64, 128):
         run(list(range(1, 258, 3)), 1, 1, d, 20, 2, seed=5)
