@@ -1369,6 +1369,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // and paged from the registers (32 prompts up to 200, d = 64: 15.9 us, 17.0 through
       // shared memory).
       constexpr bool kStaged = !PAGED && D == 128;
+      // What an item's end keeps in registers moves the whole loop's: all keys, d = 128,
+      // rows are normalised one value an instruction and lse's place is reckoned from the
+      // output's (one prompt of 16384, fp16: 311 us, 318 otherwise; chunks over 16384 91.2, 92.0;
+      // the other forms lose by it: 8 prompts with a window 262.5 for 261.6).
+      constexpr bool kPlainEnd = D == 128 && FORM == kAll;
       uint8_t *stg = smem + C::kStage + (t * 4 + quarter) * 4096;
 #pragma unroll
       for (int h = 0; h < D / 64; ++h) {
@@ -1385,9 +1390,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t v[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float2 x = f2_split(fmul2(
-                f2(__uint_as_float(c16[2 * e]), __uint_as_float(c16[2 * e + 1])), f2(inv_l, inv_l)));
-            v[e] = pack2<F16>(x.x, x.y);
+            if (kPlainEnd) {
+              v[e] = pack2<F16>(__uint_as_float(c16[2 * e]) * inv_l,
+                                __uint_as_float(c16[2 * e + 1]) * inv_l);
+            } else {
+              const float2 x = f2_split(fmul2(f2(__uint_as_float(c16[2 * e]),
+                                                 __uint_as_float(c16[2 * e + 1])),
+                                              f2(inv_l, inv_l)));
+              v[e] = pack2<F16>(x.x, x.y);
+            }
           }
           // A row that sees no key is zero whatever its accumulator holds.  Packed, a
           // query sees itself at least: a sum of 0 means scores that are all -inf, NaN
@@ -1418,7 +1429,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
       if (!PAGED && a.lse != nullptr && my_out >= 0)
-        a.lse[static_cast<int64_t>(head) * a.T + row] = (m + __log2f(l)) * 0.6931471805599453f;
+        a.lse[kPlainEnd ? static_cast<int64_t>(my_out % a.H) * a.T + my_out / a.H
+                        : static_cast<int64_t>(head) * a.T + row] =
+            (m + __log2f(l)) * 0.6931471805599453f;
     }
   }
 
