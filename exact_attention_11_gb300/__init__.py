@@ -320,12 +320,18 @@ def fa_paged_prefill(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens
         q_stride, scale, workspace, workspace_bytes, stream))
 
 
+def _mask_lengths(window, sinks):
+    """A window and a number of first tokens as C ints that see the same: past 2^30, which
+    no sequence has, 2^30 (ctypes would cut them to their low 32 bits)."""
+    return max(min(window, 1 << 30), -1), max(min(sinks, 1 << 30), -1)
+
+
 def fa_forward_packed_window(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads,
                              num_kv_heads, d, q_stride, k_stride, v_stride, scale, window, sinks,
                              stream) -> int:
     return _check("fa_forward_packed_window", load().fa_forward_packed_window(
         q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads, num_kv_heads, d, q_stride,
-        k_stride, v_stride, scale, window, sinks, stream))
+        k_stride, v_stride, scale, *_mask_lengths(window, sinks), stream))
 
 
 def fa_forward_packed_window_f16(q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads,
@@ -333,13 +339,13 @@ def fa_forward_packed_window_f16(q, k, v, o, lse, cu_seqlens, num_seqs, total_to
                                  sinks, stream) -> int:
     return _check("fa_forward_packed_window_f16", load().fa_forward_packed_window_f16(
         q, k, v, o, lse, cu_seqlens, num_seqs, total_tokens, num_heads, num_kv_heads, d, q_stride,
-        k_stride, v_stride, scale, window, sinks, stream))
+        k_stride, v_stride, scale, *_mask_lengths(window, sinks), stream))
 
 
 def fa_backward_packed_window_workspace_bytes(num_seqs, total_tokens, num_heads, num_kv_heads, d,
                                               window, sinks) -> int:
     return int(load().fa_backward_packed_window_workspace_bytes(
-        num_seqs, total_tokens, num_heads, num_kv_heads, d, window, sinks))
+        num_seqs, total_tokens, num_heads, num_kv_heads, d, *_mask_lengths(window, sinks)))
 
 
 def fa_backward_packed_window(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, num_seqs,
@@ -348,14 +354,15 @@ def fa_backward_packed_window(q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, num
                               stream) -> int:
     return _check("fa_backward_packed_window", load().fa_backward_packed_window(
         q, k, v, o, dout, lse, dq, dk, dv, cu_seqlens, num_seqs, total_tokens, num_heads,
-        num_kv_heads, d, q_stride, k_stride, v_stride, scale, window, sinks, workspace,
-        workspace_bytes, stream))
+        num_kv_heads, d, q_stride, k_stride, v_stride, scale, *_mask_lengths(window, sinks),
+        workspace, workspace_bytes, stream))
 
 
 def fa_paged_prefill_window_workspace_bytes(num_seqs, total_tokens, num_heads, num_kv_heads,
                                             max_num_blocks_per_seq, window, sinks) -> int:
     return int(load().fa_paged_prefill_window_workspace_bytes(
-        num_seqs, total_tokens, num_heads, num_kv_heads, max_num_blocks_per_seq, window, sinks))
+        num_seqs, total_tokens, num_heads, num_kv_heads, max_num_blocks_per_seq,
+        *_mask_lengths(window, sinks)))
 
 
 def fa_paged_prefill_window(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out,
@@ -365,7 +372,7 @@ def fa_paged_prefill_window(q, k_cache, v_cache, block_tables, context_lens, cu_
     return _check("fa_paged_prefill_window", load().fa_paged_prefill_window(
         q, k_cache, v_cache, block_tables, context_lens, cu_seqlens, out, num_seqs, total_tokens,
         num_heads, num_kv_heads, head_size, block_size, num_blocks, max_num_blocks_per_seq,
-        q_stride, scale, window, sinks, workspace, workspace_bytes, stream))
+        q_stride, scale, *_mask_lengths(window, sinks), workspace, workspace_bytes, stream))
 
 
 def fa_paged_prefill_shared_workspace_bytes(num_seqs, total_tokens, num_groups, num_heads,
@@ -890,11 +897,10 @@ def forward_packed_window(q, k, v, cu_seqlens, window, sinks=0, scale=None, out=
 
 
 def _window_args(window, sinks):
-    """Checks a window and a number of first tokens; lengths past 2^30, which no
-    sequence has, as 2^30."""
+    """Checks a window and a number of first tokens."""
     if window < 1 or sinks < 0:
         raise ValueError("window must be at least 1 and sinks at least 0")
-    return min(int(window), 1 << 30), min(int(sinks), 1 << 30)
+    return _mask_lengths(int(window), int(sinks))
 
 
 def _forward_packed(name, q, k, v, cu_seqlens, scale, out, lse, want_lse, *mask):
