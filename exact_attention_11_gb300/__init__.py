@@ -19,6 +19,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import threading
 
@@ -321,8 +322,9 @@ def fa_paged_prefill(q, k_cache, v_cache, block_tables, context_lens, cu_seqlens
 
 
 def _mask_lengths(window, sinks):
-    """A window and a number of first tokens as C ints that see the same: past 2^30, which
-    no sequence has, 2^30 (ctypes would cut them to their low 32 bits)."""
+    """A window and a number of first tokens (whole numbers) as C ints that see the same:
+    past 2^30, which no sequence has, 2^30 (ctypes would cut them to their low 32 bits)."""
+    window, sinks = operator.index(window), operator.index(sinks)
     return max(min(window, 1 << 30), -1), max(min(sinks, 1 << 30), -1)
 
 
@@ -898,9 +900,10 @@ def forward_packed_window(q, k, v, cu_seqlens, window, sinks=0, scale=None, out=
 
 def _window_args(window, sinks):
     """Checks a window and a number of first tokens."""
+    window, sinks = _mask_lengths(window, sinks)
     if window < 1 or sinks < 0:
         raise ValueError("window must be at least 1 and sinks at least 0")
-    return _mask_lengths(int(window), int(sinks))
+    return window, sinks
 
 
 def _forward_packed(name, q, k, v, cu_seqlens, scale, out, lse, want_lse, *mask):

@@ -1,6 +1,10 @@
 """Windows and numbers of first tokens that a C int does not hold, through the Python
 calls (no GPU needed: the calls have no sequences)."""
+import math
+
+import numpy
 import pytest
+import torch
 
 import exact_attention_11_gb300 as fa
 from exact_attention_11_gb300 import _build
@@ -37,3 +41,23 @@ def test_negative_lengths_are_refused(length):
                 call(*{**a, name: length}.values(), None)
     assert fa.fa_paged_prefill_window_workspace_bytes(1, 1, 32, 8, 1024, length, 0) == 0
     assert fa.fa_backward_packed_window_workspace_bytes(4, 9000, 8, 2, 64, 100, length) == 0
+
+
+@pytest.mark.parametrize("window,sinks", [(2.5, 0), (4.0, 0), (5, 0.9), (math.inf, 0),
+                                          (math.nan, 0), ("5", 0), (5, None)])
+def test_lengths_that_are_no_whole_numbers_are_refused(window, sinks):
+    q, ints = torch.zeros(4, 1, 64, dtype=torch.bfloat16), torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: fa.forward_packed_window(q, q, q, ints, window, sinks),
+                 lambda: fa.backward_packed_window(q, q, q, q, q, q, ints, window, sinks),
+                 lambda: fa.paged_prefill_window(q, q, q, ints, ints, ints, window, sinks)):
+        with pytest.raises(TypeError):
+            call()
+    for call, a in CALLS:
+        with pytest.raises(TypeError):
+            call(*{**a, "window": window, "sinks": sinks}.values(), None)
+
+
+def test_whole_numbers_of_other_types_are_taken():
+    for one in (numpy.int64(1), numpy.int32(1), torch.tensor(1)):
+        for call, a in CALLS:
+            assert call(*{**a, "window": one, "sinks": one}.values(), None) == 0
