@@ -237,6 +237,7 @@ struct SharedArgs : Args {
   const int *cu_groups, *prefix_lens;
   int P, pre_split;             // groups; most partitions of a prefix
   int ctas;                     // CTAs that have their first item in `start`
+  int merge_heads;              // heads of a token that a warp of the merge joins; 0: by sequence
   int *head;                    // number of entries of `first` and `rec`
   int *first;                   // [entries + 1]: their first items, heaviest first
   int4 *rec;                    // [entries][2]: begin, n, kv_len, pos;
@@ -1458,7 +1459,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // dimensions a lane.  By sequence, because a grid over all rows costs 40 us where few
 // are cut; 4 us for 16 chunks of up to 6 tokens, 32 heads, of which the rows' loads
 // are the smaller part and the launch and the chain of (max, sum) the larger.
-template <int FORM>
+// SPREAD (shared prefixes, where every row of a sharing sequence is joined, and long
+// chunks): all tokens spread evenly over eight blocks an SM, a warp joining `merge_heads`
+// heads of each.  By sequence the longest chunk's rows are the call's tail there (32 chunks up
+// to 300 behind 4096 tokens: 173 us, 139 so), but with few rows it is 1 - 3 us quicker.
+constexpr int kMergeSeqs = 1024;        // sequences that a block keeps in shared memory
+template <int FORM, bool SPREAD>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a) {
   constexpr int D = kDecodeHeadSize;
   // The next kernel of the stream may be scheduled: it waits for this grid.
@@ -1469,12 +1475,12 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31;
   Seq q;
-  int cut, pre = 0;                                      // partitions; those of the prefix
-  if constexpr (FORM == kShared) {
+  int cut = 1, pre = 0;                                  // partitions; those of the prefix
+  if constexpr (FORM == kShared && !SPREAD) {
     const int4 x = a.seq[2 * blockIdx.x], y = a.seq[2 * blockIdx.x + 1];
     q = {x.x, x.y, x.z, x.w};
     cut = y.x, pre = y.y;
-  } else {
+  } else if constexpr (FORM != kShared) {
     // The call's work, as number_items adds it up, and the sequence's partitions, by one
     // warp (every block asks L2 for the same few lines).
     __shared__ Seq shared_seq;
@@ -1502,11 +1508,10 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
     q = shared_seq;
     cut = shared_cut;
   }
-  if (cut == 1 && pre == 0) return;                      // written directly
+  if (!SPREAD && cut == 1 && pre == 0) return;           // written directly
   const int64_t stride = static_cast<int64_t>(a.T) * a.H;
-  for (int x = blockIdx.y * 8 + (threadIdx.x >> 5); x < q.n * a.H; x += gridDim.y * 8) {
-    const int i = x / a.H;                               // token of the sequence
-    const int64_t row = static_cast<int64_t>(q.begin) * a.H + x;
+  // Row `row` of the output: token i of the sequence.
+  auto join = [&](int i, int64_t row) {
     // The block's last token sets the partitions' size, the row's own those it is in.
     const int block = i / (2 * a.tpb), last = min((block + 1) * 2 * a.tpb, q.n) - 1;
     const int gap =
@@ -1572,6 +1577,37 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const FormArgs<FORM> a
     w.x = pack_bf16x2(o.x * inv, o.y * inv);
     w.y = pack_bf16x2(o.z * inv, o.w * inv);
     *reinterpret_cast<uint2 *>(a.o + row * D + lane * 4) = w;
+  };
+  const int warp = threadIdx.x >> 5;
+  if constexpr (SPREAD) {
+    __shared__ int4 seqs[2 * kMergeSeqs];
+    const bool kept = a.S <= kMergeSeqs;
+    if (kept) {
+      bool any = false;
+      for (int i = threadIdx.x; i < 2 * a.S; i += 256) {
+        const int4 x = seqs[i] = a.seq[i];
+        any |= i % 2 == 1 && (x.x > 1 || x.y > 0);
+      }
+      if (!__syncthreads_or(any)) return;                // all written directly
+    }
+    const int4 *of = kept ? seqs : a.seq;
+    const uint32_t parts = (a.H + a.merge_heads - 1) / a.merge_heads;   // of a token's heads
+    const uint32_t units = a.T * parts;
+    for (uint32_t x = blockIdx.x * 8 + warp; x < units; x += gridDim.x * 8) {
+      const int tok = x / parts, h0 = x % parts * a.merge_heads;
+      // The last sequence that begins at or before the token owns it, if any does.
+      const int s = warp_search(a.S, tok, [&](int j) { return of[2 * j].x; });
+      if (s < 0) continue;
+      const int4 u = of[2 * s], v = of[2 * s + 1];
+      q = {u.x, u.y, u.z, u.w};
+      cut = v.x, pre = v.y;
+      if (tok - q.begin >= q.n || (cut == 1 && pre == 0)) continue;
+      for (int h = h0; h < min(h0 + a.merge_heads, a.H); ++h)
+        join(tok - q.begin, static_cast<int64_t>(tok) * a.H + h);
+    }
+  } else {
+    for (int x = blockIdx.y * 8 + warp; x < q.n * a.H; x += gridDim.y * 8)
+      join(x / a.H, static_cast<int64_t>(q.begin) * a.H + x);
   }
 }
 
@@ -1687,11 +1723,17 @@ cudaError_t launch(const CUtensorMap &tq, const KvMap<PAGED, FORM> &tk,
   e = cudaLaunchKernelEx(&cfg, fwd_packed_kernel<D, F16, PAGED, FORM>, tq, tk, tv, a);
   if (e != cudaSuccess || !PAGED || (!is_shared(FORM) && a.n_split == 1)) return e;
   // Eight blocks an SM in all, spread over the sequences (at most kCachedSeqs; with
-  // shared prefixes any number).
+  // shared prefixes any number) or the tokens.
   cfg.gridDim = dim3(static_cast<unsigned>(a.S), static_cast<unsigned>(std::max(8 * sms / a.S, 1)));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_merge_kernel<FORM == kSharedFew ? kShared : FORM>, a);
+  if constexpr (is_shared(FORM)) {
+    if (a.merge_heads == 0) return cudaLaunchKernelEx(&cfg, paged_merge_kernel<kShared, false>, a);
+    cfg.gridDim = dim3(static_cast<unsigned>(8 * sms));
+    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<kShared, true>, a);
+  } else {
+    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<FORM, false>, a);
+  }
 }
 
 template <int FORM>
@@ -1837,6 +1879,12 @@ cudaError_t launch_paged_shared(const CUtensorMap &tq, const CUtensorMap &tk,
   cudaError_t e = sm_count(&a.ctas);
   if (e != cudaSuccess) return e;
   a.ctas = std::min(a.ctas, kSharedMaxCtas);
+  // The merge spreads the tokens over its 64 warps an SM where they have two rows each and the
+  // sequences eight tokens on average (with fewer, the longest is no tail).
+  const int64_t rows = static_cast<int64_t>(p.T) * p.H, warps = 64 * a.ctas;
+  a.merge_heads = rows >= 2 * warps && p.T / 8 >= p.S
+                      ? static_cast<int>(std::clamp<int64_t>(rows / warps, 1, p.H))
+                      : 0;
   if (p.S + P <= kCachedSeqs) return launch<128, false, true, kSharedFew>(tq, tk, tv, a, stream);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(1);
