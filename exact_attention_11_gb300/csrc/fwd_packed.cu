@@ -64,13 +64,15 @@
 // tokens over long contexts the 16 copies of a paged key tile and HBM; for short
 // prompts the start (5 us) and the chain of an SM's few items.  Measured: 8 prompts up
 // to 4096 tokens, 32 / 8 heads, d = 128, causal, 182 us (1497 TFLOP/s); one of 16384,
-// 8 / 1 heads, fp16, 330 us (1665); 32 prompts up to 200, 16 heads, d = 64, 16 us;
+// 8 / 1 heads, fp16, 311 - 328 us (1768 - 1676); 32 prompts up to 200, 16 heads, d = 64, 16 us;
 // chunks of 4 x 1024 tokens over 8192, 345 us (1494 TFLOP/s), up to 1024 over up to
-// 16384, 93 us; 64 single tokens over 4096, 180 us (6.0 TB/s).  Windows: 8 prompts up to
+// 16384, 91 us; 64 single tokens over 4096, 180 us (6.0 TB/s).  Windows: 8 prompts up to
 // 8192, 32 / 8 heads, d = 128, window 1024: 260 us (1230 TFLOP/s; a block's nine key tiles
 // take 1.5 us each, its start and end 3); one of 16384, 8 / 1 heads, fp16, window 4000,
-// 150 us (1605); 64 single tokens, window 4096, 182 us (5.9 TB/s); chunks up to 2048 over
-// up to 32768, window 4096, 171 us (1430 TFLOP/s).  Shared prefixes, single tokens, 32 / 8
+// 150 - 154 us (1605 - 1575); 64 single tokens, window 4096, 182 us (5.9 TB/s); chunks up to
+// 2048 over up to 32768, window 4096, 171 us (1430 TFLOP/s).  These are times of a replayed
+// call on the same tensors; with other tensors from call to call, whose lines are not in L2,
+// the prompts take 274 - 277, the one of 16384 165 - 166 and the chunks 181 us.  Shared prefixes, single tokens, 32 / 8
 // heads: 64 sequences behind 8192 tokens, up to 512 of their own, 38 us (2.6 TB/s: start,
 // the chains of an SM's four or five short items, merge; 314 without sharing); 256 behind
 // 32768, up to 2048 of their own, 280 us (4.3 TB/s; first the prefix, bound by the tensor
@@ -329,7 +331,9 @@ __device__ __forceinline__ Work work_of(const FormArgs<FORM> &a, const Seq &q) {
 // number.)  kWindow: the few rows of a sequence of one block cost little to cut, and its
 // items come last, so where such sequences are less than an eighth of the work they take
 // eight times theirs for the call's (chunks of 6, 1536, 3 and 2048 over up to 32768, window
-// 4096: 171 us, 179 without; always their own work: 178 for 170 on 31 chunks up to 289).
+// 4096: 171 us, 179 without; always their own work: 178 for 170 on 31 chunks up to 289; over
+// three times 40 mixes of all kinds four or sixteen times theirs, or the call's, were within
+// 0.3% of each other: it matters for such few rows only).
 constexpr float kPartFixed = 2.5f, kPartRow = 0.02f;
 __device__ __forceinline__ int parts_of(const Args &a, const Seq &q, int tiles, int64_t work,
                                         int most) {
@@ -730,7 +734,7 @@ struct Planner {
 
 // The numbered entries of a call with few sequences, in shared memory in place of
 // Misc's: every CTA finds the same ones for itself (64 requests behind 8192 tokens:
-// 39.9 us, 44.8 with a kernel ahead that numbers them).
+// 39.9 us, 44.8 with a kernel ahead that numbers them; both before the merge loaded rows ahead).
 struct PlanTable {
   int entries, items;
   int begins[kCachedSeqs + 1];  // first rows of the sequences
@@ -1833,7 +1837,7 @@ cudaError_t launch_paged_prefill(const CUtensorMap &tq, const CUtensorMap &tk,
 }
 
 // Workspace of a call with shared prefixes: partial rows (at least one of a row's own
-// context and one of its prefix, up to 256 MB in all), then the plan.
+// context and one of its prefix, more as far as 256 MB reach), then the plan.
 SharedLayout shared_layout(int T, int S, int P, int H, int Hk, int max_blocks) {
   SharedLayout l{};
   const double tiles = (max_blocks + kTileBlocks - 1) / kTileBlocks;
