@@ -706,8 +706,9 @@ int fa_paged_prefill_window(const void *q, const void *k_cache, const void *v_ca
  * save less than it costs: that is found on the device, so that a captured call serves
  * changing lengths.  (Where nothing is worth sharing fa_paged_prefill is the better call:
  * 3 us less as a rule in short calls; in long ones the two are within a few per cent.)
- * Contexts and prefixes are cut into partitions for any number of sequences.  Results are the same from call to
- * call, bit for bit.  Every other argument and error as for fa_paged_prefill.
+ * Contexts and prefixes are cut into partitions for any number of sequences.  Results are
+ * the same from call to call, bit for bit.  Every other argument and error as for
+ * fa_paged_prefill.
  */
 unsigned long long fa_paged_prefill_shared_workspace_bytes(int num_seqs, int total_tokens,
                                                            int num_groups, int num_heads,
